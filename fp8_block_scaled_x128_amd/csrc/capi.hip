@@ -518,9 +518,11 @@ fp8bs_status fp8_silu_mul_quant(const uint16_t* gate_up, int64_t rows, int64_t I
                     "fp8_silu_mul_quant");
 }
 
-fp8bs_status fp8_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y, const int32_t* token_rows,
-                             const float* weights, int64_t T, int32_t k, void* out, int64_t ld_out, fp8bs_out out_type,
-                             hipStream_t stream) {
+// routed: slots without a row are skipped instead of clamped, and there may be
+// no row at all.
+static fp8bs_status combine(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y, const int32_t* token_rows,
+                            const float* weights, int64_t T, int32_t k, void* out, int64_t ld_out, fp8bs_out out_type,
+                            bool routed, const char* what, hipStream_t stream) {
     if (out_type != FP8BS_OUT_BF16 && out_type != FP8BS_OUT_FP32) return fail(FP8BS_ERR_UNSUPPORTED, "out %d", out_type);
     if (rows < 0 || H < 0 || T < 0 || k < 1) return fail(FP8BS_ERR_SHAPE, "rows, H, T >= 0 and k >= 1 required");
     if (H % 8) return fail(FP8BS_ERR_SHAPE, "H %% 8 != 0 (H=%lld)", (long long)H);
@@ -528,8 +530,8 @@ fp8bs_status fp8_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t
     if (rows > INT32_MAX || H > INT32_MAX / 2 || T > INT32_MAX / 2 || T * (H / 8) > (1ll << 31))
         return fail(FP8BS_ERR_SHAPE, "tensor too large");
     if (T == 0 || H == 0) return ok();
-    if (rows == 0) return fail(FP8BS_ERR_SHAPE, "rows == 0 with T > 0");
-    if (!y || !token_rows || !weights || !out) return fail(FP8BS_ERR_NULL, "y, token_rows, weights and out are required");
+    if (rows == 0 && !routed) return fail(FP8BS_ERR_SHAPE, "rows == 0 with T > 0");
+    if ((rows > 0 && !y) || !token_rows || !weights || !out) return fail(FP8BS_ERR_NULL, "y, token_rows, weights and out are required");
     if (ld_y < H || ld_out < H) return fail(FP8BS_ERR_STRIDE, "ld_y and ld_out must be >= H");
     if (ld_y % 8 || !aligned(y, 16)) return fail(FP8BS_ERR_ALIGN, "y must be 16-byte aligned with ld_y %% 8 == 0");
     if (ld_out % 8 || !aligned(out, 16)) return fail(FP8BS_ERR_ALIGN, "out must be 16-byte aligned with ld_out %% 8 == 0");
@@ -537,8 +539,230 @@ fp8bs_status fp8_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t
     fp8bs_status d = check_device();
     if (d != FP8BS_OK) return d;
     return launched(launch_moe_combine(y, rows, H, ld_y, token_rows, weights, T, k, out, ld_out,
-                                       out_type == FP8BS_OUT_FP32, stream),
-                    "fp8_moe_combine");
+                                       out_type == FP8BS_OUT_FP32, routed, stream),
+                    what);
+}
+
+fp8bs_status fp8_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y, const int32_t* token_rows,
+                             const float* weights, int64_t T, int32_t k, void* out, int64_t ld_out, fp8bs_out out_type,
+                             hipStream_t stream) {
+    return combine(y, rows, H, ld_y, token_rows, weights, T, k, out, ld_out, out_type, false, "fp8_moe_combine", stream);
+}
+
+fp8bs_status fp8_moe_combine_routed(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y,
+                                    const int32_t* token_rows, const float* weights, int64_t T, int32_t k, void* out,
+                                    int64_t ld_out, fp8bs_out out_type, hipStream_t stream) {
+    return combine(y, rows, H, ld_y, token_rows, weights, T, k, out, ld_out, out_type, true, "fp8_moe_combine_routed",
+                   stream);
+}
+
+static bool type_ok(fp8bs_out t) { return t == FP8BS_OUT_BF16 || t == FP8BS_OUT_FP32; }
+
+fp8bs_status fp8_moe_combine_backward(const void* dout, int64_t ld_dout, fp8bs_out dout_type, const uint16_t* y,
+                                      int64_t rows, int64_t H, int64_t ld_y, const int32_t* token_rows,
+                                      const float* weights, int64_t T, int32_t k, uint16_t* dy, int64_t ld_dy,
+                                      float* dweights, hipStream_t stream) {
+    if (!type_ok(dout_type)) return fail(FP8BS_ERR_UNSUPPORTED, "dout_type %d", (int)dout_type);
+    if (rows < 0 || H < 0 || T < 0 || k < 1) return fail(FP8BS_ERR_SHAPE, "rows, H, T >= 0 and k >= 1 required");
+    if (H % 8) return fail(FP8BS_ERR_SHAPE, "H %% 8 != 0 (H=%lld)", (long long)H);
+    if (rows > INT32_MAX || H > INT32_MAX / 2 || T >= (1ll << 26)) return fail(FP8BS_ERR_SHAPE, "tensor too large");
+    if (T == 0) return ok();
+    if (!dy && !dweights) return fail(FP8BS_ERR_NULL, "dy or dweights is required");
+    if (!token_rows || !weights) return fail(FP8BS_ERR_NULL, "token_rows and weights are required");
+    if (H > 0 && (!dout || (dweights && rows > 0 && !y))) return fail(FP8BS_ERR_NULL, "dout, and y for dweights, are required");
+    if (ld_dout < H || (dweights && rows > 0 && ld_y < H) || (dy && ld_dy < H))
+        return fail(FP8BS_ERR_STRIDE, "ld_dout, ld_y and ld_dy must be >= H");
+    if (ld_dout % 8 || !aligned(dout, 16)) return fail(FP8BS_ERR_ALIGN, "dout must be 16-byte aligned with ld_dout %% 8 == 0");
+    if (dweights && (ld_y % 8 || !aligned(y, 16))) return fail(FP8BS_ERR_ALIGN, "y must be 16-byte aligned with ld_y %% 8 == 0");
+    if (dy && (ld_dy % 8 || !aligned(dy, 16))) return fail(FP8BS_ERR_ALIGN, "dy must be 16-byte aligned with ld_dy %% 8 == 0");
+    if (!aligned(token_rows, 4) || !aligned(weights, 4) || !aligned(dweights, 4))
+        return fail(FP8BS_ERR_ALIGN, "token_rows, weights, dweights misaligned");
+    fp8bs_status d = check_device();
+    if (d != FP8BS_OK) return d;
+    return launched(launch_moe_combine_bwd(dout, ld_dout, dout_type == FP8BS_OUT_FP32, y, rows, H, ld_y, token_rows,
+                                           weights, T, k, dy, ld_dy, dweights, stream),
+                    "fp8_moe_combine_backward");
+}
+
+// Sizes and types both router entry points accept.
+static fp8bs_status route_shape(int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k, int32_t renorm) {
+    if (!type_ok(type)) return fail(FP8BS_ERR_UNSUPPORTED, "type %d", (int)type);
+    if (renorm != 0 && renorm != 1) return fail(FP8BS_ERR_UNSUPPORTED, "renorm %d", (int)renorm);
+    if (T < 0 || T > (1ll << 26)) return fail(FP8BS_ERR_SHAPE, "T=%lld outside [0, 2^26]", (long long)T);
+    if (E < 1 || E > 1024) return fail(FP8BS_ERR_SHAPE, "E=%d outside [1, 1024]", (int)E);
+    if (k < 1 || k > E || k > 32) return fail(FP8BS_ERR_SHAPE, "k=%d outside [1, min(E, 32)]", (int)k);
+    if (T * k > INT32_MAX) return fail(FP8BS_ERR_SHAPE, "T * k >= 2^31");
+    if (ld < E) return fail(FP8BS_ERR_STRIDE, "ld < E");
+    return FP8BS_OK;
+}
+
+fp8bs_status fp8_moe_route_ws_size(int64_t T, int32_t E, size_t* bytes) {
+    if (T < 0 || T > (1ll << 26)) return fail(FP8BS_ERR_SHAPE, "T=%lld outside [0, 2^26]", (long long)T);
+    if (E < 1 || E > 1024) return fail(FP8BS_ERR_SHAPE, "E=%d outside [1, 1024]", (int)E);
+    if (!bytes) return fail(FP8BS_ERR_NULL, "bytes is required");
+    *bytes = route_ws_bytes(T, E);
+    return ok();
+}
+
+fp8bs_status fp8_moe_route(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k,
+                           int32_t renorm, const uint8_t* mask, int32_t* experts, float* weights, int32_t* counts,
+                           int32_t* offsets, int32_t* row_token, int32_t* token_rows, float* lse, float* loss,
+                           void* ws, size_t ws_bytes, hipStream_t stream) {
+    fp8bs_status v = route_shape(T, E, ld, type, k, renorm);
+    if (v != FP8BS_OK) return v;
+    if (!counts || !offsets || !loss) return fail(FP8BS_ERR_NULL, "counts, offsets and loss are required");
+    if (T > 0 && (!logits || !experts || !weights || !row_token || !token_rows || !lse))
+        return fail(FP8BS_ERR_NULL, "logits, experts, weights, row_token, token_rows and lse are required");
+    const size_t need = route_ws_bytes(T, E);
+    if (need > 0 && !ws) return fail(FP8BS_ERR_NULL, "a workspace of %zu bytes is required", need);
+    if (ws_bytes < need) return fail(FP8BS_ERR_SHAPE, "ws_bytes %zu < %zu", ws_bytes, need);
+    if (!aligned(logits, type == FP8BS_OUT_FP32 ? 4 : 2) || !aligned(experts, 4) || !aligned(weights, 4) ||
+        !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(token_rows, 4) ||
+        !aligned(lse, 4) || !aligned(loss, 4) || !aligned(ws, 16))
+        return fail(FP8BS_ERR_ALIGN, "a pointer is not aligned to its element (ws: 16 bytes)");
+    fp8bs_status d = check_device();
+    if (d != FP8BS_OK) return d;
+    RouteArgs p{logits, T, E, ld, type == FP8BS_OUT_FP32, k, renorm != 0, mask, experts, weights,
+                counts, offsets, row_token, token_rows, lse, loss};
+    return launched(launch_moe_route(p, ws, stream), "fp8_moe_route");
+}
+
+fp8bs_status fp8_moe_route_backward(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k,
+                                    int32_t renorm, const int32_t* experts, const float* weights,
+                                    const int32_t* counts, const float* lse, const float* dweights,
+                                    const float* dloss, void* dlogits, int64_t ld_d, hipStream_t stream) {
+    fp8bs_status v = route_shape(T, E, ld, type, k, renorm);
+    if (v != FP8BS_OK) return v;
+    if (T == 0) return ok();
+    if (!dweights && !dloss) return fail(FP8BS_ERR_NULL, "dweights or dloss is required");
+    if (!logits || !lse || !dlogits) return fail(FP8BS_ERR_NULL, "logits, lse and dlogits are required");
+    if (dweights && (!experts || !weights)) return fail(FP8BS_ERR_NULL, "experts and weights are required with dweights");
+    if (dloss && !counts) return fail(FP8BS_ERR_NULL, "counts are required with dloss");
+    if (ld_d < E) return fail(FP8BS_ERR_STRIDE, "ld_d < E");
+    const uintptr_t a = type == FP8BS_OUT_FP32 ? 4 : 2;
+    if (!aligned(logits, a) || !aligned(dlogits, a) || !aligned(experts, 4) || !aligned(weights, 4) ||
+        !aligned(counts, 4) || !aligned(lse, 4) || !aligned(dweights, 4) || !aligned(dloss, 4))
+        return fail(FP8BS_ERR_ALIGN, "a pointer is not aligned to its element");
+    fp8bs_status d = check_device();
+    if (d != FP8BS_OK) return d;
+    RouteBwdArgs p{logits, T, E, ld, type == FP8BS_OUT_FP32, k, renorm != 0, experts, weights, counts, lse,
+                   dweights, dloss, dlogits, ld_d};
+    return launched(launch_moe_route_bwd(p, stream), "fp8_moe_route_backward");
+}
+
+// One matrix argument of the norms: nullable; leading dimension and alignment.
+static fp8bs_status norm_matrix(const char* name, const void* p, int64_t cols, int64_t ld, uintptr_t align) {
+    if (!p) return FP8BS_OK;
+    if (ld < cols) return fail(FP8BS_ERR_STRIDE, "%s: leading dimension < cols", name);
+    if (ld % 8 || !aligned(p, align))
+        return fail(FP8BS_ERR_ALIGN, "%s must be %d-byte aligned with its leading dimension %% 8 == 0", name, (int)align);
+    return FP8BS_OK;
+}
+
+// What both norm entry points check of sizes, types and the branch.
+static fp8bs_status norm_common(int64_t rows, int64_t cols, fp8bs_out stream_type, fp8bs_out w_type, float scale,
+                                float eps) {
+    if (!type_ok(stream_type) || !type_ok(w_type)) return fail(FP8BS_ERR_UNSUPPORTED, "stream_type or w_type");
+    if (rows < 0 || cols < 0 || rows > INT32_MAX) return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
+    if (cols % 8 || cols > 32768) return fail(FP8BS_ERR_SHAPE, "cols %% 8 != 0 or cols > 32768 (cols=%lld)", (long long)cols);
+    // comparisons that a NaN fails
+    if (!(eps > 0.0f && eps <= 3.0e38f)) return fail(FP8BS_ERR_UNSUPPORTED, "eps must be positive and finite");
+    if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(FP8BS_ERR_UNSUPPORTED, "scale must be finite");
+    return FP8BS_OK;
+}
+
+fp8bs_status fp8_block_norm(int64_t rows, int64_t cols, const uint16_t* x, int64_t ld_x, const void* residual,
+                            int64_t ld_r, fp8bs_out stream_type, const uint16_t* gate, int64_t ld_gate,
+                            int64_t rows_per_gate, float scale, const void* w_post, const void* w_pre,
+                            fp8bs_out w_type, float eps, void* h, int64_t ld_h, uint16_t* y, int64_t ld_y, uint8_t* q,
+                            int64_t ld_q, float* s, int64_t s_stride_row, int64_t s_stride_group, hipStream_t stream) {
+    fp8bs_status v = norm_common(rows, cols, stream_type, w_type, scale, eps);
+    if (v != FP8BS_OK) return v;
+    if (gate && rows_per_gate < 1) return fail(FP8BS_ERR_SHAPE, "rows_per_gate must be >= 1");
+    if (rows == 0 || cols == 0) return ok();
+    if (!residual && !x) return fail(FP8BS_ERR_NULL, "residual or x is required");
+    if (!x && (w_post || gate)) return fail(FP8BS_ERR_NULL, "w_post and gate need x");
+    if ((q != nullptr) != (s != nullptr)) return fail(FP8BS_ERR_NULL, "q and s go together");
+    if ((y || q) && !w_pre) return fail(FP8BS_ERR_NULL, "y and q need w_pre");
+    if (w_pre && !y && !q) return fail(FP8BS_ERR_NULL, "w_pre without y or q");
+    if (!h && !y && !q) return fail(FP8BS_ERR_NULL, "no output");
+    if ((v = norm_matrix("x", x, cols, ld_x, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("residual", residual, cols, ld_r, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("gate", gate, cols, ld_gate, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("h", h, cols, ld_h, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("y", y, cols, ld_y, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("q", q, cols, ld_q, 8)) != FP8BS_OK) return v;
+    if (!aligned(w_post, 16) || !aligned(w_pre, 16) || !aligned(s, 4))
+        return fail(FP8BS_ERR_ALIGN, "w_post and w_pre must be 16-byte aligned, s 4-byte");
+    fp8bs_status d = check_device();
+    if (d != FP8BS_OK) return d;
+    NormArgs p{};
+    p.rows = rows; p.cols = (int32_t)cols; p.x = x; p.ld_x = ld_x; p.residual = residual; p.ld_r = ld_r;
+    p.res32 = stream_type == FP8BS_OUT_FP32;
+    p.gate = gate; p.ld_gate = ld_gate; p.rows_per_gate = gate ? (rows_per_gate < rows ? rows_per_gate : rows) : 1;
+    p.scale = scale; p.w_post = w_post; p.w_pre = w_pre; p.w32 = w_type == FP8BS_OUT_FP32; p.eps = eps;
+    p.h = h; p.ld_h = ld_h; p.y = y; p.ld_y = ld_y; p.q = q; p.ld_q = ld_q;
+    p.s = s; p.ssr = s_stride_row; p.ssg = s_stride_group;
+    return launched(launch_block_norm(p, stream), "fp8_block_norm");
+}
+
+fp8bs_status fp8_block_norm_backward_ws_size(int64_t rows, int64_t cols, int64_t rows_per_gate, int32_t dw_post,
+                                             int32_t dw_pre, int32_t dgate, size_t* bytes) {
+    fp8bs_status v = norm_common(rows, cols, FP8BS_OUT_BF16, FP8BS_OUT_BF16, 1.0f, 1.0f);
+    if (v != FP8BS_OK) return v;
+    if (dgate && rows_per_gate < 1) return fail(FP8BS_ERR_SHAPE, "rows_per_gate must be >= 1");
+    if (!bytes) return fail(FP8BS_ERR_NULL, "bytes is required");
+    const int64_t R = rows_per_gate < rows ? rows_per_gate : (rows > 0 ? rows : 1);
+    *bytes = plan_block_norm_bwd(rows, cols, R, dw_pre != 0, dw_post != 0, dgate != 0).ws_floats * 4;
+    return ok();
+}
+
+fp8bs_status fp8_block_norm_backward(int64_t rows, int64_t cols, const void* dy, int64_t ld_dy, fp8bs_out dy_type,
+                                     const void* dh, int64_t ld_dh, const void* h, int64_t ld_h,
+                                     fp8bs_out stream_type, const uint16_t* x, int64_t ld_x, const uint16_t* gate,
+                                     int64_t ld_gate, int64_t rows_per_gate, float scale, const void* w_post,
+                                     const void* w_pre, fp8bs_out w_type, float eps, uint16_t* dx, int64_t ld_dx,
+                                     void* dres, int64_t ld_dres, void* dgate, int64_t ld_dgate, fp8bs_out dgate_type,
+                                     float* dw_post, float* dw_pre, void* ws, size_t ws_bytes, hipStream_t stream) {
+    fp8bs_status v = norm_common(rows, cols, stream_type, w_type, scale, eps);
+    if (v != FP8BS_OK) return v;
+    if (!type_ok(dy_type) || !type_ok(dgate_type)) return fail(FP8BS_ERR_UNSUPPORTED, "dy_type or dgate_type");
+    if (gate && rows_per_gate < 1) return fail(FP8BS_ERR_SHAPE, "rows_per_gate must be >= 1");
+    if (cols == 0) return ok();
+    if (!dx && !dres && !dgate && !dw_post && !dw_pre) return fail(FP8BS_ERR_NULL, "no output");
+    if ((dgate && !gate) || (dw_post && !w_post) || (dw_pre && !w_pre))
+        return fail(FP8BS_ERR_NULL, "dgate, dw_post and dw_pre need gate, w_post and w_pre");
+    if (rows > 0) {
+        if ((w_pre != nullptr) != (dy != nullptr) || (w_pre != nullptr) != (h != nullptr))
+            return fail(FP8BS_ERR_NULL, "dy, h and w_pre go together");
+        if (!dy && !dh) return fail(FP8BS_ERR_NULL, "dy or dh is required");
+        if (!x && (w_post || gate || dx)) return fail(FP8BS_ERR_NULL, "w_post, gate and dx need x");
+    }
+    if ((v = norm_matrix("dy", dy, cols, ld_dy, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("dh", dh, cols, ld_dh, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("h", h, cols, ld_h, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("x", x, cols, ld_x, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("gate", gate, cols, ld_gate, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("dx", dx, cols, ld_dx, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("dres", dres, cols, ld_dres, 16)) != FP8BS_OK) return v;
+    if ((v = norm_matrix("dgate", dgate, cols, ld_dgate, 16)) != FP8BS_OK) return v;
+    if (!aligned(w_post, 16) || !aligned(w_pre, 16) || !aligned(dw_post, 16) || !aligned(dw_pre, 16) || !aligned(ws, 16))
+        return fail(FP8BS_ERR_ALIGN, "w_post, w_pre, dw_post, dw_pre and ws must be 16-byte aligned");
+    const int64_t R = gate ? (rows_per_gate < rows ? rows_per_gate : (rows > 0 ? rows : 1)) : 1;
+    const size_t need = plan_block_norm_bwd(rows, cols, R, dw_pre, dw_post, dgate).ws_floats * 4;
+    if (need > 0 && !ws) return fail(FP8BS_ERR_NULL, "a workspace of %zu bytes is required", need);
+    if (ws_bytes < need) return fail(FP8BS_ERR_SHAPE, "ws_bytes %zu < %zu", ws_bytes, need);
+    fp8bs_status d = check_device();
+    if (d != FP8BS_OK) return d;
+    NormBwdArgs p{};
+    p.rows = rows; p.cols = (int32_t)cols; p.dy = dy; p.ld_dy = ld_dy; p.dy32 = dy_type == FP8BS_OUT_FP32;
+    p.dh = dh; p.ld_dh = ld_dh; p.h = h; p.ld_h = ld_h; p.res32 = stream_type == FP8BS_OUT_FP32;
+    p.x = x; p.ld_x = ld_x; p.gate = gate; p.ld_gate = ld_gate; p.rows_per_gate = R; p.scale = scale;
+    p.w_post = w_post; p.w_pre = w_pre; p.w32 = w_type == FP8BS_OUT_FP32; p.eps = eps;
+    p.dx = dx; p.ld_dx = ld_dx; p.dres = dres; p.ld_dres = ld_dres;
+    p.dgate = dgate; p.ld_dgate = ld_dgate; p.dgate32 = dgate_type == FP8BS_OUT_FP32;
+    p.dw_post = dw_post; p.dw_pre = dw_pre;
+    return launched(launch_block_norm_bwd(p, static_cast<float*>(ws), stream), "fp8_block_norm_backward");
 }
 
 fp8bs_status mxfp8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, uint8_t* q, int64_t ld_q,

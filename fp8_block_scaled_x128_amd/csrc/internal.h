@@ -49,7 +49,76 @@ hipError_t launch_e4m3_encode(const float* in, uint8_t* out, int64_t n, hipStrea
 // moe.hip
 hipError_t launch_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y, const int32_t* pos,
                               const float* w, int64_t T, int32_t k, void* out, int64_t ld_out, int out_f32,
-                              hipStream_t st);
+                              bool skip, hipStream_t st);
+// Gradient of the combine: dy (nullable) and dw (nullable); slots without a
+// row give dw 0 and no dy.
+hipError_t launch_moe_combine_bwd(const void* dout, int64_t ld_do, int do_f32, const uint16_t* y, int64_t rows,
+                                  int64_t H, int64_t ld_y, const int32_t* pos, const float* w, int64_t T, int32_t k,
+                                  uint16_t* dy, int64_t ld_dy, float* dw, hipStream_t st);
+
+// norm.hip.  Null pointers switch parts off (capi.hip checks which may be).
+struct NormArgs {
+    int64_t rows; int32_t cols;
+    const uint16_t* x; int64_t ld_x;
+    const void* residual; int64_t ld_r; bool res32;       // residual and h
+    const uint16_t* gate; int64_t ld_gate; int64_t rows_per_gate;
+    float scale;
+    const void* w_post; const void* w_pre; bool w32;
+    float eps;
+    void* h; int64_t ld_h;
+    uint16_t* y; int64_t ld_y;
+    uint8_t* q; int64_t ld_q; float* s; int64_t ssr, ssg;
+};
+hipError_t launch_block_norm(const NormArgs& p, hipStream_t st);
+
+struct NormBwdArgs {
+    int64_t rows; int32_t cols;
+    const void* dy; int64_t ld_dy; bool dy32;
+    const void* dh; int64_t ld_dh; const void* h; int64_t ld_h; bool res32;     // dh, h and dres
+    const uint16_t* x; int64_t ld_x;
+    const uint16_t* gate; int64_t ld_gate; int64_t rows_per_gate;
+    float scale;
+    const void* w_post; const void* w_pre; bool w32;
+    float eps;
+    uint16_t* dx; int64_t ld_dx;
+    void* dres; int64_t ld_dres;
+    void* dgate; int64_t ld_dgate; bool dgate32;
+    float* dw_post; float* dw_pre;
+};
+// How the rows are dealt: units of `chunk` rows, `splits` of them per gate row
+// (or over all rows), walked by `slots` workgroups or waves; the column sums'
+// partials lie at the three offsets (in floats) of the workspace.
+struct NormBwdPlan {
+    int wpr, nv;
+    int32_t slots;
+    int64_t units, splits, chunk, unit_rows, groups;
+    size_t off_pre, off_post, off_gate, ws_floats;
+    float *ws_pre, *ws_post, *ws_gate;
+};
+NormBwdPlan plan_block_norm_bwd(int64_t rows, int64_t cols, int64_t rows_per_gate, bool dw_pre, bool dw_post,
+                                bool dgate);
+hipError_t launch_block_norm_bwd(const NormBwdArgs& p, float* ws, hipStream_t st);
+
+// route.hip
+struct RouteArgs {
+    const void* logits; int64_t T; int32_t E; int64_t ld; bool logits32;
+    int32_t k; bool renorm;
+    const uint8_t* mask;
+    int32_t* experts; float* weights; int32_t* counts; int32_t* offsets; int32_t* row_token; int32_t* token_rows;
+    float* lse; float* loss;
+};
+struct RouteWs { int32_t* hist; float* psum; float* lse2; int32_t* live; float* total; };
+size_t route_ws_bytes(int64_t T, int32_t E);
+hipError_t launch_moe_route(const RouteArgs& p, void* ws, hipStream_t st);
+
+struct RouteBwdArgs {
+    const void* logits; int64_t T; int32_t E; int64_t ld; bool logits32;      // dlogits has the same type
+    int32_t k; bool renorm;
+    const int32_t* experts; const float* weights; const int32_t* counts; const float* lse;
+    const float* dweights; const float* dloss;
+    void* dlogits; int64_t ld_d;
+};
+hipError_t launch_moe_route_bwd(const RouteBwdArgs& p, hipStream_t st);
 
 // gemm.hip
 struct GemmArgs {

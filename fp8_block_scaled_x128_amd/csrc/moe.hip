@@ -11,13 +11,16 @@
 // (deterministic: no atomics, no order that depends on scheduling).
 #include "device_common.h"
 #include "internal.h"
+#include "reduce.h"
 
 namespace fp8bs {
 namespace {
 
 constexpr int kThreads = 256;
 
-template <bool OUTF32>
+// SKIP: a slot whose position is outside [0, rows) contributes nothing (the
+// router leaves -1 there); otherwise positions are clamped.
+template <bool OUTF32, bool SKIP>
 __global__ void __launch_bounds__(kThreads) k_moe_combine(const uint16_t* __restrict__ y, int32_t rows, int32_t nch,
                                                           int64_t ld_y, const int32_t* __restrict__ pos,
                                                           const float* __restrict__ w, int64_t T, int32_t k,
@@ -37,9 +40,15 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine(const uint16_t* __rest
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
             if (j0 + u < k) {
+                const int pj = pt[j0 + u];
+                if (SKIP && (uint32_t)pj >= (uint32_t)rows) {
+                    raw[u] = make_uint4(0, 0, 0, 0);
+                    wj[u] = 0.0f;
+                    continue;
+                }
                 // positions outside [0, rows) are clamped: a bad map reads
                 // wrong rows, never outside y
-                const int r = min(max(pt[j0 + u], 0), rows - 1);
+                const int r = SKIP ? pj : min(max(pj, 0), rows - 1);
                 raw[u] = load_nt16(y + (int64_t)r * ld_y + 8 * c);
                 wj[u] = wt[j0 + u];
             }
@@ -67,20 +76,94 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine(const uint16_t* __rest
     }
 }
 
+// Gradient of the combine: dy[row] = w dout[t] and dw = <dout[t], y[row]> for
+// every (token, slot) with a row.  One wave holds a token and walks the
+// columns in runs of 512 (8 per lane): per run, dout is loaded once and up to
+// eight y rows are in flight, each giving its part of a dot product and
+// taking its dy row at once, so nothing of a row stays in registers.
+template <bool DO32>
+__global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const void* __restrict__ dout, int64_t ld_do,
+                                                              const uint16_t* __restrict__ y, int32_t rows,
+                                                              int32_t nch, int64_t ld_y,
+                                                              const int32_t* __restrict__ pos,
+                                                              const float* __restrict__ w, int64_t T, int32_t k,
+                                                              uint16_t* __restrict__ dy, int64_t ld_dy,
+                                                              float* __restrict__ dw) {
+    const int lane = threadIdx.x & 63;
+    const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    if (t >= T) return;
+    for (int j0 = 0; j0 < k; j0 += 8) {
+        int r[8];
+        float wj[8], dot[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+            const int pj = j0 + u < k ? pos[t * k + j0 + u] : -1;
+            r[u] = (uint32_t)pj < (uint32_t)rows ? pj : -1;
+            wj[u] = r[u] >= 0 ? w[t * k + j0 + u] : 0.0f;
+            dot[u] = 0.0f;
+        }
+        for (int c = lane; c < nch; c += 64) {
+            uint4 raw[8];
+            float d[8];
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (r[u] >= 0 && dw) raw[u] = load_nt16(y + (int64_t)r[u] * ld_y + 8 * c);
+            if (DO32) {
+                const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(dout) + t * ld_do + 8 * c);
+                const float4 a = f[0], b = f[1];
+                d[0] = a.x; d[1] = a.y; d[2] = a.z; d[3] = a.w;
+                d[4] = b.x; d[5] = b.y; d[6] = b.z; d[7] = b.w;
+            } else {
+                unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(dout) + t * ld_do + 8 * c), d);
+            }
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if (r[u] < 0) continue;
+                if (dw) {
+                    float v[8];
+                    unpack8(raw[u], v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) dot[u] = __builtin_fmaf(d[i], v[i], dot[u]);
+                }
+                if (dy)
+                    store_nt16(dy + (int64_t)r[u] * ld_dy + 8 * c,
+                               make_uint4(pack_bf16x2(wj[u] * d[0], wj[u] * d[1]), pack_bf16x2(wj[u] * d[2], wj[u] * d[3]),
+                                          pack_bf16x2(wj[u] * d[4], wj[u] * d[5]), pack_bf16x2(wj[u] * d[6], wj[u] * d[7])));
+            }
+        }
+        if (dw) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                const float s = lanes_sum<64>(dot[u]);
+                if (lane == 0 && j0 + u < k) dw[t * k + j0 + u] = s;
+            }
+        }
+    }
+}
+
 }  // namespace
 
 hipError_t launch_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y, const int32_t* pos,
                               const float* w, int64_t T, int32_t k, void* out, int64_t ld_out, int out_f32,
-                              hipStream_t st) {
+                              bool skip, hipStream_t st) {
     if (T == 0 || H == 0) return hipSuccess;
     const int32_t nch = (int32_t)(H / 8);
     const int64_t blocks = (T * nch + kThreads - 1) / kThreads;
-    if (out_f32)
-        hipLaunchKernelGGL(k_moe_combine<true>, dim3((unsigned)blocks), dim3(kThreads), 0, st, y, (int32_t)rows, nch,
-                           ld_y, pos, w, T, k, out, ld_out);
-    else
-        hipLaunchKernelGGL(k_moe_combine<false>, dim3((unsigned)blocks), dim3(kThreads), 0, st, y, (int32_t)rows, nch,
-                           ld_y, pos, w, T, k, out, ld_out);
+    const auto k_fn = out_f32 ? (skip ? k_moe_combine<true, true> : k_moe_combine<true, false>)
+                              : (skip ? k_moe_combine<false, true> : k_moe_combine<false, false>);
+    hipLaunchKernelGGL(k_fn, dim3((unsigned)blocks), dim3(kThreads), 0, st, y, (int32_t)rows, nch, ld_y, pos, w, T, k,
+                       out, ld_out);
+    return hipGetLastError();
+}
+
+hipError_t launch_moe_combine_bwd(const void* dout, int64_t ld_do, int do_f32, const uint16_t* y, int64_t rows,
+                                  int64_t H, int64_t ld_y, const int32_t* pos, const float* w, int64_t T, int32_t k,
+                                  uint16_t* dy, int64_t ld_dy, float* dw, hipStream_t st) {
+    if (T == 0) return hipSuccess;
+    const dim3 grid((unsigned)((T + kThreads / 64 - 1) / (kThreads / 64)));
+    const auto k_fn = do_f32 ? k_moe_combine_bwd<true> : k_moe_combine_bwd<false>;
+    hipLaunchKernelGGL(k_fn, grid, dim3(kThreads), 0, st, dout, ld_do, y, (int32_t)rows, (int32_t)(H / 8), ld_y, pos,
+                       w, T, k, dy, ld_dy, dw);
     return hipGetLastError();
 }
 

@@ -1,0 +1,83 @@
+// Lane reductions shared by the norm and router kernels (64-wide waves).
+// The first four steps of every butterfly are DPP moves, which cost a VALU
+// instruction each; only the 16- and 32-lane steps go through LDS crossbar
+// shuffles.  Sums have a fixed order, so results do not depend on scheduling.
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace fp8bs {
+
+// Source lane of each DPP step inside a 16-lane row: xor 1, xor 2 (quad
+// permutes), 7 - i within 8 lanes, 15 - i within 16.  After each step the
+// lanes it has joined hold the same value, so the four make an all-reduce.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp_mov(uint32_t v) {
+    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+template <int CTRL>
+__device__ __forceinline__ float dpp_movf(float v) {
+    return __uint_as_float(dpp_mov<CTRL>(__float_as_uint(v)));
+}
+
+__device__ __forceinline__ float row16_sum(float v) {
+    v += dpp_movf<kDppXor1>(v);
+    v += dpp_movf<kDppXor2>(v);
+    v += dpp_movf<kDppHalfMirror>(v);
+    v += dpp_movf<kDppMirror>(v);
+    return v;
+}
+__device__ __forceinline__ float row16_max(float v) {
+    v = fmaxf(v, dpp_movf<kDppXor1>(v));
+    v = fmaxf(v, dpp_movf<kDppXor2>(v));
+    v = fmaxf(v, dpp_movf<kDppHalfMirror>(v));
+    v = fmaxf(v, dpp_movf<kDppMirror>(v));
+    return v;
+}
+__device__ __forceinline__ uint32_t row16_umax(uint32_t v) {
+    v = max(v, dpp_mov<kDppXor1>(v));
+    v = max(v, dpp_mov<kDppXor2>(v));
+    v = max(v, dpp_mov<kDppHalfMirror>(v));
+    v = max(v, dpp_mov<kDppMirror>(v));
+    return v;
+}
+__device__ __forceinline__ uint32_t row16_umin(uint32_t v) {
+    v = min(v, dpp_mov<kDppXor1>(v));
+    v = min(v, dpp_mov<kDppXor2>(v));
+    v = min(v, dpp_mov<kDppHalfMirror>(v));
+    v = min(v, dpp_mov<kDppMirror>(v));
+    return v;
+}
+
+// All-reduce over LANES lanes (16: a DPP row, 64: the wave).
+template <int LANES>
+__device__ __forceinline__ float lanes_sum(float v) {
+    v = row16_sum(v);
+    if (LANES == 64) {
+        v += __shfl_xor(v, 16, 64);
+        v += __shfl_xor(v, 32, 64);
+    }
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_umax(uint32_t v) {
+    v = row16_umax(v);
+    if (LANES == 64) {
+        v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+        v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+    }
+    return v;
+}
+template <int LANES>
+__device__ __forceinline__ uint32_t lanes_umin(uint32_t v) {
+    v = row16_umin(v);
+    if (LANES == 64) {
+        v = min(v, (uint32_t)__shfl_xor((int)v, 16, 64));
+        v = min(v, (uint32_t)__shfl_xor((int)v, 32, 64));
+    }
+    return v;
+}
+
+}  // namespace fp8bs

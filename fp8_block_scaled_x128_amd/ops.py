@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import threading
+from typing import NamedTuple, Optional
 
 import torch
 
@@ -27,7 +28,9 @@ BSCALE_BLOCK128, BSCALE_ROW128 = 0, 1
 EXPORTS = ["fp8_quant_rowblock", "fp8_quant_block2d", "fp8_quant_linear", "fp8_quant_rowwise", "fp8_quant_tensorwise", "fp8_blockscaled_gemm", "fp8_blockscaled_gemm_plan",
            "fp8_blockscaled_gemm_splitk", "fp8_blockscaled_gemm_splitk_noalloc", "fp8_blockscaled_gemm_splitk_plan",
            "fp8_grouped_gemm", "fp8_grouped_gemm_ws_size", "fp8_grouped_gemm_swiglu_quant", "mxfp8_grouped_gemm_swiglu_quant",
-           "fp8_silu_mul_quant", "fp8_moe_combine", "mxfp8_quant", "mxfp8_quant_t",
+           "fp8_silu_mul_quant", "fp8_moe_combine", "fp8_moe_combine_routed", "fp8_moe_combine_backward",
+           "fp8_moe_route", "fp8_moe_route_ws_size", "fp8_moe_route_backward",
+           "fp8_block_norm", "fp8_block_norm_backward", "fp8_block_norm_backward_ws_size", "mxfp8_quant", "mxfp8_quant_t",
            "fp8_quant_dual_axis", "fp8_transpose_codes", "fp8_quant_linear_pow2",
            "fp8_quant_pow2", "fp8_blockscaled_gemm_pow2", "mxfp8_gemm", "fp8bs_e4m3_encode",
            "fp8bs_status_string", "fp8bs_last_error_detail"]
@@ -54,7 +57,7 @@ def load():
             raise RuntimeError("libfp8bs.so is not built (%s); run `python -m fp8_block_scaled_x128_amd.build`"
                                % _LIB_PATH)
         lib = ctypes.CDLL(_LIB_PATH)
-        P, I64, I32, INT = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int
+        P, I64, I32, INT, F32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int32, ctypes.c_int, ctypes.c_float
         sig = {
             "fp8_quant_rowblock": [P, I64, I64, I64, INT, P, I64, P, I64, I64, P],
             "fp8_quant_block2d": [P, I64, I64, I64, I64, P, I64, P, I64, P, P],
@@ -77,6 +80,16 @@ def load():
                                                 I64, P, I64, P, I64, I64, P],
             "fp8_silu_mul_quant": [P, I64, I64, I64, INT, P, I64, P, I64, I64, P, I64, P],
             "fp8_moe_combine": [P, I64, I64, I64, P, P, I64, I32, P, I64, INT, P],
+            "fp8_moe_combine_routed": [P, I64, I64, I64, P, P, I64, I32, P, I64, INT, P],
+            "fp8_moe_combine_backward": [P, I64, INT, P, I64, I64, I64, P, P, I64, I32, P, I64, P, P],
+            "fp8_moe_route": [P, I64, I32, I64, INT, I32, I32, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P],
+            "fp8_moe_route_ws_size": [I64, I32, P],
+            "fp8_moe_route_backward": [P, I64, I32, I64, INT, I32, I32, P, P, P, P, P, P, P, I64, P],
+            "fp8_block_norm": [I64, I64, P, I64, P, I64, INT, P, I64, I64, F32, P, P, INT, F32, P, I64, P, I64, P,
+                               I64, P, I64, I64, P],
+            "fp8_block_norm_backward": [I64, I64, P, I64, INT, P, I64, P, I64, INT, P, I64, P, I64, I64, F32, P, P,
+                                        INT, F32, P, I64, P, I64, P, I64, INT, P, P, P, ctypes.c_size_t, P],
+            "fp8_block_norm_backward_ws_size": [I64, I64, I64, I32, I32, I32, P],
             "mxfp8_quant": [P, I64, I64, I64, P, I64, P, I64, I64, P],
             "mxfp8_quant_t": [P, I64, I64, I64, P, I64, P, I64, I64, P],
             "fp8_quant_dual_axis": [P, I64, I64, I64, I32, P, I64, P, I64, I64, P, I64, P, I64, I64, P],
@@ -243,6 +256,70 @@ def fp8_moe_combine(y, rows, H, ld_y, token_rows, weights, T, k, out, ld_out, ou
     st = load().fp8_moe_combine(_p(y), rows, H, ld_y, _p(token_rows), _p(weights), T, k, _p(out), ld_out,
                                 out_type, _stream(stream))
     return _check("fp8_moe_combine", st, raise_on_error)
+
+
+def fp8_moe_combine_routed(y, rows, H, ld_y, token_rows, weights, T, k, out, ld_out, out_type, stream=None,
+                           raise_on_error=True):
+    st = load().fp8_moe_combine_routed(_p(y), rows, H, ld_y, _p(token_rows), _p(weights), T, k, _p(out), ld_out,
+                                       out_type, _stream(stream))
+    return _check("fp8_moe_combine_routed", st, raise_on_error)
+
+
+def fp8_moe_combine_backward(dout, ld_dout, dout_type, y, rows, H, ld_y, token_rows, weights, T, k, dy, ld_dy,
+                             dweights, stream=None, raise_on_error=True):
+    st = load().fp8_moe_combine_backward(_p(dout), ld_dout, dout_type, _p(y), rows, H, ld_y, _p(token_rows),
+                                         _p(weights), T, k, _p(dy), ld_dy, _p(dweights), _stream(stream))
+    return _check("fp8_moe_combine_backward", st, raise_on_error)
+
+
+def fp8_moe_route(logits, T, E, ld, type_, k, renorm, mask, experts, weights, counts, offsets, row_token, token_rows,
+                  lse, loss, ws, ws_bytes, stream=None, raise_on_error=True):
+    st = load().fp8_moe_route(_p(logits), T, E, ld, type_, k, renorm, _p(mask), _p(experts), _p(weights), _p(counts),
+                              _p(offsets), _p(row_token), _p(token_rows), _p(lse), _p(loss), _p(ws), ws_bytes,
+                              _stream(stream))
+    return _check("fp8_moe_route", st, raise_on_error)
+
+
+def fp8_moe_route_ws_size(T, E):
+    """Workspace bytes of fp8_moe_route (host only)."""
+    out = ctypes.c_size_t(0)
+    _check("fp8_moe_route_ws_size", load().fp8_moe_route_ws_size(T, E, ctypes.byref(out)))
+    return out.value
+
+
+def fp8_moe_route_backward(logits, T, E, ld, type_, k, renorm, experts, weights, counts, lse, dweights, dloss,
+                           dlogits, ld_d, stream=None, raise_on_error=True):
+    st = load().fp8_moe_route_backward(_p(logits), T, E, ld, type_, k, renorm, _p(experts), _p(weights), _p(counts),
+                                       _p(lse), _p(dweights), _p(dloss), _p(dlogits), ld_d, _stream(stream))
+    return _check("fp8_moe_route_backward", st, raise_on_error)
+
+
+def fp8_block_norm(rows, cols, x, ld_x, residual, ld_r, stream_type, gate, ld_gate, rows_per_gate, scale, w_post,
+                   w_pre, w_type, eps, h, ld_h, y, ld_y, q, ld_q, s, s_stride_row, s_stride_group, stream=None,
+                   raise_on_error=True):
+    st = load().fp8_block_norm(rows, cols, _p(x), ld_x, _p(residual), ld_r, stream_type, _p(gate), ld_gate,
+                               rows_per_gate, scale, _p(w_post), _p(w_pre), w_type, eps, _p(h), ld_h, _p(y), ld_y,
+                               _p(q), ld_q, _p(s), s_stride_row, s_stride_group, _stream(stream))
+    return _check("fp8_block_norm", st, raise_on_error)
+
+
+def fp8_block_norm_backward(rows, cols, dy, ld_dy, dy_type, dh, ld_dh, h, ld_h, stream_type, x, ld_x, gate, ld_gate,
+                            rows_per_gate, scale, w_post, w_pre, w_type, eps, dx, ld_dx, dres, ld_dres, dgate,
+                            ld_dgate, dgate_type, dw_post, dw_pre, ws, ws_bytes, stream=None, raise_on_error=True):
+    st = load().fp8_block_norm_backward(rows, cols, _p(dy), ld_dy, dy_type, _p(dh), ld_dh, _p(h), ld_h, stream_type,
+                                        _p(x), ld_x, _p(gate), ld_gate, rows_per_gate, scale, _p(w_post), _p(w_pre),
+                                        w_type, eps, _p(dx), ld_dx, _p(dres), ld_dres, _p(dgate), ld_dgate,
+                                        dgate_type, _p(dw_post), _p(dw_pre), _p(ws), ws_bytes, _stream(stream))
+    return _check("fp8_block_norm_backward", st, raise_on_error)
+
+
+def fp8_block_norm_backward_ws_size(rows, cols, rows_per_gate, dw_post, dw_pre, dgate):
+    """Workspace bytes of fp8_block_norm_backward (host only)."""
+    out = ctypes.c_size_t(0)
+    _check("fp8_block_norm_backward_ws_size",
+           load().fp8_block_norm_backward_ws_size(rows, cols, rows_per_gate, int(dw_post), int(dw_pre), int(dgate),
+                                                  ctypes.byref(out)))
+    return out.value
 
 
 def mxfp8_quant(x, rows, cols, ld_x, q, ld_q, s, s_stride_row, s_stride_group, stream=None, raise_on_error=True):
@@ -453,6 +530,23 @@ def linear_backward(dy: torch.Tensor, saved):
     return dx, dw
 
 
+def _moe_experts(qx, sx, T, qgu, sgu, qdt, sdt, offsets, row_token):
+    """The experts' MLPs over the routed rows of a quantized activation: y
+    bf16 [rows, H] in expert-sorted order."""
+    G, N2, H = qgu.shape
+    I = N2 // 2
+    rows = row_token.numel()
+    dev = qx.device
+    qh = _u8((rows, I), dev)
+    shb = torch.empty((I // 128, rows), dtype=torch.float32, device=dev)
+    fp8_grouped_gemm_swiglu_quant(rows, I, H, G, offsets, row_token, T, qx, H, sx, sx.stride(0), sx.stride(1), qgu, H,
+                                  N2 * H, sgu, sgu.stride(0), sgu.stride(1), sgu.stride(2), qh, I, shb, 1, rows)
+    y = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
+    fp8_grouped_gemm(rows, H, I, G, offsets, None, rows, qh, I, shb, 1, rows, qdt, I, H * I, sdt, sdt.stride(0),
+                     sdt.stride(2), sdt.stride(1), y, H, OUT_BF16)
+    return y
+
+
 def moe_forward(x, qgu, sgu, qdt, sdt, offsets, row_token, token_rows, weights, out_dtype=torch.bfloat16):
     """One block-wise FP8 MoE layer forward: X [T, H] in 1x128 groups; the
     grouped gate/up GEMM over the experts' rows (gathered by row_token), with
@@ -465,21 +559,291 @@ def moe_forward(x, qgu, sgu, qdt, sdt, offsets, row_token, token_rows, weights, 
     [T, k] (grouped row of each token's slot), weights fp32 [T, k]."""
     assert x.dtype == torch.bfloat16 and x.dim() == 2 and x.is_contiguous()
     T, H = x.shape
-    G, N2, _ = qgu.shape
-    I = N2 // 2
     rows = row_token.numel()
     qx, sx = quant_rowblock(x, AXIS_ROW, "m_major")
-    qh = _u8((rows, I), x.device)
-    shb = torch.empty((I // 128, rows), dtype=torch.float32, device=x.device)
-    fp8_grouped_gemm_swiglu_quant(rows, I, H, G, offsets, row_token, T, qx, H, sx, sx.stride(0), sx.stride(1), qgu, H,
-                                  N2 * H, sgu, sgu.stride(0), sgu.stride(1), sgu.stride(2), qh, I, shb, 1, rows)
-    y = torch.empty((rows, H), dtype=torch.bfloat16, device=x.device)
-    fp8_grouped_gemm(rows, H, I, G, offsets, None, rows, qh, I, shb, 1, rows, qdt, I, H * I, sdt, sdt.stride(0),
-                     sdt.stride(2), sdt.stride(1), y, H, OUT_BF16)
+    y = _moe_experts(qx, sx, T, qgu, sgu, qdt, sdt, offsets, row_token)
     k = token_rows.shape[1]
     out = torch.empty((T, H), dtype=out_dtype, device=x.device)
     fp8_moe_combine(y, rows, H, H, token_rows.contiguous(), weights.contiguous(), T, k, out, H,
                     OUT_FP32 if out_dtype == torch.float32 else OUT_BF16)
+    return out
+
+
+def moe_forward_routed(codes, logits, top_k, qgu, sgu, qdt, sdt, *, renorm=True, mask=None,
+                       out_dtype=torch.bfloat16):
+    """One block-wise FP8 MoE layer from router logits [T, G]: moe_route, the
+    experts on the activation's codes, the combine.  codes = (q [T, H], s
+    [T, H/128]) as quant_rowblock or block_norm give them; weights as in
+    moe_forward.  Masked tokens reach no expert and get zeros.  Returns (out
+    [T, H], routing, y): y is the experts' output, which
+    moe_combine_backward reads."""
+    qx, sx = codes
+    T, H = qx.shape
+    if tuple(logits.shape) != (T, qgu.shape[0]):
+        raise ValueError("logits: [%d, %d] expected, got %s" % (T, qgu.shape[0], tuple(logits.shape)))
+    r = moe_route(logits, top_k, renorm=renorm, mask=mask)
+    y = _moe_experts(qx, sx, T, qgu, sgu, qdt, sdt, r.offsets, r.row_token)
+    out = torch.empty((T, H), dtype=out_dtype, device=qx.device)
+    fp8_moe_combine_routed(y, T * top_k, H, H, r.token_rows, r.weights, T, top_k, out, H, _otype(out_dtype))
+    return out, r, y
+
+
+# ---------------------------------- between the GEMMs: norms and the router
+def _otype(t_or_dtype):
+    dt = t_or_dtype.dtype if isinstance(t_or_dtype, torch.Tensor) else t_or_dtype
+    if dt == torch.bfloat16:
+        return OUT_BF16
+    if dt == torch.float32:
+        return OUT_FP32
+    raise TypeError("bfloat16 or float32 expected, got %s" % dt)
+
+
+def _on_device(*tensors):
+    """Every call runs on the current device's current stream: tensors that
+    live elsewhere are refused."""
+    cur = torch.cuda.current_device()
+    for t in tensors:
+        if t is not None and (not t.is_cuda or t.get_device() != cur):
+            raise ValueError("tensor on %s; the current device is cuda:%d" % (t.device, cur))
+
+
+def _matrix(name, t, rows, cols, *dtypes):
+    if t is None:
+        return 0
+    if t.dtype not in dtypes or t.dim() != 2 or tuple(t.shape) != (rows, cols) or (t.stride(1) != 1 and cols > 1):
+        raise ValueError("%s: [%d, %d] of %s with unit column stride expected, got %s %s, strides %s"
+                         % (name, rows, cols, "/".join(str(d) for d in dtypes), tuple(t.shape), t.dtype, t.stride()))
+    # a single row's stride is never used: torch may leave anything there
+    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+
+
+def _vector(name, t, n, *dtypes):
+    if t is not None and (t.dtype not in dtypes or tuple(t.shape) != (n,) or not t.is_contiguous()):
+        raise ValueError("%s: contiguous [%d] of %s expected, got %s %s"
+                         % (name, n, "/".join(str(d) for d in dtypes), tuple(t.shape), t.dtype))
+
+
+_BF, _F32 = torch.bfloat16, torch.float32
+
+
+class BlockNorm(NamedTuple):
+    """Outputs of block_norm (None where not asked for).  s is a [rows,
+    groups] view of a [groups, rows] buffer, the layout the GEMMs read."""
+    h: Optional[torch.Tensor]
+    y: Optional[torch.Tensor]
+    q: Optional[torch.Tensor]
+    s: Optional[torch.Tensor]
+
+
+def block_norm(residual=None, x=None, *, w_pre=None, w_post=None, gate=None, rows_per_gate=1, scale=1.0, eps=1e-6,
+               h=True, y=True, quant=True, out: Optional[BlockNorm] = None) -> BlockNorm:
+    """h = residual + scale * gate * N(x; w_post) and y = N(h; w_pre) with
+    1x128 E4M3 codes (q, s) for the next linear layer, in one pass (see
+    fp8_block_norm).  residual [rows, cols] bf16 or fp32 and x bf16 (one of
+    them may be missing), gate bf16 [ceil(rows / rows_per_gate), cols], weights
+    bf16 or fp32 [cols].  h, y, quant say which outputs to make (y and quant
+    only with w_pre; h takes the residual's type); `out` is an earlier result
+    of the same call whose tensors are written again."""
+    ref = x if residual is None else residual
+    if ref is None:
+        raise ValueError("residual or x is required")
+    rows, cols = ref.shape
+    stream_dt = _BF if residual is None else residual.dtype
+    stype = _otype(stream_dt)
+    ld_r, ld_x = _matrix("residual", residual, rows, cols, _BF, _F32), _matrix("x", x, rows, cols, _BF)
+    ld_g = 0
+    if gate is not None:
+        if rows_per_gate < 1:
+            raise ValueError("rows_per_gate must be >= 1")
+        ld_g = _matrix("gate", gate, -(-rows // rows_per_gate), cols, _BF)
+    w = w_pre if w_pre is not None else w_post
+    wt = OUT_BF16 if w is None else _otype(w)
+    for name, v in (("w_pre", w_pre), ("w_post", w_post)):
+        _vector(name, v, cols, _BF if w is None else w.dtype)
+    if w_pre is None:
+        y = quant = False
+    dev = ref.device
+    if out is None:
+        ng = (cols + 127) // 128
+        out = BlockNorm(torch.empty((rows, cols), dtype=stream_dt, device=dev) if h else None,
+                        torch.empty((rows, cols), dtype=_BF, device=dev) if y else None,
+                        _u8((rows, cols), dev) if quant else None,
+                        torch.empty((ng, rows), dtype=_F32, device=dev).t() if quant else None)
+    ho, yo, qo, so = out
+    if (ho is not None) != bool(h) or (yo is not None) != bool(y) or (qo is not None) != bool(quant):
+        raise ValueError("out does not hold the outputs asked for")
+    ld_h, ld_y = _matrix("out.h", ho, rows, cols, stream_dt), _matrix("out.y", yo, rows, cols, _BF)
+    ld_q = _matrix("out.q", qo, rows, cols, torch.uint8)
+    if qo is not None and (so is None or so.dtype != _F32 or tuple(so.shape) != (rows, (cols + 127) // 128)):
+        raise ValueError("out.s: float32 [%d, %d] expected" % (rows, (cols + 127) // 128))
+    _on_device(residual, x, gate, w_pre, w_post, ho, yo, qo, so)
+    fp8_block_norm(rows, cols, x, ld_x, residual, ld_r, stype, gate, ld_g, rows_per_gate, scale, w_post, w_pre, wt,
+                   eps, ho, ld_h, yo, ld_y, qo, ld_q, so, 0 if so is None else so.stride(0),
+                   0 if so is None else so.stride(1))
+    return out
+
+
+class BlockNormGrads(NamedTuple):
+    """Outputs of block_norm_backward (None where there is nothing to give);
+    ws is the call's workspace."""
+    dres: Optional[torch.Tensor]
+    dx: Optional[torch.Tensor]
+    dgate: Optional[torch.Tensor]
+    dw_post: Optional[torch.Tensor]
+    dw_pre: Optional[torch.Tensor]
+    ws: Optional[torch.Tensor]
+
+
+def block_norm_backward(dy=None, dh=None, h=None, x=None, *, w_pre=None, w_post=None, gate=None, rows_per_gate=1,
+                        scale=1.0, eps=1e-6, dres=True, dgate_dtype=torch.float32,
+                        out: Optional[BlockNormGrads] = None) -> BlockNormGrads:
+    """Gradients of block_norm from dy = dL/dy (bf16 or fp32; with h and
+    w_pre) and dh = dL/dh past y (h's type), at the saved h and x: dres (the
+    stream's type; not made with dres=False), dx bf16 when there is an x, dgate
+    (dgate_dtype) when there is a gate, dw_post and dw_pre fp32.  `out` is an
+    earlier result of the same call whose tensors are written again."""
+    ref = dh if dh is not None else h
+    if ref is None:
+        raise ValueError("dh, or dy with h, is required")
+    rows, cols = ref.shape
+    stream_dt = ref.dtype
+    stype = _otype(stream_dt)
+    if (dy is None) != (w_pre is None) or (dy is None) != (h is None):
+        raise ValueError("dy, h and w_pre go together")
+    if x is None and (w_post is not None or gate is not None):
+        raise ValueError("w_post and gate need x")
+    ld_dy, ld_dh = _matrix("dy", dy, rows, cols, _BF, _F32), _matrix("dh", dh, rows, cols, stream_dt)
+    ld_h, ld_x = _matrix("h", h, rows, cols, stream_dt), _matrix("x", x, rows, cols, _BF)
+    ld_g = ngate = 0
+    if gate is not None:
+        if rows_per_gate < 1:
+            raise ValueError("rows_per_gate must be >= 1")
+        ngate = -(-rows // rows_per_gate)
+        ld_g = _matrix("gate", gate, ngate, cols, _BF)
+    w = w_pre if w_pre is not None else w_post
+    wt = OUT_BF16 if w is None else _otype(w)
+    for name, v in (("w_pre", w_pre), ("w_post", w_post)):
+        _vector(name, v, cols, _BF if w is None else w.dtype)
+    dev = ref.device
+    need = fp8_block_norm_backward_ws_size(rows, cols, rows_per_gate, w_post is not None, w_pre is not None,
+                                           gate is not None)
+    if out is None:
+        e = lambda n, dt: torch.empty((n, cols), dtype=dt, device=dev)
+        out = BlockNormGrads(e(rows, stream_dt) if dres else None, e(rows, _BF) if x is not None else None,
+                             e(ngate, dgate_dtype) if gate is not None else None,
+                             torch.empty(cols, dtype=_F32, device=dev) if w_post is not None else None,
+                             torch.empty(cols, dtype=_F32, device=dev) if w_pre is not None else None,
+                             _u8((need,), dev) if need else None)
+    o = out
+    for name, t, asked in (("dres", o.dres, dres), ("dx", o.dx, x is not None), ("dgate", o.dgate, gate is not None),
+                           ("dw_post", o.dw_post, w_post is not None), ("dw_pre", o.dw_pre, w_pre is not None)):
+        if (t is not None) != bool(asked):
+            raise ValueError("out.%s does not fit the call" % name)
+    ld_dres, ld_dx = _matrix("out.dres", o.dres, rows, cols, stream_dt), _matrix("out.dx", o.dx, rows, cols, _BF)
+    ld_dg = _matrix("out.dgate", o.dgate, ngate, cols, dgate_dtype)
+    _vector("out.dw_post", o.dw_post, cols, _F32)
+    _vector("out.dw_pre", o.dw_pre, cols, _F32)
+    _on_device(dy, dh, h, x, gate, w_pre, w_post, *o)
+    fp8_block_norm_backward(rows, cols, dy, ld_dy, OUT_BF16 if dy is None else _otype(dy), dh, ld_dh, h, ld_h, stype,
+                            x, ld_x, gate, ld_g, rows_per_gate, scale, w_post, w_pre, wt, eps, o.dx, ld_dx, o.dres,
+                            ld_dres, o.dgate, ld_dg, _otype(dgate_dtype), o.dw_post, o.dw_pre, o.ws,
+                            0 if o.ws is None else o.ws.numel())
+    return out
+
+
+class Routing(NamedTuple):
+    """Outputs of moe_route: int32 experts [T, k] (-1: none), fp32 weights
+    [T, k], int32 counts [E + 1] (the last one: routed tokens), offsets
+    [E + 1], row_token [T * k], token_rows [T, k] (-1: no row), fp32 lse [T]
+    and loss [2] (balance, z); ws is the call's workspace."""
+    experts: torch.Tensor
+    weights: torch.Tensor
+    counts: torch.Tensor
+    offsets: torch.Tensor
+    row_token: torch.Tensor
+    token_rows: torch.Tensor
+    lse: torch.Tensor
+    loss: torch.Tensor
+    ws: Optional[torch.Tensor]
+
+
+def _mask_bytes(mask, T):
+    if mask is None:
+        return None
+    if mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (T,) or not mask.is_contiguous():
+        raise ValueError("mask: contiguous bool or uint8 [%d] expected" % T)
+    return mask
+
+
+def moe_route(logits, top_k, *, renorm=True, mask=None, out: Optional[Routing] = None) -> Routing:
+    """Top-k routing of router logits [T, E] (bf16 or fp32): experts, weights,
+    counts, the expert-sorted row maps of moe_forward and the grouped GEMMs,
+    and the balance and z losses (see fp8_moe_route).  mask [T] (bool or
+    uint8): tokens with False are not routed.  `out` is an earlier result for
+    the same sizes whose tensors are written again."""
+    T, E = logits.shape
+    ld = _matrix("logits", logits, T, E, _BF, _F32)
+    mask = _mask_bytes(mask, T)
+    need = fp8_moe_route_ws_size(T, E)
+    dev, i32 = logits.device, torch.int32
+    if out is None:
+        e = lambda *s, dtype=i32: torch.empty(s, dtype=dtype, device=dev)
+        out = Routing(e(T, top_k), e(T, top_k, dtype=_F32), e(E + 1), e(E + 1), e(T * top_k), e(T, top_k),
+                      e(T, dtype=_F32), e(2, dtype=_F32), _u8((need,), dev) if need else None)
+    o = out
+    for name, t, shape, dt in (("experts", o.experts, (T, top_k), i32), ("weights", o.weights, (T, top_k), _F32),
+                               ("counts", o.counts, (E + 1,), i32), ("offsets", o.offsets, (E + 1,), i32),
+                               ("row_token", o.row_token, (T * top_k,), i32),
+                               ("token_rows", o.token_rows, (T, top_k), i32), ("lse", o.lse, (T,), _F32),
+                               ("loss", o.loss, (2,), _F32)):
+        if t.shape != shape or t.dtype != dt or not t.is_contiguous():
+            raise ValueError("out.%s: contiguous %s %s expected" % (name, dt, list(shape)))
+    _on_device(logits, mask, *o)
+    fp8_moe_route(logits, T, E, ld, _otype(logits), top_k, int(bool(renorm)), mask, o.experts, o.weights, o.counts,
+                  o.offsets, o.row_token, o.token_rows, o.lse, o.loss, o.ws, 0 if o.ws is None else o.ws.numel())
+    return out
+
+
+def moe_route_backward(logits, experts, weights, counts, lse, *, dweights=None, dloss=None, renorm=True, out=None):
+    """dlogits [T, E] (the logits' type) of sum(weights * dweights) +
+    dloss . loss, from moe_route's outputs (see fp8_moe_route_backward)."""
+    T, E = logits.shape
+    k = experts.shape[1]
+    ld = _matrix("logits", logits, T, E, _BF, _F32)
+    for name, t, shape, dt in (("experts", experts, (T, k), torch.int32), ("weights", weights, (T, k), _F32),
+                               ("counts", counts, (E + 1,), torch.int32), ("lse", lse, (T,), _F32),
+                               ("dweights", dweights, (T, k), _F32), ("dloss", dloss, (2,), _F32)):
+        if t is not None and (t.shape != shape or t.dtype != dt or not t.is_contiguous()):
+            raise ValueError("%s: contiguous %s %s expected" % (name, dt, list(shape)))
+    if out is None:
+        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
+    ld_d = _matrix("out", out, T, E, logits.dtype)
+    _on_device(logits, experts, weights, counts, lse, dweights, dloss, out)
+    fp8_moe_route_backward(logits, T, E, ld, _otype(logits), k, int(bool(renorm)), experts, weights, counts, lse,
+                           dweights, dloss, out, ld_d)
+    return out
+
+
+def moe_combine_backward(dout, y, token_rows, weights, *, out=None):
+    """(dy bf16 [rows, H], dweights fp32 [T, k]) of the combine, from dout
+    [T, H] (bf16 or fp32) and the y [rows, H] it read.  Rows of dy without a
+    slot are not written."""
+    T, H = dout.shape
+    k = token_rows.shape[1]
+    rows = y.shape[0]
+    ld_do, ld_y = _matrix("dout", dout, T, H, _BF, _F32), _matrix("y", y, rows, H, _BF)
+    for name, t, dt in (("token_rows", token_rows, torch.int32), ("weights", weights, _F32)):
+        if t.shape != (T, k) or t.dtype != dt or not t.is_contiguous():
+            raise ValueError("%s: contiguous %s [%d, %d] expected" % (name, dt, T, k))
+    if out is None:
+        out = (torch.empty((rows, H), dtype=_BF, device=dout.device),
+               torch.empty((T, k), dtype=_F32, device=dout.device))
+    dy, dw = out
+    ld_dy = _matrix("out[0]", dy, rows, H, _BF)
+    if dw.shape != (T, k) or dw.dtype != _F32 or not dw.is_contiguous():
+        raise ValueError("out[1]: contiguous float32 [%d, %d] expected" % (T, k))
+    _on_device(dout, y, token_rows, weights, dy, dw)
+    fp8_moe_combine_backward(dout, ld_do, _otype(dout), y, rows, H, ld_y, token_rows, weights, T, k, dy, ld_dy, dw)
     return out
 
 

@@ -315,7 +315,8 @@ fp8bs_status fp8_blockscaled_gemm_splitk_plan(int64_t M, int64_t N, int64_t K, f
  *
  * offsets : device int32 [G + 1]; rows offsets[g] .. offsets[g+1]-1 of the
  *           output belong to expert g.  offsets[0] == 0, non-decreasing,
- *           offsets[G] == total_rows; empty groups are allowed.  The offsets
+ *           offsets[G] <= total_rows; empty groups are allowed, and rows
+ *           behind offsets[G] are neither read nor written.  The offsets
  *           stay on the device (no host synchronization); a violation of this
  *           contract is not detected.
  * a_rows  : nullable device int32 [total_rows]; if given, output row r reads
@@ -464,6 +465,195 @@ fp8bs_status fp8_silu_mul_quant(const uint16_t* gate_up, int64_t rows, int64_t I
 fp8bs_status fp8_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y,
                              const int32_t* token_rows, const float* weights, int64_t T, int32_t k,
                              void* out, int64_t ld_out, fp8bs_out out_type, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_moe_combine_routed -- fp8_moe_combine (same formula, order, arguments
+ * and requirements) for the maps fp8_moe_route writes: a slot whose
+ * token_rows entry is outside [0, rows) (the router's -1) contributes
+ * nothing, whatever its weight.  A token without any row gets zeros.  rows
+ * may be 0 with T > 0 (y is then not read).
+ * ------------------------------------------------------------------------ */
+fp8bs_status fp8_moe_combine_routed(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y,
+                                    const int32_t* token_rows, const float* weights, int64_t T, int32_t k,
+                                    void* out, int64_t ld_out, fp8bs_out out_type, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_moe_combine_backward -- gradient of the combine,
+ *
+ *   dy[token_rows[t*k + j]]  = weights[t*k + j] * dout[t]
+ *   dweights[t*k + j]        = sum_n dout[t][n] * y[token_rows[t*k + j]][n]
+ *
+ * in fp32, dy rounded to bf16 (nearest even).  Slots without a row (entries
+ * outside [0, rows)) give dweights 0 and no dy; rows of dy that no slot names
+ * are left as they were.  Two slots must not name the same row when dy is
+ * written (fp8_moe_route never does that).
+ *
+ * dout     : [T][ld_dout], bf16 or fp32 per dout_type.
+ * y        : as in fp8_moe_combine; read only for dweights (may be NULL
+ *            without them).
+ * dy       : nullable bf16 [rows][ld_dy].   dweights : nullable fp32 [T][k].
+ *            At least one of them.
+ * Requirements: rows, H, T >= 0, k >= 1, H % 8 == 0; leading dimensions >= H
+ * and % 8 == 0; dout, y, dy 16-byte aligned, the rest 4-byte aligned;
+ * T < 2^26.
+ * ------------------------------------------------------------------------ */
+fp8bs_status fp8_moe_combine_backward(const void* dout, int64_t ld_dout, fp8bs_out dout_type,
+                                      const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y,
+                                      const int32_t* token_rows, const float* weights, int64_t T, int32_t k,
+                                      uint16_t* dy, int64_t ld_dy, float* dweights, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_moe_route -- from router logits to everything the grouped GEMMs and
+ * the combine read (the routing of the Qwen3-30B-A3B recipe of "Low Precision
+ * RL", section "2. Unified block-wise FP8 (DeepSeek-style)"), with per-expert
+ * counts and the two auxiliary losses.
+ *
+ * Selection: each token takes the k experts with the largest logits, in that
+ * order; equal logits (-0 and +0 are equal) go to the lower expert, NaN counts
+ * as the largest and makes its token's weights, lse and the losses NaN.  A
+ * token whose mask byte is 0 is not routed and its logits are not read; an
+ * expert whose logit is -inf is not taken.  A slot that takes no expert has
+ * expert -1, weight 0 and row -1.
+ *
+ *   lse_t  = log sum_e exp(z_te)  (-inf if the token is masked or has only
+ *            -inf logits: a token that is not routed)
+ *   weight = exp(z_j) / sum over the token's selected experts of exp(z)
+ *            (renorm 1), or exp(z_j - lse_t) (renorm 0)
+ *   counts[e] = tokens routed to expert e
+ *   loss[0] = E * sum_e f_e P_e,  f_e = counts[e] / sum(counts),
+ *             P_e = mean over routed tokens of exp(z_te - lse_t)
+ *   loss[1] = mean over routed tokens of lse_t^2
+ *   (both 0 when no token is routed)
+ *
+ * Rows: the assignments sorted stably by (expert, token).  offsets[e] is the
+ * first row of expert e, offsets[E] the number of rows; row_token[row] is the
+ * row's token, 0 behind the last row; token_rows is the inverse.  The grouped
+ * GEMMs walk the offsets, so they take these maps with total_rows = T * k and
+ * leave the rows behind offsets[E] as they were.
+ *
+ * logits : [T][ld], bf16 or fp32 per `type`.   mask : nullable, uint8 [T].
+ * experts, token_rows : int32 [T][k].   weights : fp32 [T][k].
+ * counts : int32 [E + 1]; counts[E] is the number of routed tokens.
+ * offsets : int32 [E + 1].   row_token : int32 [T * k].   lse : fp32 [T].
+ * loss : fp32 [2].
+ * ws : device workspace of fp8_moe_route_ws_size bytes, 16-byte aligned
+ *      (nullable when that is 0); its contents on entry are ignored.  Calls
+ *      that overlap in time need separate workspaces.
+ * The results are the same bits every time.  Requirements: 0 <= T <= 2^26,
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32), T * k < 2^31, ld >= E; pointers
+ * aligned to their element.
+ * ------------------------------------------------------------------------ */
+fp8bs_status fp8_moe_route(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k,
+                           int32_t renorm, const uint8_t* mask, int32_t* experts, float* weights, int32_t* counts,
+                           int32_t* offsets, int32_t* row_token, int32_t* token_rows, float* lse, float* loss,
+                           void* ws, size_t ws_bytes, hipStream_t stream);
+/* Host only: the workspace fp8_moe_route needs. */
+fp8bs_status fp8_moe_route_ws_size(int64_t T, int32_t E, size_t* bytes);
+
+/* ------------------------------------------------------------------------
+ * fp8_moe_route_backward -- gradient at the logits of
+ *     sum(weights * dweights) + dloss[0] loss[0] + dloss[1] loss[1]
+ * (the selection and the counts are constants, as is usual for this loss).
+ * experts, weights, counts, lse: fp8_moe_route's outputs; a token whose lse
+ * is -inf gets zeros and its logits are not read for their values.
+ * dweights : nullable fp32 [T][k] (fp8_moe_combine_backward's); entries of
+ *            slots without an expert are not read.
+ * dloss    : nullable device fp32 [2].  At least one of the two; experts and
+ *            weights are required with dweights, counts with dloss.
+ * dlogits  : [T][ld_d] of the logits' type (rounded once from fp32).
+ * Requirements: as fp8_moe_route; ld_d >= E; dlogits must not overlap logits.
+ * ------------------------------------------------------------------------ */
+fp8bs_status fp8_moe_route_backward(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k,
+                                    int32_t renorm, const int32_t* experts, const float* weights,
+                                    const int32_t* counts, const float* lse, const float* dweights,
+                                    const float* dloss, void* dlogits, int64_t ld_d, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_block_norm -- the norm behind a block, its gate and scale, the residual
+ * add, and the norm before the next block with its 1x128 quantization, in one
+ * pass.  With N(v; w) = v * rsqrt(mean(v^2) + eps) * w over each row:
+ *
+ *     h = residual + scale * gate * N(x; w_post)
+ *     y = N(h; w_pre);   q, s: y's 1x128 groups, S = max|y| / 448,
+ *                        q = E4M3(y / S) (RNE, saturating; S = 0 and codes 0
+ *                        for an all-zero group)
+ *
+ * ("per-token" activation groups: "Unified FP8: Beyond Mixed Precision...",
+ * section "FP8 Quantization").  Parts that are not given fall away: no
+ * residual (0), no x (h = residual), no w_post (x itself), no gate (1).
+ * fp32 throughout: h and y are each rounded once when stored, and y and its
+ * codes come from the unrounded h and y (so the codes are not those of
+ * fp8_quant_rowblock on the bf16 y, which rounds twice).  The quotient y / S
+ * is correct to one fp32 ulp before the E4M3 rounding.
+ *
+ * x        : nullable bf16 [rows][ld_x], the block's output.
+ * residual : nullable [rows][ld_r], bf16 or fp32 per stream_type.
+ * gate     : nullable bf16 [ceil(rows / rows_per_gate)][ld_gate]; row r is
+ *            gated by gate row r / rows_per_gate (1: a gate per token; the
+ *            sequence length: a gate per sequence; rows: one gate vector).
+ * w_post, w_pre : nullable [cols], bf16 or fp32 per w_type.
+ * h        : nullable [rows][ld_h], stream_type; may be `residual` itself
+ *            with the same leading dimension (updated in place).
+ * y        : nullable bf16 [rows][ld_y].
+ * q, s     : nullable together; codes [rows][ld_q], the scale of (row r,
+ *            group g) at s[r * s_stride_row + g * s_stride_group].
+ * Requirements: rows, cols >= 0, cols % 8 == 0, cols <= 32768, rows < 2^31;
+ * residual or x; w_post and gate only with x; y and q only with w_pre, and
+ * w_pre only with one of them; at least one output; eps > 0 and scale finite;
+ * leading dimensions >= cols and % 8 == 0; bf16, fp32 and weight pointers
+ * 16-byte aligned, q 8-byte, s 4-byte.  Inputs are expected to be finite with
+ * mean squares in fp32's range.
+ * ------------------------------------------------------------------------ */
+fp8bs_status fp8_block_norm(int64_t rows, int64_t cols, const uint16_t* x, int64_t ld_x,
+                            const void* residual, int64_t ld_r, fp8bs_out stream_type,
+                            const uint16_t* gate, int64_t ld_gate, int64_t rows_per_gate, float scale,
+                            const void* w_post, const void* w_pre, fp8bs_out w_type, float eps,
+                            void* h, int64_t ld_h, uint16_t* y, int64_t ld_y, uint8_t* q, int64_t ld_q,
+                            float* s, int64_t s_stride_row, int64_t s_stride_group, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_block_norm_backward -- gradient of fp8_block_norm's h and y (codes are
+ * not differentiated: straight through).  From dy = dL/dy, dh = the part of
+ * dL/dh that arrives past y, and the saved h and x:
+ *
+ *     r = rsqrt(mean(h^2) + eps), hh = h r, g = dy w_pre
+ *     dH = dh + r (g - hh mean(g hh));    dres = dH
+ *     dw_pre = sum over rows of dy hh
+ *     r' = rsqrt(mean(x^2) + eps), xh = x r', dn = scale gate dH
+ *     dx = r' (dn w_post - xh mean(dn w_post xh))   (dn without w_post)
+ *     dw_post = sum over rows of dn xh
+ *     dgate = sum over the gate row's rows of scale dH N(x; w_post)
+ *
+ * dy    : [rows][ld_dy], bf16 or fp32 per dy_type; with h and w_pre, or none
+ *         of the three.
+ * dh    : nullable [rows][ld_dh], stream_type.   h : [rows][ld_h], stream_type.
+ * x     : nullable: without it there was no branch (no dx, dgate, w_post,
+ *         gate).
+ * gate, rows_per_gate, scale, w_post, w_pre, w_type, eps : as in the forward.
+ * dx    : nullable bf16.   dres : nullable, stream_type; may be `dh` itself
+ *         with the same leading dimension.
+ * dgate : nullable [gate rows][ld_dgate], bf16 or fp32 per dgate_type.
+ * dw_post, dw_pre : nullable fp32 [cols]; written (not added to), zeros when
+ *         rows == 0.
+ * ws    : device workspace of fp8_block_norm_backward_ws_size bytes, 16-byte
+ *         aligned (nullable when that is 0); contents on entry are ignored.
+ *         Calls that overlap in time need separate workspaces.
+ * The sums have a fixed order: the results are the same bits every time.
+ * Requirements: as fp8_block_norm; dy or dh; at least one output; each of
+ * dgate, dw_post, dw_pre only with its gate or weight.
+ * ------------------------------------------------------------------------ */
+fp8bs_status fp8_block_norm_backward(int64_t rows, int64_t cols, const void* dy, int64_t ld_dy, fp8bs_out dy_type,
+                                     const void* dh, int64_t ld_dh, const void* h, int64_t ld_h,
+                                     fp8bs_out stream_type, const uint16_t* x, int64_t ld_x,
+                                     const uint16_t* gate, int64_t ld_gate, int64_t rows_per_gate, float scale,
+                                     const void* w_post, const void* w_pre, fp8bs_out w_type, float eps,
+                                     uint16_t* dx, int64_t ld_dx, void* dres, int64_t ld_dres,
+                                     void* dgate, int64_t ld_dgate, fp8bs_out dgate_type,
+                                     float* dw_post, float* dw_pre, void* ws, size_t ws_bytes, hipStream_t stream);
+/* Host only: the workspace for these sizes; the three flags say which of
+ * dw_post, dw_pre and dgate the call will write. */
+fp8bs_status fp8_block_norm_backward_ws_size(int64_t rows, int64_t cols, int64_t rows_per_gate, int32_t dw_post,
+                                             int32_t dw_pre, int32_t dgate, size_t* bytes);
 
 /* ------------------------------------------------------------------------
  * fp8_quant_pow2 / fp8_blockscaled_gemm_pow2 -- the block-wise recipe with
