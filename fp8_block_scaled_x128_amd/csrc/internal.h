@@ -90,6 +90,7 @@ struct NormBwdArgs {
 // partials lie at the three offsets (in floats) of the workspace.
 struct NormBwdPlan {
     int wpr, nv;
+    bool grouped, by_wave;
     int32_t slots;
     int64_t units, splits, chunk, unit_rows, groups;
     size_t off_pre, off_post, off_gate, ws_floats;
@@ -107,7 +108,7 @@ struct RouteArgs {
     int32_t* experts; float* weights; int32_t* counts; int32_t* offsets; int32_t* row_token; int32_t* token_rows;
     float* lse; float* loss;
 };
-struct RouteWs { int32_t* hist; float* psum; float* lse2; int32_t* live; float* total; };
+struct RouteWs { int32_t epad; uint8_t* hist; float* psum; float* lse2; int32_t* live; int32_t* base; float* total; };
 size_t route_ws_bytes(int64_t T, int32_t E);
 hipError_t launch_moe_route(const RouteArgs& p, void* ws, hipStream_t st);
 

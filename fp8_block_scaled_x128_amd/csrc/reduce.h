@@ -13,7 +13,9 @@ namespace fp8bs {
 // lanes it has joined hold the same value, so the four make an all-reduce.
 template <int CTRL>
 __device__ __forceinline__ uint32_t dpp_mov(uint32_t v) {
-    return (uint32_t)__builtin_amdgcn_update_dpp((int)v, (int)v, CTRL, 0xf, 0xf, false);
+    // every source lane exists, so the bound control never matters; with it
+    // set the compiler folds the move into the operation that follows
+    return (uint32_t)__builtin_amdgcn_mov_dpp((int)v, CTRL, 0xf, 0xf, true);
 }
 constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
 
@@ -51,32 +53,32 @@ __device__ __forceinline__ uint32_t row16_umin(uint32_t v) {
     return v;
 }
 
-// All-reduce over LANES lanes (16: a DPP row, 64: the wave).
+// All-reduce over LANES lanes (16: a DPP row, 64: the wave).  The four rows of
+// a wave meet in scalar registers: no LDS crossbar, and the result is uniform.
+// Every lane of the wave must be active.
+__device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);
+}
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
     v = row16_sum(v);
     if (LANES == 64) {
-        v += __shfl_xor(v, 16, 64);
-        v += __shfl_xor(v, 32, 64);
+        const uint32_t u = __float_as_uint(v);
+        v = (__uint_as_float(lane_value(u, 0)) + __uint_as_float(lane_value(u, 16))) +
+            (__uint_as_float(lane_value(u, 32)) + __uint_as_float(lane_value(u, 48)));
     }
     return v;
 }
 template <int LANES>
 __device__ __forceinline__ uint32_t lanes_umax(uint32_t v) {
     v = row16_umax(v);
-    if (LANES == 64) {
-        v = max(v, (uint32_t)__shfl_xor((int)v, 16, 64));
-        v = max(v, (uint32_t)__shfl_xor((int)v, 32, 64));
-    }
+    if (LANES == 64) v = max(max(lane_value(v, 0), lane_value(v, 16)), max(lane_value(v, 32), lane_value(v, 48)));
     return v;
 }
 template <int LANES>
 __device__ __forceinline__ uint32_t lanes_umin(uint32_t v) {
     v = row16_umin(v);
-    if (LANES == 64) {
-        v = min(v, (uint32_t)__shfl_xor((int)v, 16, 64));
-        v = min(v, (uint32_t)__shfl_xor((int)v, 32, 64));
-    }
+    if (LANES == 64) v = min(min(lane_value(v, 0), lane_value(v, 16)), min(lane_value(v, 32), lane_value(v, 48)));
     return v;
 }
 

@@ -32,10 +32,23 @@ __device__ __forceinline__ float key_logit(uint32_t k) {
 }
 constexpr uint32_t kKeyNegInf = 0x007fffffu;
 
-template <bool F32>
-__device__ __forceinline__ float load_logit(const void* z, int64_t i) {
-    if (F32) return static_cast<const float*>(z)[i];
-    return __uint_as_float((uint32_t)static_cast<const uint16_t*>(z)[i] << 16);
+// A lane's logits l, l + L, ... of the row that starts at element `row`.  No
+// load is conditional (past the row: the last expert's, dropped by the
+// caller), so all are in flight at once.
+template <int L, int V, bool F32>
+__device__ __forceinline__ void load_logits(const void* base, int64_t row, int l, int E, float (&z)[V]) {
+    if (F32) {
+        const float* r = static_cast<const float*>(base) + row;
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = r[min(l + i * L, E - 1)];
+    } else {
+        const uint16_t* r = static_cast<const uint16_t*>(base) + row;
+        uint16_t w[V];
+#pragma unroll
+        for (int i = 0; i < V; ++i) w[i] = r[min(l + i * L, E - 1)];
+#pragma unroll
+        for (int i = 0; i < V; ++i) z[i] = __uint_as_float((uint32_t)w[i] << 16);
+    }
 }
 
 // Exclusive prefix of counts[0..E) into LDS, by the first wave; E <= 1024.
@@ -58,93 +71,105 @@ __device__ __forceinline__ void scan_experts(const int* counts, int* excl, int E
     }
 }
 
-// Sum of one value per thread over the workgroup, in a fixed order (all
-// threads call; the result is valid in thread 0).
-__device__ __forceinline__ float block_sum(float v, float* lds) {
-    v = lanes_sum<64>(v);
+// Sums of K values per thread over the 16 waves of a workgroup, in a fixed
+// order (all threads call; lds holds 16 K floats; every thread has the result).
+template <int K>
+__device__ __forceinline__ void block_sums(float (&v)[K], float* lds) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = lanes_sum<64>(v[i]);
+    if ((threadIdx.x & 63) == 0) {
+#pragma unroll
+        for (int i = 0; i < K; ++i) lds[16 * i + (threadIdx.x >> 6)] = v[i];
+    }
     __syncthreads();
-    if ((threadIdx.x & 63) == 0) lds[threadIdx.x >> 6] = v;
-    __syncthreads();
-    float s = 0.0f;
-    if (threadIdx.x == 0)
-        for (int w = 0; w < (int)(blockDim.x >> 6); ++w) s += lds[w];
-    return s;
+#pragma unroll
+    for (int i = 0; i < K; ++i) v[i] = row16_sum(lds[16 * i + (threadIdx.x & 15)]);
 }
+
+// LDS of a selecting workgroup: the experts' token masks, and the probability
+// sums of half of its waves [8][E] (the halves take turns: 1024 experts would
+// pass 64 KB otherwise).
+constexpr int kHalf = kThreads / 128;
+__host__ __device__ constexpr size_t select_lds(int E) { return (size_t)E * (8 + 4 * kHalf); }
 
 // Selection.  L lanes hold a token's logits, lane l the experts l, l + L, ...
 // Each of the k rounds takes the largest key among the lanes and, of equal
-// keys, the lowest expert.  The workgroup's 64 tokens leave in LDS, per
-// expert, the mask of the tokens that chose it: the histogram is its
-// population count, and a slot's rank among earlier tokens that of the bits
-// below it, so the stable (expert, token) order needs no sort.
+// keys, the lowest expert; lane j keeps slot j (and slot j + L).  The
+// workgroup's 64 tokens leave in LDS, per expert, the mask of the tokens that
+// chose it: the histogram is its population count, and a slot's rank among
+// earlier tokens that of the bits below it, so the stable (expert, token)
+// order needs no sort.  On return psum[0..E) holds the probability sums, and
+// {sum of lse^2, routed tokens} are returned to every thread.
 template <int L, int V, bool F32>
-__device__ __forceinline__ void select_tokens(const RouteArgs& p, int64_t t0, unsigned long long* mask,
-                                              float* psum, float* s_lse2, int* s_live) {
+__device__ __forceinline__ float2 select_tokens(const RouteArgs& p, int64_t t0, unsigned long long* mask, float* psum) {
     constexpr int kGroups = kThreads / L;
+    __shared__ float red[32];
     const int l = threadIdx.x % L, grp = threadIdx.x / L;
     float acc[V];
 #pragma unroll
     for (int i = 0; i < V; ++i) acc[i] = 0.0f;
-    float lse2 = 0.0f;
-    int live_n = 0;
+    float sums[2] = {0.0f, 0.0f};                   // lse^2, tokens: in lane 0 of a group
     for (int tt = grp; tt < kTok; tt += kGroups) {
         const int64_t t = t0 + tt;
+        if (t0 + tt - grp % (64 / L) >= p.T) break;   // no lane of the wave has a token
+        float z[V];
+        load_logits<L, V, F32>(p.logits, min(t, p.T - 1) * p.ld, l, p.E, z);
         const bool have = t < p.T && (!p.mask || p.mask[t]);
-        uint32_t key[V];
-#pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const int e = l + i * L;
-            key[i] = 0;
-            if (have && e < p.E) key[i] = logit_key(load_logit<F32>(p.logits, t * p.ld + e));
-        }
         uint32_t left[V];
         uint32_t best = 0;
 #pragma unroll
-        for (int i = 0; i < V; ++i) { left[i] = key[i]; best = max(best, key[i]); }
+        for (int i = 0; i < V; ++i) {
+            left[i] = (have && l + i * L < p.E) ? logit_key(z[i]) : 0u;
+            best = max(best, left[i]);
+        }
         const uint32_t top = lanes_umax<L>(best);
         const bool live = top > kKeyNegInf;
         const float m = live ? key_logit(top) : 0.0f;
         float ex[V], sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            ex[i] = key[i] ? __builtin_amdgcn_exp2f((key_logit(key[i]) - m) * kLog2e) : 0.0f;
+            const float v = __builtin_amdgcn_exp2f((z[i] - m) * kLog2e);
+            ex[i] = left[i] ? v : 0.0f;
             sum += ex[i];
         }
         sum = lanes_sum<L>(sum);
-        const float lse = live ? m + logf(sum) : -INFINITY;
-        float wsel = 0.0f, wnorm = 0.0f;            // lane j holds slot j's weight (slots past L: in turn)
-        int esel = -1;
-        float wsel2 = 0.0f;
-        int esel2 = -1;
+        uint32_t ksel[2] = {0, 0}, esel[2] = {0, 0};
+        uint32_t mx = top;
         for (int j = 0; j < p.k; ++j) {
-            uint32_t b = 0;
+            if (j > 0) {
+                best = 0;
 #pragma unroll
-            for (int i = 0; i < V; ++i) b = max(b, left[i]);
-            const uint32_t mx = lanes_umax<L>(b);
-            uint32_t at = 0xffffffffu;
-#pragma unroll
-            for (int i = V - 1; i >= 0; --i) at = left[i] == mx ? (uint32_t)(l + i * L) : at;
-            at = lanes_umin<L>(at);
-            const bool ok = mx > kKeyNegInf;
-#pragma unroll
-            for (int i = 0; i < V; ++i) left[i] = (uint32_t)(l + i * L) == at ? 0u : left[i];
-            const float w = ok ? __builtin_amdgcn_exp2f((key_logit(mx) - m) * kLog2e) : 0.0f;
-            wnorm += w;
-            if (l == (j % L)) {
-                if (j < L) { wsel = w; esel = ok ? (int)at : -1; }
-                else { wsel2 = w; esel2 = ok ? (int)at : -1; }
+                for (int i = 0; i < V; ++i) best = max(best, left[i]);
+                mx = lanes_umax<L>(best);
             }
-            if (ok && l == 0) atomicOr(&mask[at], 1ull << tt);
+            uint32_t at = 0x10000u;
+#pragma unroll
+            for (int i = V - 1; i >= 0; --i) at = left[i] == mx ? (uint32_t)(i * L) : at;
+            at = lanes_umin<L>(at + l);
+            const uint32_t mine = at - l;
+#pragma unroll
+            for (int i = 0; i < V; ++i) left[i] = mine == (uint32_t)(i * L) ? 0u : left[i];
+            if (l == j) { ksel[0] = mx; esel[0] = at; }
+            if (l + L == j) { ksel[1] = mx; esel[1] = at; }
         }
-        const float norm = p.renorm ? wnorm : sum;
+        float w[2], wsum = 0.0f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            w[u] = ksel[u] > kKeyNegInf ? __builtin_amdgcn_exp2f((key_logit(ksel[u]) - m) * kLog2e) : 0.0f;
+            wsum += w[u];
+        }
+        const float norm = p.renorm ? lanes_sum<L>(wsum) : sum;
+        const float lse = live ? m + logf(sum) : -INFINITY;
         if (t < p.T) {
-            if (l < p.k) {
-                p.experts[t * p.k + l] = esel;
-                p.weights[t * p.k + l] = esel >= 0 ? wsel / norm : 0.0f;
-            }
-            if (l + L < p.k) {
-                p.experts[t * p.k + l + L] = esel2;
-                p.weights[t * p.k + l + L] = esel2 >= 0 ? wsel2 / norm : 0.0f;
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int j = l + u * L;
+                if (j < p.k) {
+                    const bool ok = ksel[u] > kKeyNegInf;
+                    p.experts[t * p.k + j] = ok ? (int)esel[u] : -1;
+                    p.weights[t * p.k + j] = ok ? w[u] / norm : 0.0f;
+                    if (ok) atomicOr(&mask[esel[u]], 1ull << tt);
+                }
             }
             if (l == 0) p.lse[t] = lse;
         }
@@ -152,53 +177,53 @@ __device__ __forceinline__ void select_tokens(const RouteArgs& p, int64_t t0, un
             const float inv = 1.0f / sum;
 #pragma unroll
             for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(ex[i], inv, acc[i]);
-            lse2 = __builtin_fmaf(lse, lse, lse2);
-            live_n++;
+            if (l == 0) {
+                sums[0] = __builtin_fmaf(lse, lse, sums[0]);
+                sums[1] += 1.0f;
+            }
         }
     }
-    // per-expert probability sums of the workgroup: the 64 / L groups of a
-    // wave by shuffles, then the waves in order through LDS
+    // the 64 / L groups of a wave by shuffles, waves w and w + 8, then those in
+    // order
+    const int wave = threadIdx.x >> 6;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         if (L == 16) {
             acc[i] += __shfl_xor(acc[i], 16, 64);
             acc[i] += __shfl_xor(acc[i], 32, 64);
         }
+        const int e = l + i * L;
+        if (wave >= kHalf && (threadIdx.x & 63) < L && e < p.E) psum[(wave - kHalf) * p.E + e] = acc[i];
     }
-    for (int w = 0; w < kThreads / 64; ++w) {
-        __syncthreads();
-        if ((int)(threadIdx.x >> 6) == w && (threadIdx.x & 63) < L) {
-#pragma unroll
-            for (int i = 0; i < V; ++i) {
-                const int e = l + i * L;
-                if (e < p.E) psum[e] = (w ? psum[e] : 0.0f) + acc[i];
-            }
-        }
-    }
-    // lane 0 of every group holds its tokens' lse^2 and count
-    float v[2] = {l == 0 ? lse2 : 0.0f, l == 0 ? (float)live_n : 0.0f};
-    const float a = block_sum(v[0], s_lse2), b = block_sum(v[1], s_lse2);
-    if (threadIdx.x == 0) { s_lse2[0] = a; *s_live = (int)b; }
     __syncthreads();
+#pragma unroll
+    for (int i = 0; i < V; ++i) {
+        const int e = l + i * L;
+        if (wave < kHalf && (threadIdx.x & 63) < L && e < p.E) psum[wave * p.E + e] += acc[i];
+    }
+    block_sums(sums, red);                          // its barrier covers psum and mask too
+    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+        float s = 0.0f;
+#pragma unroll
+        for (int w = 0; w < kHalf; ++w) s += psum[w * p.E + e];
+        psum[e] = s;                                // column e is this thread's alone
+    }
+    return make_float2(sums[0], sums[1]);
 }
 
-// The rows of a workgroup's tokens, given in LDS the first row of each expert
-// for them, and the zeros of row_token behind the last row.
-__device__ __forceinline__ void place_rows(const RouteArgs& p, int64_t t0, const unsigned long long* mask,
-                                           const int* base, int total) {
-    const int64_t n = min((int64_t)kTok, p.T - t0) * p.k;
-    for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-        const int64_t at = t0 * p.k + i;
-        const int tt = (int)(i / p.k);
-        const int e = p.experts[at];
-        int row = -1;
-        if (e >= 0) {
-            row = base[e] + __popcll(mask[e] & ((1ull << tt) - 1));
-            p.row_token[row] = (int32_t)(t0 + tt);
-        }
-        p.token_rows[at] = row;
-        if (at >= total) p.row_token[at] = 0;
+// The rows of a workgroup's tokens, given in LDS the masks and the first row
+// of each expert for them, and the zeros of row_token behind the last row.
+__device__ __forceinline__ void place_row(const RouteArgs& p, int64_t t0, int64_t i, int e,
+                                          const unsigned long long* mask, const int* base, int total) {
+    const int64_t at = t0 * p.k + i;
+    const int tt = (int)((uint32_t)i / (uint32_t)p.k);
+    int row = -1;
+    if (e >= 0) {
+        row = base[e] + __popcll(mask[e] & ((1ull << tt) - 1));
+        p.row_token[row] = (int32_t)(t0 + tt);
     }
+    p.token_rows[at] = row;
+    if (at >= total) p.row_token[at] = 0;
 }
 
 __device__ __forceinline__ void write_losses(const RouteArgs& p, float fp, float lse2, int64_t sum_counts, int live) {
@@ -213,132 +238,268 @@ __global__ void __launch_bounds__(kThreads) k_route_one(RouteArgs p) {
     extern __shared__ __align__(16) unsigned char dyn[];
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(dyn);
     float* psum = reinterpret_cast<float*>(mask + p.E);
-    int* counts = reinterpret_cast<int*>(psum + p.E);
+    int* counts = reinterpret_cast<int*>(psum + p.E * kHalf);
     int* base = counts + p.E;                       // [E + 1]
-    __shared__ float red[kThreads / 64];
-    __shared__ int s_live;
+    __shared__ float red[16];
     for (int e = threadIdx.x; e < p.E; e += kThreads) mask[e] = 0;
     __syncthreads();
-    select_tokens<L, V, F32>(p, 0, mask, psum, red, &s_live);
-    const float lse2 = red[0];
-    const int live = s_live;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) counts[e] = __popcll(mask[e]);
-    __syncthreads();
+    const float2 s = select_tokens<L, V, F32>(p, 0, mask, psum);
+    float f[1] = {0.0f};
+    for (int e = threadIdx.x; e < p.E; e += kThreads) {
+        const int c = __popcll(mask[e]);
+        counts[e] = c;
+        p.counts[e] = c;
+        f[0] = __builtin_fmaf((float)c, psum[e], f[0]);
+    }
+    block_sums(f, red);                             // its barrier covers counts too
     scan_experts(counts, base, p.E);
     __syncthreads();
-    float f = 0.0f;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
-        p.counts[e] = counts[e];
-        p.offsets[e] = base[e];
-        f = __builtin_fmaf((float)counts[e], psum[e], f);
-    }
-    place_rows(p, 0, mask, base, base[p.E]);
-    f = block_sum(f, red);
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = base[e];
+    for (int64_t i = threadIdx.x; i < p.T * p.k; i += kThreads)
+        place_row(p, 0, i, p.experts[i], mask, base, base[p.E]);
     if (threadIdx.x == 0) {
-        p.counts[p.E] = live;
-        p.offsets[p.E] = base[p.E];
-        write_losses(p, f, lse2, base[p.E], live);
+        p.counts[p.E] = (int)s.y;
+        write_losses(p, f[0], s.x, base[p.E], (int)s.y);
     }
 }
 
-// More tokens, first launch: selection, and per workgroup the histogram, the
-// probability sums and the loss terms.
+// More tokens, first launch: selection, and per workgroup the histogram (a
+// byte per expert: at most 64), the probability sums and the loss terms.
 template <int L, int V, bool F32>
 __global__ void __launch_bounds__(kThreads) k_route_select(RouteArgs p, RouteWs ws) {
     extern __shared__ __align__(16) unsigned char dyn[];
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(dyn);
     float* psum = reinterpret_cast<float*>(mask + p.E);
-    __shared__ float red[kThreads / 64];
-    __shared__ int s_live;
     for (int e = threadIdx.x; e < p.E; e += kThreads) mask[e] = 0;
     __syncthreads();
-    select_tokens<L, V, F32>(p, (int64_t)blockIdx.x * kTok, mask, psum, red, &s_live);
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
-        ws.hist[(int64_t)blockIdx.x * p.E + e] = __popcll(mask[e]);
-        ws.psum[(int64_t)blockIdx.x * p.E + e] = psum[e];
+    const float2 s = select_tokens<L, V, F32>(p, (int64_t)blockIdx.x * kTok, mask, psum);
+    for (int e = threadIdx.x; e < ws.epad; e += kThreads) {
+        ws.hist[(int64_t)blockIdx.x * ws.epad + e] = e < p.E ? (uint8_t)__popcll(mask[e]) : (uint8_t)0;
+        ws.psum[(int64_t)blockIdx.x * ws.epad + e] = e < p.E ? psum[e] : 0.0f;
     }
     if (threadIdx.x == 0) {
-        ws.lse2[blockIdx.x] = red[0];
-        ws.live[blockIdx.x] = s_live;
+        ws.lse2[blockIdx.x] = s.x;
+        ws.live[blockIdx.x] = (int)s.y;
     }
 }
 
-// Second launch: per expert, the running row count over the workgroups (in
-// place of the histogram) and the sum of the probabilities.  One wave per
-// expert.
-__global__ void __launch_bounds__(256) k_route_scan(RouteArgs p, RouteWs ws, int nblk) {
-    const int e = blockIdx.x * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;
-    if (e >= p.E) return;
-    int carry = 0;
-    float s = 0.0f;
-    for (int b0 = 0; b0 < nblk; b0 += 64) {
-        const int b = b0 + lane;
-        const int c = b < nblk ? ws.hist[(int64_t)b * p.E + e] : 0;
-        if (b < nblk) s += ws.psum[(int64_t)b * p.E + e];
-        int v = c;
+// Histogram bytes of 16 experts as 16-bit sums, two to a word: word 2 i + h
+// holds experts 4 i + h and 4 i + h + 2.
+__device__ __forceinline__ void add_bytes(uint32_t (&a)[8], const uint4 v) {
+    const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        a[2 * i] += w[i] & 0x00ff00ffu;
+        a[2 * i + 1] += (w[i] >> 8) & 0x00ff00ffu;
+    }
+}
+
+// Second launch, up to kDirect workgroups of tokens: every workgroup adds the
+// histograms of all workgroups and of those before it (32 KB from the L2 at
+// 16384 tokens and 128 experts), scans the counts over the experts and places
+// its tokens' rows; one more workgroup forms the counts, offsets and losses.
+// Sums of at most 512 x 64 fit 16 bits.
+constexpr int kDirect = 512;
+__global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs ws, int nblk) {
+    extern __shared__ __align__(16) unsigned char dyn[];
+    const int epad = ws.epad, nch = epad >> 4;      // chunks of 16 experts: a power of two, at most 64
+    unsigned long long* mask = reinterpret_cast<unsigned long long*>(dyn);
+    int* counts = reinterpret_cast<int*>(mask + epad);
+    int* base = counts + epad;                      // [epad + 1], then the waves' sums
+    uint32_t* part = reinterpret_cast<uint32_t*>(base + epad + 4);     // [8 waves][nch][16]
+    // the workgroup without tokens goes first: it has the longest way
+    const int blk = (int)blockIdx.x - 1;
+    const int64_t t0 = (int64_t)blk * kTok;
+    const bool tokens = blk >= 0;
+    const int n = tokens ? (int)min((int64_t)kTok, p.T - t0) * p.k : 0;
+    int es[2];
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int i = threadIdx.x + u * kThreads;
+        es[u] = i < n ? p.experts[t0 * p.k + i] : -1;
+    }
+    uint32_t tot[8], pre[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) tot[i] = pre[i] = 0;
+    const int ch = threadIdx.x & (nch - 1), rows = kThreads / nch;
+    for (int b = threadIdx.x / nch; b < nblk; b += rows) {
+        const uint4 v = *reinterpret_cast<const uint4*>(ws.hist + (int64_t)b * epad + 16 * ch);
+        add_bytes(tot, v);
+        if (b < blk) add_bytes(pre, v);
+    }
+    for (int e = threadIdx.x; e < epad; e += kThreads) mask[e] = 0;
+    for (int d = nch; d < 64; d <<= 1) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            tot[i] += (uint32_t)__shfl_xor((int)tot[i], d, 64);
+            pre[i] += (uint32_t)__shfl_xor((int)pre[i], d, 64);
+        }
+    }
+    const int wave = threadIdx.x >> 6;
+    uint32_t* dst = part + ((wave & (kHalf - 1)) * nch + ch) * 16;
+    if (wave >= kHalf && (int)(threadIdx.x & 63) < nch) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) { dst[i] = tot[i]; dst[8 + i] = pre[i]; }
+    }
+    __syncthreads();
+    if (wave < kHalf && (int)(threadIdx.x & 63) < nch) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) { dst[i] += tot[i]; dst[8 + i] += pre[i]; }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+        if (es[u] >= 0) atomicOr(&mask[es[u]], 1ull << ((uint32_t)(threadIdx.x + u * kThreads) / (uint32_t)p.k));
+    int before = 0;
+    if ((int)threadIdx.x < epad) {
+        const int e = threadIdx.x, i = e & 15;
+        const int word = 2 * (i >> 2) + (i & 1), sh = (i & 2) * 8;
+        int c = 0;
+        for (int w = 0; w < kHalf; ++w) {
+            const uint32_t* src = part + (w * nch + (e >> 4)) * 16;
+            c += (int)((src[word] >> sh) & 0xffffu);
+            before += (int)((src[8 + word] >> sh) & 0xffffu);
+        }
+        counts[e] = c;
+    }
+    __syncthreads();
+    scan_experts(counts, base, p.E);
+    __syncthreads();
+    const int total = base[p.E];
+    if (tokens) {
+        __syncthreads();
+        if ((int)threadIdx.x < p.E) base[threadIdx.x] += before;
+        __syncthreads();
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int i = threadIdx.x + u * kThreads;
+            if (i < n) place_row(p, t0, i, es[u], mask, base, total);
+        }
+        return;
+    }
+    __shared__ float red[48];
+    float s[3] = {0.0f, 0.0f, 0.0f};                // counts . probabilities, lse^2, tokens (at most 2^15)
+    // four experts per thread, every (4096 / epad)-th workgroup's
+    const int e4 = (threadIdx.x * 4) & (epad - 1), prows = kThreads * 4 / epad;
+    const float c0 = (float)counts[e4], c1 = (float)counts[e4 + 1], c2 = (float)counts[e4 + 2], c3 = (float)counts[e4 + 3];
+#pragma unroll 8
+    for (int b = threadIdx.x * 4 / epad; b < nblk; b += prows) {
+        const float4 v = *reinterpret_cast<const float4*>(ws.psum + (int64_t)b * epad + e4);
+        s[0] += __builtin_fmaf(c0, v.x, c1 * v.y) + __builtin_fmaf(c2, v.z, c3 * v.w);
+    }
+    for (int b = threadIdx.x; b < nblk; b += kThreads) { s[1] += ws.lse2[b]; s[2] += (float)ws.live[b]; }
+    block_sums(s, red);
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) {
+        p.offsets[e] = base[e];
+        p.counts[e] = e < p.E ? counts[e] : (int)s[2];
+    }
+    if (threadIdx.x == 0) write_losses(p, s[0], s[1], total, (int)s[2]);
+}
+
+// More workgroups than that, second launch: for 16 experts, the running row
+// count over the workgroups and the sums of counts and probabilities.  Every
+// thread takes a run of workgroups, twice: for its sums, and after their scan
+// over the threads for the counts before each.
+__global__ void __launch_bounds__(kThreads) k_route_scan(RouteArgs p, RouteWs ws, int nblk) {
+    __shared__ int lds[kThreads / 64][16];
+    __shared__ float ldp[16][kThreads / 16 + 1];
+    const int per = (nblk + kThreads - 1) / kThreads, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int b0 = min((int)threadIdx.x * per, nblk), b1 = min(b0 + per, nblk);
+    const uint8_t* src = ws.hist + 16 * blockIdx.x;
+    int sum[16], run[16];
+#pragma unroll
+    for (int i = 0; i < 16; ++i) sum[i] = 0;
+#pragma unroll 2
+    for (int b = b0; b < b1; ++b) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + (int64_t)b * ws.epad);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+        for (int i = 0; i < 16; ++i) sum[i] += (int)((w[i >> 2] >> (8 * (i & 3))) & 0xffu);
+    }
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        run[i] = sum[i];
 #pragma unroll
         for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(v, d, 64);
-            if (lane >= d) v += o;
+            const int o = __shfl_up(run[i], d, 64);
+            if (lane >= d) run[i] += o;
         }
-        if (b < nblk) ws.hist[(int64_t)b * p.E + e] = carry + v - c;
-        carry += __shfl(v, 63, 64);
+        if (lane == 63) lds[wave][i] = run[i];
     }
-    s = lanes_sum<64>(s);
-    if (lane == 0) {
-        p.counts[e] = carry;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 16; ++i) {
+        int before = 0, all = 0;
+        for (int w = 0; w < kThreads / 64; ++w) {
+            if (w < wave) before += lds[w][i];
+            all += lds[w][i];
+        }
+        run[i] += before - sum[i];
+        const int e = 16 * blockIdx.x + i;
+        if (threadIdx.x == 0 && e < p.E) p.counts[e] = all;
+    }
+#pragma unroll 2
+    for (int b = b0; b < b1; ++b) {
+        const uint4 v = *reinterpret_cast<const uint4*>(src + (int64_t)b * ws.epad);
+        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+        int4* dst = reinterpret_cast<int4*>(ws.base + (int64_t)b * ws.epad + 16 * blockIdx.x);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) dst[i] = make_int4(run[4 * i], run[4 * i + 1], run[4 * i + 2], run[4 * i + 3]);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) run[i] += (int)((w[i >> 2] >> (8 * (i & 3))) & 0xffu);
+    }
+    // probabilities: thread (e, r) adds every 64th workgroup's, then e's threads in order
+    const int e = 16 * blockIdx.x + (threadIdx.x & 15);
+    float f = 0.0f;
+    if (e < p.E)
+        for (int b = threadIdx.x >> 4; b < nblk; b += kThreads / 16) f += ws.psum[(int64_t)b * ws.epad + e];
+    ldp[threadIdx.x & 15][threadIdx.x >> 4] = f;
+    __syncthreads();
+    if (threadIdx.x < 16 && e < p.E) {
+        float s = 0.0f;
+        for (int r = 0; r < kThreads / 16; ++r) s += ldp[threadIdx.x][r];
         ws.total[e] = s;
     }
 }
 
-// Third launch: every workgroup scans the counts over the experts and places
-// its tokens' rows; one more forms the losses.
-__global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs ws, int nblk) {
+// ... and third launch: as k_route_place from the scanned counts.
+__global__ void __launch_bounds__(kThreads) k_route_place_scanned(RouteArgs p, RouteWs ws, int nblk) {
     extern __shared__ __align__(16) unsigned char dyn[];
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(dyn);
     int* counts = reinterpret_cast<int*>(mask + p.E);
     int* base = counts + p.E;                       // [E + 1]
-    __shared__ float red[kThreads / 64];
+    __shared__ float red[32];
+    __shared__ int s_live;
+    const int64_t t0 = (int64_t)blockIdx.x * kTok;
+    const bool tokens = (int)blockIdx.x < nblk;
+    const int n = tokens ? (int)min((int64_t)kTok, p.T - t0) * p.k : 0;
     for (int e = threadIdx.x; e < p.E; e += kThreads) { mask[e] = 0; counts[e] = p.counts[e]; }
+    if (threadIdx.x == 0) s_live = 0;
     __syncthreads();
     scan_experts(counts, base, p.E);
-    const int64_t t0 = (int64_t)blockIdx.x * kTok;
-    if ((int)blockIdx.x < nblk) {
-        const int64_t n = min((int64_t)kTok, p.T - t0) * p.k;
-        for (int64_t i = threadIdx.x; i < n; i += kThreads) {
-            const int e = p.experts[t0 * p.k + i];
-            if (e >= 0) atomicOr(&mask[e], 1ull << (int)(i / p.k));
-        }
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+        const int e = p.experts[t0 * p.k + i];
+        if (e >= 0) atomicOr(&mask[e], 1ull << ((uint32_t)i / (uint32_t)p.k));
     }
     __syncthreads();
     const int total = base[p.E];
-    if ((int)blockIdx.x < nblk) {
+    if (tokens) {
         __syncthreads();
-        for (int e = threadIdx.x; e < p.E; e += kThreads) base[e] += ws.hist[(int64_t)blockIdx.x * p.E + e];
+        if ((int)threadIdx.x < p.E) base[threadIdx.x] += ws.base[(int64_t)blockIdx.x * ws.epad + threadIdx.x];
         __syncthreads();
-        place_rows(p, t0, mask, base, total);
+        for (int i = threadIdx.x; i < n; i += kThreads) place_row(p, t0, i, p.experts[t0 * p.k + i], mask, base, total);
         return;
     }
-    float f = 0.0f, l2 = 0.0f, lv = 0.0f;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) {
-        f = __builtin_fmaf((float)counts[e], ws.total[e], f);
-        p.offsets[e] = base[e];
-    }
+    float s[2] = {0.0f, 0.0f};
     int live = 0;
-    for (int b = threadIdx.x; b < nblk; b += kThreads) { l2 += ws.lse2[b]; live += ws.live[b]; }
-    f = block_sum(f, red);
-    l2 = block_sum(l2, red);
-    // token counts below 2^24 a thread and 2^31 in all: summed as integers
-    __shared__ int s_live;
-    if (threadIdx.x == 0) s_live = 0;
-    __syncthreads();
-    atomicAdd(&s_live, live);
-    __syncthreads();
-    (void)lv;
+    for (int e = threadIdx.x; e < p.E; e += kThreads) s[0] = __builtin_fmaf((float)counts[e], ws.total[e], s[0]);
+    for (int b = threadIdx.x; b < nblk; b += kThreads) { s[1] += ws.lse2[b]; live += ws.live[b]; }
+    atomicAdd(&s_live, live);                       // whole numbers: any order gives the same
+    block_sums(s, red);                             // its barrier covers s_live too
+    for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = base[e];
     if (threadIdx.x == 0) {
-        p.offsets[p.E] = total;
         p.counts[p.E] = s_live;
-        write_losses(p, f, l2, total, s_live);
+        write_losses(p, s[0], s[1], total, s_live);
     }
 }
 
@@ -347,93 +508,102 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
 //   weights      renormalized: w_j (dw_j - sum_i w_i dw_i) at the selected;
 //                else p_te (dw_e [selected] - sum_i w_i dw_i)
 // L lanes hold a token; the selected slots' part meets the experts' lanes
-// through one LDS row per token.
+// through one LDS row per token.  Latency-bound at these sizes: everything a
+// token needs is loaded before the first use of any of it.
 template <int L, int V, bool F32>
 __global__ void __launch_bounds__(256) k_route_bwd(RouteBwdArgs p) {
     extern __shared__ __align__(16) unsigned char dyn[];
     constexpr int kGroups = 256 / L;
     const int l = threadIdx.x % L, grp = threadIdx.x / L;
     float* part = reinterpret_cast<float*>(dyn) + (int64_t)grp * (L * V);
-    float f[V];
-    float fsum = 0.0f;
+    float f[V], fsum = 0.0f;
 #pragma unroll
     for (int i = 0; i < V; ++i) {
         const int e = l + i * L;
         f[i] = (p.dloss && e < p.E) ? (float)p.counts[e] : 0.0f;
+        fsum += f[i];
         part[e] = 0.0f;
     }
-    // counts are whole numbers: their sum is exact below 2^24 and rounded once above
-    for (int e = l; p.dloss && e < p.E; e += L) fsum += (float)p.counts[e];
-    fsum = lanes_sum<L>(fsum);
     float gb = 0.0f, gz = 0.0f;
     if (p.dloss) {
         const float n = (float)max(p.counts[p.E], 1);
         gb = p.dloss[0] * (float)p.E / n;
         gz = 2.0f * p.dloss[1] / n;
     }
+    fsum = lanes_sum<L>(fsum);
     const float finv = 1.0f / fmaxf(fsum, 1.0f);
 #pragma unroll
     for (int i = 0; i < V; ++i) f[i] *= finv;
-    for (int64_t t = (int64_t)blockIdx.x * kGroups + grp; t < p.T; t += (int64_t)gridDim.x * kGroups) {
+    const int64_t step = (int64_t)gridDim.x * kGroups;
+    // whole waves take part while any of their tokens is left: the reductions
+    // need all lanes
+    for (int64_t t1 = (int64_t)blockIdx.x * kGroups; t1 < p.T; t1 += step) {
+        const bool have = t1 + grp < p.T;
+        const int64_t t = have ? t1 + grp : p.T - 1;
         const float lse = p.lse[t];
+        float z[V];
+        load_logits<L, V, F32>(p.logits, t * p.ld, l, p.E, z);
+        float w[2] = {0.0f, 0.0f}, dw[2] = {0.0f, 0.0f};
+        int es[2] = {-1, -1};
+        if (p.dweights) {
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int j = l + u * L;
+                if (j < p.k) {
+                    es[u] = p.experts[t * p.k + j];
+                    w[u] = p.weights[t * p.k + j];
+                    dw[u] = p.dweights[t * p.k + j];
+                }
+            }
+        }
         const bool live = !(lse == -INFINITY);
         // p from the largest logit and the sum, as in the forward pass: exp(z -
         // lse) is wrong where lse has lost log(sum) to rounding (logits of the
         // type's lowest value)
-        float pr[V], dot = 0.0f, sum = 0.0f;
         uint32_t key[V], best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            const int e = l + i * L;
-            key[i] = (live && e < p.E) ? logit_key(load_logit<F32>(p.logits, t * p.ld + e)) : 0u;
+            key[i] = (live && l + i * L < p.E) ? logit_key(z[i]) : 0u;
             best = max(best, key[i]);
         }
         const float m = key_logit(lanes_umax<L>(best));
+        float pr[V], dot = 0.0f, sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            pr[i] = key[i] ? __builtin_amdgcn_exp2f((key_logit(key[i]) - m) * kLog2e) : 0.0f;
+            const float v = __builtin_amdgcn_exp2f((z[i] - m) * kLog2e);
+            pr[i] = key[i] ? v : 0.0f;
             sum += pr[i];
             dot = __builtin_fmaf(pr[i], f[i], dot);
         }
         sum = lanes_sum<L>(sum);
         const float inv = live ? 1.0f / sum : 0.0f;
         dot = lanes_sum<L>(dot) * inv;
-#pragma unroll
-        for (int i = 0; i < V; ++i) pr[i] *= inv;
         float wd = 0.0f;
-        float w[2] = {0.0f, 0.0f}, dw[2] = {0.0f, 0.0f};
-        int es[2] = {-1, -1};
-        if (p.dweights && live) {
 #pragma unroll
-            for (int u = 0; u < 2; ++u) {
-                const int j = l + u * L;
-                if (j < p.k) {
-                    es[u] = p.experts[t * p.k + j];
-                    w[u] = es[u] >= 0 ? p.weights[t * p.k + j] : 0.0f;
-                    dw[u] = es[u] >= 0 ? p.dweights[t * p.k + j] : 0.0f;
-                    wd = __builtin_fmaf(w[u], dw[u], wd);
-                }
-            }
+        for (int u = 0; u < 2; ++u) {
+            if (!live || es[u] < 0 || es[u] >= p.E) { es[u] = -1; w[u] = dw[u] = 0.0f; }
+            wd = __builtin_fmaf(w[u], dw[u], wd);
         }
         wd = lanes_sum<L>(wd);
+        // the group's LDS row, within one wave: ordered by the fences
+        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+        __builtin_amdgcn_wave_barrier();
 #pragma unroll
         for (int u = 0; u < 2; ++u)
-            if (es[u] >= 0 && es[u] < p.E) part[es[u]] = p.renorm ? w[u] * (dw[u] - wd) : w[u] * dw[u];
+            if (es[u] >= 0) part[es[u]] = p.renorm ? w[u] * (dw[u] - wd) : w[u] * dw[u];
         __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
         __builtin_amdgcn_wave_barrier();
         const float zt = gz * (live ? lse : 0.0f) - (p.renorm ? 0.0f : wd);
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const int e = l + i * L;
-            const float d = __builtin_fmaf(pr[i], __builtin_fmaf(gb, f[i] - dot, zt), part[e]);
+            const float d = __builtin_fmaf(pr[i] * inv, __builtin_fmaf(gb, f[i] - dot, zt), part[e]);
             part[e] = 0.0f;
-            if (e < p.E) {
+            if (have && e < p.E) {
                 if (F32) static_cast<float*>(p.dlogits)[t * p.ld_d + e] = d;
                 else static_cast<uint16_t*>(p.dlogits)[t * p.ld_d + e] = (uint16_t)f32_to_bf16_rne(d);
             }
         }
-        __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-        __builtin_amdgcn_wave_barrier();
     }
 }
 
@@ -453,11 +623,11 @@ template <int L, int V>
 struct Select {
     static hipError_t run(const RouteArgs& p, const RouteWs& ws, int nblk, hipStream_t st) {
         if (nblk <= 1) {
-            const size_t lds = (size_t)p.E * 20 + 8;
+            const size_t lds = select_lds(p.E) + (size_t)p.E * 8 + 8;
             if (p.logits32) hipLaunchKernelGGL((k_route_one<L, V, true>), dim3(1), dim3(kThreads), lds, st, p);
             else hipLaunchKernelGGL((k_route_one<L, V, false>), dim3(1), dim3(kThreads), lds, st, p);
         } else {
-            const size_t lds = (size_t)p.E * 12;
+            const size_t lds = select_lds(p.E);
             if (p.logits32) hipLaunchKernelGGL((k_route_select<L, V, true>), dim3(nblk), dim3(kThreads), lds, st, p, ws);
             else hipLaunchKernelGGL((k_route_select<L, V, false>), dim3(nblk), dim3(kThreads), lds, st, p, ws);
         }
@@ -480,25 +650,50 @@ struct Backward {
 
 }  // namespace
 
-size_t route_ws_bytes(int64_t T, int32_t E) {
+// Workspace: per workgroup of tokens the histogram bytes [epad] and the
+// probability sums [epad]; per workgroup the loss terms; for more than kDirect of
+// them the scanned counts [epad] and the sums [E].
+static RouteWs route_ws(int64_t T, int32_t E, void* base, size_t* bytes) {
     const int64_t nblk = (T + kTok - 1) / kTok;
-    if (nblk <= 1) return 0;
-    return (size_t)(nblk * (2 * (int64_t)E + 2) + E) * 4;
+    RouteWs ws{};
+    ws.epad = 16;
+    while (ws.epad < E) ws.epad *= 2;
+    size_t off = 0;
+    auto take = [&](size_t n) { const size_t o = off; off += (n + 15) / 16 * 16; return static_cast<char*>(base) + o; };
+    if (nblk > 1) {
+        ws.hist = reinterpret_cast<uint8_t*>(take((size_t)nblk * ws.epad));
+        ws.psum = reinterpret_cast<float*>(take((size_t)nblk * ws.epad * 4));
+        ws.lse2 = reinterpret_cast<float*>(take((size_t)nblk * 4));
+        ws.live = reinterpret_cast<int32_t*>(take((size_t)nblk * 4));
+    }
+    if (nblk > kDirect) {
+        ws.base = reinterpret_cast<int32_t*>(take((size_t)nblk * ws.epad * 4));
+        ws.total = reinterpret_cast<float*>(take((size_t)E * 4));
+    }
+    *bytes = off;
+    return ws;
+}
+
+size_t route_ws_bytes(int64_t T, int32_t E) {
+    size_t bytes;
+    route_ws(T, E, nullptr, &bytes);
+    return bytes;
 }
 
 hipError_t launch_moe_route(const RouteArgs& p, void* wsp, hipStream_t st) {
     const int nblk = (int)((p.T + kTok - 1) / kTok);
-    RouteWs ws{};
-    ws.hist = static_cast<int32_t*>(wsp);
-    ws.psum = reinterpret_cast<float*>(ws.hist + (int64_t)nblk * p.E);
-    ws.lse2 = ws.psum + (int64_t)nblk * p.E;
-    ws.live = reinterpret_cast<int32_t*>(ws.lse2 + nblk);
-    ws.total = reinterpret_cast<float*>(ws.live + nblk);
+    size_t bytes;
+    const RouteWs ws = route_ws(p.T, p.E, wsp, &bytes);
     hipError_t e = by_experts<Select>(p.E, p, ws, nblk, st);
     if (e != hipSuccess || nblk <= 1) return e;
-    hipLaunchKernelGGL(k_route_scan, dim3((p.E + 3) / 4), dim3(256), 0, st, p, ws, nblk);
+    if (nblk <= kDirect) {
+        const size_t lds = (size_t)ws.epad * 16 + 16 + (size_t)kHalf * ws.epad * 4;
+        hipLaunchKernelGGL(k_route_place, dim3(nblk + 1), dim3(kThreads), lds, st, p, ws, nblk);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(k_route_scan, dim3((p.E + 15) / 16), dim3(kThreads), 0, st, p, ws, nblk);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(k_route_place, dim3(nblk + 1), dim3(kThreads), (size_t)p.E * 16 + 8, st, p, ws, nblk);
+    hipLaunchKernelGGL(k_route_place_scanned, dim3(nblk + 1), dim3(kThreads), (size_t)p.E * 16 + 8, st, p, ws, nblk);
     return hipGetLastError();
 }
 

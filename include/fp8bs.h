@@ -511,7 +511,7 @@ fp8bs_status fp8_moe_combine_backward(const void* dout, int64_t ld_dout, fp8bs_o
  * Selection: each token takes the k experts with the largest logits, in that
  * order; equal logits (-0 and +0 are equal) go to the lower expert, NaN counts
  * as the largest and makes its token's weights, lse and the losses NaN.  A
- * token whose mask byte is 0 is not routed and its logits are not read; an
+ * token whose mask byte is 0 is not routed, whatever its logits; an
  * expert whose logit is -inf is not taken.  A slot that takes no expert has
  * expert -1, weight 0 and row -1.
  *
@@ -555,9 +555,9 @@ fp8bs_status fp8_moe_route_ws_size(int64_t T, int32_t E, size_t* bytes);
  *     sum(weights * dweights) + dloss[0] loss[0] + dloss[1] loss[1]
  * (the selection and the counts are constants, as is usual for this loss).
  * experts, weights, counts, lse: fp8_moe_route's outputs; a token whose lse
- * is -inf gets zeros and its logits are not read for their values.
+ * is -inf gets zeros, whatever its logits.
  * dweights : nullable fp32 [T][k] (fp8_moe_combine_backward's); entries of
- *            slots without an expert are not read.
+ *            slots without an expert have no effect.
  * dloss    : nullable device fp32 [2].  At least one of the two; experts and
  *            weights are required with dweights, counts with dloss.
  * dlogits  : [T][ld_d] of the logits' type (rounded once from fp32).
