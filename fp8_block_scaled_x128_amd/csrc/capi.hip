@@ -588,16 +588,15 @@ fp8bs_status fp8_moe_combine_backward(const void* dout, int64_t ld_dout, fp8bs_o
 static fp8bs_status route_shape(int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k, int32_t renorm) {
     if (!type_ok(type)) return fail(FP8BS_ERR_UNSUPPORTED, "type %d", (int)type);
     if (renorm != 0 && renorm != 1) return fail(FP8BS_ERR_UNSUPPORTED, "renorm %d", (int)renorm);
-    if (T < 0 || T > (1ll << 26)) return fail(FP8BS_ERR_SHAPE, "T=%lld outside [0, 2^26]", (long long)T);
+    if (T < 0 || T > (1ll << 22)) return fail(FP8BS_ERR_SHAPE, "T=%lld outside [0, 2^22]", (long long)T);
     if (E < 1 || E > 1024) return fail(FP8BS_ERR_SHAPE, "E=%d outside [1, 1024]", (int)E);
     if (k < 1 || k > E || k > 32) return fail(FP8BS_ERR_SHAPE, "k=%d outside [1, min(E, 32)]", (int)k);
-    if (T * k > INT32_MAX) return fail(FP8BS_ERR_SHAPE, "T * k >= 2^31");
     if (ld < E) return fail(FP8BS_ERR_STRIDE, "ld < E");
     return FP8BS_OK;
 }
 
 fp8bs_status fp8_moe_route_ws_size(int64_t T, int32_t E, size_t* bytes) {
-    if (T < 0 || T > (1ll << 26)) return fail(FP8BS_ERR_SHAPE, "T=%lld outside [0, 2^26]", (long long)T);
+    if (T < 0 || T > (1ll << 22)) return fail(FP8BS_ERR_SHAPE, "T=%lld outside [0, 2^22]", (long long)T);
     if (E < 1 || E > 1024) return fail(FP8BS_ERR_SHAPE, "E=%d outside [1, 1024]", (int)E);
     if (!bytes) return fail(FP8BS_ERR_NULL, "bytes is required");
     *bytes = route_ws_bytes(T, E);
@@ -664,7 +663,7 @@ static fp8bs_status norm_common(int64_t rows, int64_t cols, fp8bs_out stream_typ
                                 float eps) {
     if (!type_ok(stream_type) || !type_ok(w_type)) return fail(FP8BS_ERR_UNSUPPORTED, "stream_type or w_type");
     if (rows < 0 || cols < 0 || rows > INT32_MAX) return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
-    if (cols % 8 || cols > 32768) return fail(FP8BS_ERR_SHAPE, "cols %% 8 != 0 or cols > 32768 (cols=%lld)", (long long)cols);
+    if (cols % 8 || cols > 16384) return fail(FP8BS_ERR_SHAPE, "cols %% 8 != 0 or cols > 16384 (cols=%lld)", (long long)cols);
     // comparisons that a NaN fails
     if (!(eps > 0.0f && eps <= 3.0e38f)) return fail(FP8BS_ERR_UNSUPPORTED, "eps must be positive and finite");
     if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(FP8BS_ERR_UNSUPPORTED, "scale must be finite");

@@ -85,14 +85,14 @@ struct NormBwdArgs {
     void* dgate; int64_t ld_dgate; bool dgate32;
     float* dw_post; float* dw_pre;
 };
-// How the rows are dealt: units of `chunk` rows, `splits` of them per gate row
-// (or over all rows), walked by `slots` workgroups or waves; the column sums'
+// How the rows are dealt: `splits` units per gate row (or over all rows), every
+// splits-th row each, walked by `slots` workgroups; the column sums'
 // partials lie at the three offsets (in floats) of the workspace.
 struct NormBwdPlan {
     int wpr, nv;
     bool grouped, by_wave;
     int32_t slots;
-    int64_t units, splits, chunk, unit_rows, groups;
+    int64_t units, splits, unit_rows, groups;
     size_t off_pre, off_post, off_gate, ws_floats;
     float *ws_pre, *ws_post, *ws_gate;
 };
@@ -108,7 +108,7 @@ struct RouteArgs {
     int32_t* experts; float* weights; int32_t* counts; int32_t* offsets; int32_t* row_token; int32_t* token_rows;
     float* lse; float* loss;
 };
-struct RouteWs { int32_t epad; uint8_t* hist; float* psum; float* lse2; int32_t* live; int32_t* base; float* total; };
+struct RouteWs { int32_t epad; uint8_t* hist; float* psum; float* lse2; int32_t* live; int32_t* run_cnt; float* run_psum; };
 size_t route_ws_bytes(int64_t T, int32_t E);
 hipError_t launch_moe_route(const RouteArgs& p, void* ws, hipStream_t st);
 

@@ -77,11 +77,11 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine(const uint16_t* __rest
 }
 
 // Gradient of the combine: dy[row] = w dout[t] and dw = <dout[t], y[row]> for
-// every (token, slot) with a row.  One wave holds a token and walks the
-// columns in runs of 512 (8 per lane): per run, dout is loaded once and up to
+// every (token, slot) with a row.  WPT waves hold a token and walk the columns
+// in runs of 512 each (8 per lane): per run, dout is loaded once and up to
 // eight y rows are in flight, each giving its part of a dot product and
 // taking its dy row at once, so nothing of a row stays in registers.
-template <bool DO32>
+template <bool DO32, int WPT>
 __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const void* __restrict__ dout, int64_t ld_do,
                                                               const uint16_t* __restrict__ y, int32_t rows,
                                                               int32_t nch, int64_t ld_y,
@@ -89,20 +89,22 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const void* __rest
                                                               const float* __restrict__ w, int64_t T, int32_t k,
                                                               uint16_t* __restrict__ dy, int64_t ld_dy,
                                                               float* __restrict__ dw) {
-    const int lane = threadIdx.x & 63;
-    const int64_t t = (int64_t)blockIdx.x * (kThreads / 64) + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    if (t >= T) return;
+    constexpr int kWaves = kThreads / 64, kPer = kWaves / WPT;
+    __shared__ float part[WPT > 1 ? kWaves : 1][8];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * kPer + wave / WPT;
+    const bool have = t < T;
     for (int j0 = 0; j0 < k; j0 += 8) {
         int r[8];
         float wj[8], dot[8];
 #pragma unroll
         for (int u = 0; u < 8; ++u) {
-            const int pj = j0 + u < k ? pos[t * k + j0 + u] : -1;
+            const int pj = have && j0 + u < k ? pos[t * k + j0 + u] : -1;
             r[u] = (uint32_t)pj < (uint32_t)rows ? pj : -1;
             wj[u] = r[u] >= 0 ? w[t * k + j0 + u] : 0.0f;
             dot[u] = 0.0f;
         }
-        for (int c = lane; c < nch; c += 64) {
+        for (int c = have ? (wave % WPT) * 64 + lane : nch; c < nch; c += 64 * WPT) {
             uint4 raw[8];
             float d[8];
 #pragma unroll
@@ -131,12 +133,26 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const void* __rest
                                           pack_bf16x2(wj[u] * d[4], wj[u] * d[5]), pack_bf16x2(wj[u] * d[6], wj[u] * d[7])));
             }
         }
-        if (dw) {
+        if (!dw) continue;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                const float s = lanes_sum<64>(dot[u]);
-                if (lane == 0 && j0 + u < k) dw[t * k + j0 + u] = s;
+        for (int u = 0; u < 8; ++u) dot[u] = lanes_sum<64>(dot[u]);
+        if (WPT > 1) {
+            if (lane == 0) {
+#pragma unroll
+                for (int u = 0; u < 8; ++u) part[WPT > 1 ? wave : 0][u] = dot[u];
             }
+            __syncthreads();
+            if (wave % WPT == 0 && lane < 8 && have && j0 + lane < k) {
+                float s = 0.0f;
+#pragma unroll
+                for (int i = 0; i < WPT; ++i) s += part[WPT > 1 ? wave + i : 0][lane];
+                dw[t * k + j0 + lane] = s;
+            }
+            __syncthreads();
+        } else if (have) {
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+                if (lane == 0 && j0 + u < k) dw[t * k + j0 + u] = dot[u];
         }
     }
 }
@@ -160,9 +176,17 @@ hipError_t launch_moe_combine_bwd(const void* dout, int64_t ld_do, int do_f32, c
                                   int64_t H, int64_t ld_y, const int32_t* pos, const float* w, int64_t T, int32_t k,
                                   uint16_t* dy, int64_t ld_dy, float* dw, hipStream_t st) {
     if (T == 0) return hipSuccess;
-    const dim3 grid((unsigned)((T + kThreads / 64 - 1) / (kThreads / 64)));
-    const auto k_fn = do_f32 ? k_moe_combine_bwd<true> : k_moe_combine_bwd<false>;
-    hipLaunchKernelGGL(k_fn, grid, dim3(kThreads), 0, st, dout, ld_do, y, (int32_t)rows, (int32_t)(H / 8), ld_y, pos,
+    // Waves per token: as many as have a run of columns each and, over the
+    // slots, four rows of one (16384 tokens x 2048, k 8: 1 / 2 / 4 waves 224 /
+    // 214 / 205 us; k 1: 34.1 / 34.8 / 41.8; 16384 x 128, k 2: 12.6 / 18.4 /
+    // 30.1).
+    const int64_t runs = (H / 8 + 63) / 64, rows_of = runs * (k < 8 ? k : 8);
+    const int wpt = runs >= 4 && rows_of >= 16 ? 4 : runs >= 2 && rows_of >= 8 ? 2 : 1;
+    const int64_t per = kThreads / 64 / wpt;
+    const auto k_fn =
+        do_f32 ? (wpt == 4 ? k_moe_combine_bwd<true, 4> : wpt == 2 ? k_moe_combine_bwd<true, 2> : k_moe_combine_bwd<true, 1>)
+               : (wpt == 4 ? k_moe_combine_bwd<false, 4> : wpt == 2 ? k_moe_combine_bwd<false, 2> : k_moe_combine_bwd<false, 1>);
+    hipLaunchKernelGGL(k_fn, dim3((unsigned)((T + per - 1) / per)), dim3(kThreads), 0, st, dout, ld_do, y, (int32_t)rows, (int32_t)(H / 8), ld_y, pos,
                        w, T, k, dy, ld_dy, dw);
     return hipGetLastError();
 }

@@ -15,7 +15,15 @@ namespace fp8bs {
 namespace {
 
 constexpr int kRowWaves = 4;         // waves of a workgroup whose rows need one wave each
-constexpr int kBlocks = 1024;        // workgroups at most
+// Workgroups at most: about 5120 waves of one chunk per lane, which is where
+// more rows in flight stop paying (16384x768: 1024 workgroups of two waves 34.7
+// us, 2048 25.4; 4096x5120: 1024 workgroups of five waves with two chunks 49.0,
+// 512 39.2; 4096x2560: 1024 of five waves 20.8, 2048 23.9), equally many per
+// compute unit (16384x2048: 1024 of four waves 90.5, 1261 93.6) and two at least.
+int64_t workgroups(int wpr, int nv) {
+    const int64_t n = 5120 / (wpr * nv) / kCUs * kCUs;
+    return n < 2 * kCUs ? 2 * kCUs : n;
+}
 
 // One row as loaded.
 template <int NV, bool RES32>
@@ -23,26 +31,28 @@ struct RowIn {
     Raw8<RES32> res[NV];
     Raw8<false> x[NV], gate[NV];
     __device__ __forceinline__ void load(const NormArgs& p, int64_t row, int tid, int step, int nc) {
+        const void* residual_row = row_ptr<RES32>(p.residual, row, p.ld_r);
+        const void* x_row = row_ptr<false>(p.x, row, p.ld_x);
         if (p.x) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = tid + i * step;
-                if (i < kSure<NV> || c < nc) x[i].load(p.x, row * p.ld_x + 8 * c);
+                if (i < kSure<NV> || c < nc) x[i].load(x_row, c);
             }
         }
         if (p.residual) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = tid + i * step;
-                if (i < kSure<NV> || c < nc) res[i].load(p.residual, row * p.ld_r + 8 * c);
+                if (i < kSure<NV> || c < nc) res[i].load(residual_row, c);
             }
         }
         if (p.gate) {
-            const int64_t g = (int64_t)((uint32_t)row / (uint32_t)p.rows_per_gate) * p.ld_gate;
+            const uint16_t* g_row = row_ptr<false>(p.gate, (int64_t)((uint32_t)row / (uint32_t)p.rows_per_gate), p.ld_gate);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = tid + i * step;
-                if (i < kSure<NV> || c < nc) gate[i].load_shared(p.gate, g + 8 * c);
+                if (i < kSure<NV> || c < nc) gate[i].load_shared(g_row, c);
             }
         }
     }
@@ -72,8 +82,8 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
         const int c = min(tid + i * step, nc - 1);          // past the row: x and residual are 0
 #pragma unroll
         for (int e = 0; e < 8; ++e) wpre[i][e] = wpost[i][e] = 1.0f;
-        if (AHEAD && p.w_pre) load8_shared(p.w_pre, 8 * c, p.w32, wpre[i]);
-        if (AHEAD && p.w_post) load8_shared(p.w_post, 8 * c, p.w32, wpost[i]);
+        if (AHEAD && p.w_pre) load8_shared(p.w_pre, c, p.w32, wpre[i]);
+        if (AHEAD && p.w_post) load8_shared(p.w_post, c, p.w32, wpost[i]);
     }
     const int64_t per = MULTI ? 1 : kRowWaves;              // rows a workgroup has at a time
     const int64_t first = MULTI ? (int64_t)blockIdx.x
@@ -112,7 +122,7 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
             float v[8], gate[8];
             in.res[i].get(h[i]);
             in.x[i].get(v);
-            if (!AHEAD && p.w_post) load8_shared(p.w_post, 8 * min(c, nc - 1), p.w32, wpost[i % KEPT]);
+            if (!AHEAD && p.w_post) load8_shared(p.w_post, min(c, nc - 1), p.w32, wpost[i % KEPT]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) v[e] = v[e] * r * wpost[i % KEPT][e];
             if (p.gate) {
@@ -122,7 +132,7 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = __builtin_fmaf(v[e], p.scale, h[i][e]);
-            if (p.h && (i < kSure<NV> || c < nc)) store8<RES32>(p.h, row * p.ld_h + 8 * c, h[i]);
+            if (p.h && (i < kSure<NV> || c < nc)) store8<RES32>(row_ptr<RES32>(p.h, row, p.ld_h), c, h[i]);
             ss[0] += sumsq8(h[i]);
         }
         if (!p.w_pre) continue;
@@ -134,17 +144,17 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * step;
             const bool in_row = i < kSure<NV> || c < nc;
-            if (!AHEAD) load8_shared(p.w_pre, 8 * min(c, nc - 1), p.w32, wpre[i % KEPT]);
+            if (!AHEAD) load8_shared(p.w_pre, min(c, nc - 1), p.w32, wpre[i % KEPT]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * r * wpre[i % KEPT][e];
-            if (p.y && in_row) store8<false>(p.y, row * p.ld_y + 8 * c, h[i]);
+            if (p.y && in_row) store8<false>(row_ptr<false>(p.y, row, p.ld_y), c, h[i]);
             if (p.q) {
                 // 16 lanes hold a 128-column group; lanes past the row hold zeros
                 const float s = row16_max(absmax8(h[i])) / kE4M3Max;
                 uint32_t w0, w1;
                 encode8(h[i], s, w0, w1);
                 if (in_row) {
-                    *reinterpret_cast<uint2*>(p.q + row * p.ld_q + 8 * c) = make_uint2(w0, w1);
+                    *reinterpret_cast<uint2*>(p.q + row * p.ld_q + 8u * (uint32_t)c) = make_uint2(w0, w1);
                     if ((c & 15) == 0) p.s[row * p.ssr + (int64_t)(c >> 4) * p.ssg] = s;
                 }
             }
@@ -155,9 +165,9 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
 template <int NV, bool MULTI>
 hipError_t launch_types(const NormArgs& p, int wpr, hipStream_t st) {
     const int per = MULTI ? 1 : kRowWaves;
-    const int64_t blocks = (p.rows + per - 1) / per;
+    const int64_t blocks = (p.rows + per - 1) / per, most = workgroups(MULTI ? wpr : per, NV);
     hipLaunchKernelGGL((p.res32 ? k_block_norm<NV, true, MULTI> : k_block_norm<NV, false, MULTI>),
-                       dim3((unsigned)(blocks < kBlocks ? blocks : kBlocks)), dim3(MULTI ? 64 * wpr : 64 * kRowWaves), 0,
+                       dim3((unsigned)(blocks < most ? blocks : most)), dim3(MULTI ? 64 * wpr : 64 * kRowWaves), 0,
                        st, p, wpr);
     return hipGetLastError();
 }
@@ -166,13 +176,12 @@ hipError_t launch_types(const NormArgs& p, int wpr, hipStream_t st) {
 
 hipError_t launch_block_norm(const NormArgs& p, hipStream_t st) {
     int wpr, nv;
-    row_split(p.cols, 1, &wpr, &nv);
+    row_split(p.cols, &wpr, &nv);
     switch (nv) {
         case 1: return wpr == 1 ? launch_types<1, false>(p, wpr, st) : launch_types<1, true>(p, wpr, st);
-        case 2: return wpr == 1 ? launch_types<2, false>(p, wpr, st) : launch_types<2, true>(p, wpr, st);
+        case 2: return launch_types<2, true>(p, wpr, st);
         case 3: return launch_types<3, true>(p, wpr, st);
-        case 4: return launch_types<4, true>(p, wpr, st);
-        default: return launch_types<kMaxNv, true>(p, wpr, st);
+        default: return launch_types<4, true>(p, wpr, st);
     }
 }
 

@@ -7,8 +7,7 @@
 //   xh = x r';  dn = scale gate dH;  dgate = sum scale dH xh w_post
 //   dw_post = sum_rows dn xh;  dx = r' (dn w_post - xh mean(dn w_post xh))
 //
-// HBM-bound.  A workgroup walks units of consecutive rows that share a gate
-// row; its column sums of dw_pre and dw_post stay in registers over all its
+// HBM-bound.  A workgroup walks units of rows that share a gate row; its column sums of dw_pre and dw_post stay in registers over all its
 // rows and leave one partial row each, which k_col_reduce adds in workgroup
 // order (no atomics: the same bits every time).
 #include "norm_common.h"
@@ -17,7 +16,6 @@ namespace fp8bs {
 namespace {
 
 constexpr int kWaves = 8;                // waves of a workgroup whose rows need one wave each
-constexpr int kSlots = 512;              // workgroups at most
 
 // Adds the waves' register sums in wave order (one wave per row: 8 rows at a
 // time); the last wave's registers hold the result.
@@ -39,20 +37,71 @@ __device__ __forceinline__ void combine_waves(float (&a)[8], float (*comb)[8], i
     __syncthreads();
 }
 
+// Adds eight values to a lane's sums in LDS.
+__device__ __forceinline__ void add_lds(float4* a, const float v[8]) {
+    float4* b = a + 64 * kMaxRowWaves;
+    const float4 u = *a, w = *b;
+    *a = make_float4(u.x + v[0], u.y + v[1], u.z + v[2], u.w + v[3]);
+    *b = make_float4(w.x + v[4], w.y + v[5], w.z + v[6], w.w + v[7]);
+}
+
+// A row's weights as loaded, and their values (`kind` 0: bf16, 1: fp32, 2:
+// none, all 1).
+template <int NV>
+struct Weights {
+    uint4 r[NV][2];
+    __device__ __forceinline__ void load(const void* p, bool f32, int tid, int step, int nc) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const uint32_t c = min(tid + i * step, nc - 1);
+            if (f32) {
+                const uint4* f = reinterpret_cast<const uint4*>(static_cast<const char*>(p) + c * 32u);
+                r[i][0] = f[0];
+                r[i][1] = f[1];
+            } else {
+                r[i][0] = *reinterpret_cast<const uint4*>(static_cast<const char*>(p) + c * 16u);
+            }
+        }
+    }
+    __device__ __forceinline__ void get(int i, int kind, float v[8]) const {
+        if (kind == 2) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = 1.0f;
+        } else if (kind == 1) {
+            const uint4 a = r[i][0], b = r[i][1];
+            v[0] = __uint_as_float(a.x); v[1] = __uint_as_float(a.y);
+            v[2] = __uint_as_float(a.z); v[3] = __uint_as_float(a.w);
+            v[4] = __uint_as_float(b.x); v[5] = __uint_as_float(b.y);
+            v[6] = __uint_as_float(b.z); v[7] = __uint_as_float(b.w);
+        } else {
+            unpack8(r[i][0], v);
+        }
+    }
+};
+
+// What there is of a gate: none; a gradient per row (or none wanted); a
+// gradient summed over the rows of a gate row.
+enum { kGateNone, kGateRow, kGateSum };
+
 // One row as loaded.
-template <int NV, bool RES32, bool DY32, bool GACC>
+template <int NV, bool RES32, bool DY32, int GATE>
 struct RowIn {
     Raw8<RES32> dh[NV], h[NV];
     Raw8<DY32> dy[NV];
-    Raw8<false> x[NV], gate[GACC ? 1 : NV];
+    static constexpr bool GATE_IN = GATE == kGateRow || (GATE == kGateSum && NV > 2);     // the gate comes with the row
+    Raw8<false> x[NV], gate[GATE_IN ? NV : 1];
     __device__ __forceinline__ void load(const NormBwdArgs& p, int64_t row, int tid, int step, int nc) {
+        const void* h_row = row_ptr<RES32>(p.h, row, p.ld_h);
+        const void* dy_row = row_ptr<DY32>(p.dy, row, p.ld_dy);
+        const void* dh_row = row_ptr<RES32>(p.dh, row, p.ld_dh);
+        const void* x_row = row_ptr<false>(p.x, row, p.ld_x);
         if (p.w_pre) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = tid + i * step;
                 if (i < kSure<NV> || c < nc) {
-                    h[i].load(p.h, row * p.ld_h + 8 * c);
-                    dy[i].load(p.dy, row * p.ld_dy + 8 * c);
+                    h[i].load(h_row, c);
+                    dy[i].load(dy_row, c);
                 }
             }
         }
@@ -60,103 +109,122 @@ struct RowIn {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = tid + i * step;
-                if (i < kSure<NV> || c < nc) x[i].load(p.x, row * p.ld_x + 8 * c);
+                if (i < kSure<NV> || c < nc) x[i].load(x_row, c);
             }
         }
         if (p.dh) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = tid + i * step;
-                if (i < kSure<NV> || c < nc) dh[i].load(p.dh, row * p.ld_dh + 8 * c);
+                if (i < kSure<NV> || c < nc) dh[i].load(dh_row, c);
             }
         }
-        if (!GACC && p.gate) {
-            const int64_t g = (int64_t)((uint32_t)row / (uint32_t)p.rows_per_gate) * p.ld_gate;
+        if (GATE_IN) {
+            const uint16_t* g_row = row_ptr<false>(p.gate, (int64_t)((uint32_t)row / (uint32_t)p.rows_per_gate), p.ld_gate);
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = tid + i * step;
-                if (i < kSure<NV> || c < nc) gate[GACC ? 0 : i].load(p.gate, g + 8 * c);
+                if (i < kSure<NV> || c < nc) gate[GATE_IN ? i : 0].load_shared(g_row, c);
             }
         }
     }
     __device__ __forceinline__ void zero() {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            dh[i].zero(); h[i].zero(); dy[i].zero(); x[i].zero(); gate[GACC ? 0 : i].zero();
+            dh[i].zero(); h[i].zero(); dy[i].zero(); x[i].zero(); gate[GATE_IN ? i : 0].zero();
         }
     }
 };
 
 // MULTI: a workgroup has one row at a time, else each of its waves has one.
-// GACC: the gate's gradient is summed over the rows of a gate row.
-// One or two chunks per lane (AHEAD): the next row is loaded while this one is
-// reduced and stored, and the weights stay in registers: a weight load from
-// the L2 behind the next row's loads would wait for them, since loads return
-// in order.  More chunks have no registers left for it.
-template <int NV, bool RES32, bool DY32, bool MULTI, bool GACC>
+//
+// The next row is loaded while this one is reduced and stored, as far as the
+// registers go (AHEAD).  Loads return in order, so a weight load from the L2 behind the next row's loads would
+// wait for them: up to two chunks per lane the weights stay in registers
+// (KEEP), above that each row's are loaded ahead of the next row's data.
+// Column sums are in registers too up to two chunks per lane; above that the
+// registers would spill (measured with 2048x10240: 99 us), and each lane keeps
+// its columns' sums in LDS, 16 bytes a column (halves of a chunk 16 bytes
+// apart from lane to lane: no bank conflicts).
+template <int NV, bool RES32, bool DY32, bool MULTI, int GATE>
 __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPlan pl) {
-    constexpr bool AHEAD = NV <= 2;
+    constexpr bool GACC = GATE == kGateSum;
+    constexpr bool KEEP = NV <= 2;
+    constexpr bool AHEAD = NV <= 2 || (NV == 3 && GATE == kGateNone);
+    constexpr int KEPT = KEEP ? NV : 1;
     __shared__ float lds[2][kMaxRowWaves][4];
     __shared__ float comb[MULTI ? 1 : 64][8];
+    __shared__ float4 lacc[KEEP ? 1 : NV * 4][KEEP ? 1 : 64 * kMaxRowWaves];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wpr = pl.wpr;
     const int tid = MULTI ? threadIdx.x : (threadIdx.x & 63);
     const int nc = p.cols >> 3, step = MULTI ? wpr * 64 : 64;
     const float inv_n = 1.0f / (float)p.cols;
     int turn = 0;
-    float awpre[NV][8], awpost[NV][8], agate[NV][8];
-    constexpr int KEPT = AHEAD ? NV : 1;
-    float wpre[KEPT][8], wpost[KEPT][8], wgate[KEPT][8];
+    float awpre[KEPT][8], awpost[KEPT][8], agate[GACC ? NV : 1][8];
+    Weights<KEEP ? 1 : NV> rpre, rpost;                 // as loaded, for !KEEP
+    float wpre[KEPT][8], wpost[KEPT][8], wgate[8];
+    float kgate[GACC && KEEP ? NV : 1][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) wgate[e] = 1.0f;
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            awpre[i][e] = awpost[i][e] = 0.0f;
-            wpre[i % KEPT][e] = wpost[i % KEPT][e] = wgate[i % KEPT][e] = 1.0f;
-        }
         const int c = min(tid + i * step, nc - 1);      // past the row: dy, dh and x are 0
-        if (AHEAD && p.w_pre) load8_shared(p.w_pre, 8 * c, p.w32, wpre[i % KEPT]);
-        if (AHEAD && p.w_post) load8_shared(p.w_post, 8 * c, p.w32, wpost[i % KEPT]);
+        if (KEEP) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                awpre[i % KEPT][e] = awpost[i % KEPT][e] = 0.0f;
+                wpre[i % KEPT][e] = wpost[i % KEPT][e] = 1.0f;
+            }
+            if (p.w_pre) load8_shared(p.w_pre, c, p.w32, wpre[i % KEPT]);
+            if (p.w_post) load8_shared(p.w_post, c, p.w32, wpost[i % KEPT]);
+        } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) lacc[(i * 4 + j) % (KEEP ? 1 : NV * 4)][tid] = make_float4(0, 0, 0, 0);
+        }
     }
     // units by workgroup, its waves taking rows in turn; or (short gate rows)
     // by wave
     const bool by_wave = !MULTI && pl.by_wave;
     const int64_t u0 = by_wave ? (int64_t)blockIdx.x * kWaves + wave : blockIdx.x;
     const int64_t ustep = by_wave ? (int64_t)gridDim.x * kWaves : gridDim.x;
-    const int rstep = MULTI || by_wave ? 1 : kWaves;
+    // a unit's rows: every splits-th of its gate row's, eight at a time where
+    // each wave has one
+    const int lanes = MULTI || by_wave ? 1 : kWaves;
+    const int64_t rstep = pl.splits * lanes;
     for (int64_t u = u0; u < pl.units; u += ustep) {
         const int64_t g = u / pl.splits;
-        const int64_t r0 = g * pl.unit_rows + (u - g * pl.splits) * pl.chunk + (rstep == 1 ? 0 : wave);
-        const int64_t r1 = min(min(r0 - (rstep == 1 ? 0 : wave) + pl.chunk, (g + 1) * pl.unit_rows), p.rows);
+        const int64_t r0 = g * pl.unit_rows + (u - g * pl.splits) * lanes + (lanes == 1 ? 0 : wave);
+        const int64_t r1 = min((g + 1) * pl.unit_rows, p.rows);
         if (GACC) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
                 const int c = min(tid + i * step, nc - 1);
-                if (AHEAD) load8_shared(p.gate, g * p.ld_gate + 8 * c, false, wgate[i % KEPT]);
+                if (KEEP) load8_shared(row_ptr<false>(p.gate, g, p.ld_gate), c, false, kgate[GACC && KEEP ? i : 0]);
 #pragma unroll
-                for (int e = 0; e < 8; ++e) agate[i][e] = 0.0f;
+                for (int e = 0; e < 8; ++e) agate[GACC ? i : 0][e] = 0.0f;
             }
         }
-        RowIn<NV, RES32, DY32, GACC> in, ahead;
+        RowIn<NV, RES32, DY32, GATE> in, ahead;
         in.zero();
         if (AHEAD) {
             ahead.zero();
             if (r0 < r1) ahead.load(p, r0, tid, step, nc);
         }
         for (int64_t row = r0; row < r1; row += rstep) {
-            if (AHEAD) {
-                in = ahead;
-                if (row + rstep < r1) ahead.load(p, row + rstep, tid, step, nc);
-            } else {
-                in.load(p, row, tid, step, nc);
+            if (AHEAD) in = ahead;
+            if (!KEEP) {
+                if (p.w_pre) rpre.load(p.w_pre, p.w32, tid, step, nc);
+                if (p.w_post) rpost.load(p.w_post, p.w32, tid, step, nc);
             }
+            if (!AHEAD) in.load(p, row, tid, step, nc);
+            else if (row + rstep < r1) ahead.load(p, row + rstep, tid, step, nc);
             float sums[3] = {0.0f, 0.0f, 0.0f};     // sum h^2, sum dy w_pre h, sum x^2
             if (p.w_pre) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = min(tid + i * step, nc - 1);
                     float h[8], dy[8];
-                    if (!AHEAD) load8_shared(p.w_pre, 8 * c, p.w32, wpre[i % KEPT]);
+                    if (!KEEP) rpre.get(KEEP ? 0 : i, p.w32, wpre[i % KEPT]);
                     in.h[i].get(h);
                     in.dy[i].get(dy);
                     sums[0] += sumsq8(h);
@@ -172,6 +240,8 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
                 sums[2] += sumsq8(x);
             }
             row_sums<MULTI>(sums, wpr, lds, turn);
+#pragma unroll
+            for (int i = 0; i < NV; ++i) { in.h[i].forget(); in.dy[i].forget(); in.x[i].forget(); }
             float dh[NV][8];
 #pragma unroll
             for (int i = 0; i < NV; ++i) in.dh[i].get(dh[i]);
@@ -180,23 +250,24 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
                 const float m = sums[1] * inv_n * r * r;        // mean(g hh) r: times h, hh mean(g hh)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
-                    const int c = min(tid + i * step, nc - 1);
                     float h[8], dy[8];
-                    if (!AHEAD) load8_shared(p.w_pre, 8 * c, p.w32, wpre[i % KEPT]);
+                    if (!KEEP) rpre.get(KEEP ? 0 : i, p.w32, wpre[i % KEPT]);
                     in.h[i].get(h);
                     in.dy[i].get(dy);
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
-                        awpre[i][e] = __builtin_fmaf(dy[e] * r, h[e], awpre[i][e]);
+                        if (KEEP) awpre[i % KEPT][e] = __builtin_fmaf(dy[e] * r, h[e], awpre[i % KEPT][e]);
                         dh[i][e] = __builtin_fmaf(r, __builtin_fmaf(-m, h[e], dy[e] * wpre[i % KEPT][e]), dh[i][e]);
+                        h[e] *= dy[e] * r;
                     }
+                    if (!KEEP) add_lds(&lacc[KEEP ? 0 : i * 4][tid], h);
                 }
             }
             if (p.dres) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = tid + i * step;
-                    if (i < kSure<NV> || c < nc) store8<RES32>(p.dres, row * p.ld_dres + 8 * c, dh[i]);
+                    if (i < kSure<NV> || c < nc) store8<RES32>(row_ptr<RES32>(p.dres, row, p.ld_dres), c, dh[i]);
                 }
             }
             if (!p.x) continue;
@@ -204,35 +275,42 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
             float dot[1] = {0.0f};
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
-                const int c = min(tid + i * step, nc - 1);
-                float dg[8], x[8];
+                float dg[8], x[8], aw[8];
                 in.x[i].get(x);
-                if (!AHEAD && p.w_post) load8_shared(p.w_post, 8 * c, p.w32, wpost[i % KEPT]);
-                if (!AHEAD && GACC) load8_shared(p.gate, g * p.ld_gate + 8 * c, false, wgate[i % KEPT]);
-                if (!GACC && p.gate) in.gate[GACC ? 0 : i].get(wgate[i % KEPT]);
+                if (!KEEP) rpost.get(KEEP ? 0 : i, p.w_post ? p.w32 : 2, wpost[i % KEPT]);
+                if (GACC && KEEP) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) wgate[e] = kgate[GACC && KEEP ? i : 0][e];
+                } else if (GATE != kGateNone) {
+                    in.gate[GATE == kGateNone || (GACC && KEEP) ? 0 : i].get(wgate);
+                }
 #pragma unroll
                 for (int e = 0; e < 8; ++e) {
                     float dn = dh[i][e] * p.scale;
                     const float xh = x[e] * rx;
-                    if (GACC || p.gate) {
+                    if (GATE != kGateNone) {
                         dg[e] = dn * (xh * wpost[i % KEPT][e]);
-                        if (GACC) agate[i][e] += dg[e];
-                        dn *= wgate[i % KEPT][e];
+                        if (GACC) agate[GACC ? i : 0][e] += dg[e];
+                        dn *= wgate[e];
                     }
-                    awpost[i][e] = __builtin_fmaf(dn, xh, awpost[i][e]);
+                    if (KEEP) awpost[i % KEPT][e] = __builtin_fmaf(dn, xh, awpost[i % KEPT][e]);
+                    aw[e] = dn * xh;
                     dn *= wpost[i % KEPT][e];
                     dot[0] = __builtin_fmaf(dn, xh, dot[0]);
                     dh[i][e] = dn;                      // the gradient at xh from here on
                 }
-                if (!GACC && p.dgate && (i < kSure<NV> || tid + i * step < nc)) {
-                    if (p.dgate32) store8<true>(p.dgate, row * p.ld_dgate + 8 * c, dg);
-                    else store8<false>(p.dgate, row * p.ld_dgate + 8 * c, dg);
+                if (!KEEP) add_lds(&lacc[KEEP ? 0 : i * 4 + 2][tid], aw);
+                if (GATE == kGateRow && p.dgate && (i < kSure<NV> || tid + i * step < nc)) {
+                    if (p.dgate32) store8<true>(row_ptr<true>(p.dgate, row, p.ld_dgate), tid + i * step, dg);
+                    else store8<false>(row_ptr<false>(p.dgate, row, p.ld_dgate), tid + i * step, dg);
                 }
             }
             if (!p.dx) continue;
             float m = 0.0f;
             if (p.w_post) {
                 row_sums<MULTI>(dot, wpr, lds, turn);
+#pragma unroll
+                for (int i = 0; i < NV; ++i) in.x[i].forget();
                 m = dot[0] * inv_n * rx * rx;           // mean(g xh) r': times x
             }
 #pragma unroll
@@ -242,22 +320,22 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
                 in.x[i].get(x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] = __builtin_fmaf(-m, x[e], dh[i][e] * rx);
-                if (i < kSure<NV> || c < nc) store8<false>(p.dx, row * p.ld_dx + 8 * c, d);
+                if (i < kSure<NV> || c < nc) store8<false>(row_ptr<false>(p.dx, row, p.ld_dx), c, d);
             }
         }
         if (GACC) {
             if (!MULTI && !by_wave) {
 #pragma unroll
-                for (int i = 0; i < NV; ++i) combine_waves(agate[i], comb, wave);
+                for (int i = 0; i < NV; ++i) combine_waves(agate[GACC ? i : 0], comb, wave);
             }
             if (MULTI || by_wave || wave == kWaves - 1) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = tid + i * step;
                     if (i >= kSure<NV> && c >= nc) continue;
-                    if (pl.splits > 1) store8<true>(pl.ws_gate, u * p.cols + 8 * c, agate[i]);
-                    else if (p.dgate32) store8<true>(p.dgate, g * p.ld_dgate + 8 * c, agate[i]);
-                    else store8<false>(p.dgate, g * p.ld_dgate + 8 * c, agate[i]);
+                    if (pl.splits > 1) store8<true>(row_ptr<true>(pl.ws_gate, u, p.cols), c, agate[GACC ? i : 0]);
+                    else if (p.dgate32) store8<true>(row_ptr<true>(p.dgate, g, p.ld_dgate), c, agate[GACC ? i : 0]);
+                    else store8<false>(row_ptr<false>(p.dgate, g, p.ld_dgate), c, agate[GACC ? i : 0]);
                 }
             }
         }
@@ -265,8 +343,8 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
     if (!MULTI) {
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            if (p.dw_pre) combine_waves(awpre[i], comb, wave);
-            if (p.dw_post) combine_waves(awpost[i], comb, wave);
+            if (p.dw_pre) combine_waves(awpre[i % KEPT], comb, wave);
+            if (p.dw_post) combine_waves(awpost[i % KEPT], comb, wave);
         }
         if (wave != kWaves - 1) return;
     }
@@ -274,27 +352,44 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
     for (int i = 0; i < NV; ++i) {
         const int c = tid + i * step;
         if (i >= kSure<NV> && c >= nc) continue;
-        if (p.dw_pre) store8<true>(pl.ws_pre, (int64_t)blockIdx.x * p.cols + 8 * c, awpre[i]);
-        if (p.dw_post) store8<true>(pl.ws_post, (int64_t)blockIdx.x * p.cols + 8 * c, awpost[i]);
+        if (KEEP) {
+            if (p.dw_pre) store8<true>(row_ptr<true>(pl.ws_pre, blockIdx.x, p.cols), c, awpre[i % KEPT]);
+            if (p.dw_post) store8<true>(row_ptr<true>(pl.ws_post, blockIdx.x, p.cols), c, awpost[i % KEPT]);
+        } else {
+            const float4* a = &lacc[KEEP ? 0 : i * 4][tid];
+            constexpr int kRow = KEEP ? 0 : 64 * kMaxRowWaves;
+            float4* pre = reinterpret_cast<float4*>(pl.ws_pre + (int64_t)blockIdx.x * p.cols + 8 * c);
+            float4* post = reinterpret_cast<float4*>(pl.ws_post + (int64_t)blockIdx.x * p.cols + 8 * c);
+            if (p.dw_pre) { pre[0] = a[0]; pre[1] = a[kRow]; }
+            if (p.dw_post) { post[0] = a[2 * kRow]; post[1] = a[3 * kRow]; }
+        }
     }
 }
 
-// Column sums of partial rows: job 0 / 1 (dw_pre, dw_post) over the
-// workgroups, job 2 + g (dgate row g) over its units, each in order.  A
-// workgroup takes 32 columns; its 128 row lanes add every 128th partial, then
-// meet in LDS in a fixed order.
-constexpr int kRedCols = 32, kRedRows = 128;
-__global__ void __launch_bounds__(1024) k_col_reduce(NormBwdArgs p, NormBwdPlan pl) {
+// Column sums of partial rows.  Jobs 0 and 1 (dw_pre, dw_post) add the
+// workgroups' rows, job 2 + g (dgate row g) the rows of its units: a workgroup
+// takes 32 columns, its 128 row lanes add every 128th row and meet in LDS in a
+// fixed order.
+__device__ __forceinline__ void store_dgate(const NormBwdArgs& p, int64_t g, int c, const float4 t) {
+    if (p.dgate32)
+        *reinterpret_cast<float4*>(static_cast<float*>(p.dgate) + g * p.ld_dgate + c) = t;
+    else
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dgate) + g * p.ld_dgate + c) =
+            make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
+}
+
+constexpr int kRedCols = 32, kRedRows = 128, kRedThreads = kRedCols / 4 * kRedRows;
+__global__ void __launch_bounds__(kRedThreads) k_col_reduce(NormBwdArgs p, NormBwdPlan pl) {
     __shared__ float4 acc[kRedRows][kRedCols / 4];
     const int tx = threadIdx.x % (kRedCols / 4), ty = threadIdx.x / (kRedCols / 4);
     const int c = blockIdx.x * kRedCols + 4 * tx;
     const int j = blockIdx.y;
-    const bool gate = j >= 2;
     const float* src = j == 0 ? pl.ws_pre : j == 1 ? pl.ws_post : pl.ws_gate + (int64_t)(j - 2) * pl.splits * p.cols;
-    const int64_t n = gate ? pl.splits : pl.slots;
+    const int64_t n = j >= 2 ? pl.splits : pl.slots;
     if ((j == 0 && !p.dw_pre) || (j == 1 && !p.dw_post)) return;
     float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
     if (c < p.cols) {
+#pragma unroll 4
         for (int64_t r = ty; r < n; r += kRedRows) {
             const float4 v = *reinterpret_cast<const float4*>(src + r * p.cols + c);
             a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
@@ -313,34 +408,52 @@ __global__ void __launch_bounds__(1024) k_col_reduce(NormBwdArgs p, NormBwdPlan 
     }
     if (ty == 0 && c < p.cols) {
         const float4 t = acc[0][tx];
-        if (!gate) {
-            *reinterpret_cast<float4*>((j == 0 ? p.dw_pre : p.dw_post) + c) = t;
-        } else if (p.dgate32) {
-            *reinterpret_cast<float4*>(static_cast<float*>(p.dgate) + (int64_t)(j - 2) * p.ld_dgate + c) = t;
-        } else {
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.dgate) + (int64_t)(j - 2) * p.ld_dgate + c) =
-                make_uint2(pack_bf16x2(t.x, t.y), pack_bf16x2(t.z, t.w));
-        }
+        if (j < 2) *reinterpret_cast<float4*>((j == 0 ? p.dw_pre : p.dw_post) + c) = t;
+        else store_dgate(p, j - 2, c, t);
     }
 }
 
-template <int NV, bool MULTI, bool GACC>
+// Gate rows of few units (at most kFewUnits): a thread adds four columns of
+// one.  (8192x2048 with a gate row per 33 rows, two units each: 99 us with a
+// workgroup per 32 columns of every gate row, see below for this one.)
+constexpr int kFewUnits = 32;
+__global__ void __launch_bounds__(256) k_gate_reduce(NormBwdArgs p, NormBwdPlan pl) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x, per = p.cols >> 2;
+    if (i >= pl.groups * per) return;
+    const int64_t g = i / per;
+    const int c = (int)(i - g * per) * 4;
+    const float* src = pl.ws_gate + g * pl.splits * p.cols + c;
+    float4 a = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+    for (int64_t r = 0; r < pl.splits; ++r) {
+        const float4 v = *reinterpret_cast<const float4*>(src + r * p.cols);
+        a.x += v.x; a.y += v.y; a.z += v.z; a.w += v.w;
+    }
+    store_dgate(p, g, c, a);
+}
+
+template <int NV, bool MULTI, int GATE>
 hipError_t launch_types(const NormBwdArgs& p, const NormBwdPlan& pl, hipStream_t st) {
-    const auto k = p.res32 ? (p.dy32 ? k_block_norm_bwd<NV, true, true, MULTI, GACC>
-                                     : k_block_norm_bwd<NV, true, false, MULTI, GACC>)
-                           : (p.dy32 ? k_block_norm_bwd<NV, false, true, MULTI, GACC>
-                                     : k_block_norm_bwd<NV, false, false, MULTI, GACC>);
+    const auto k = p.res32 ? (p.dy32 ? k_block_norm_bwd<NV, true, true, MULTI, GATE>
+                                     : k_block_norm_bwd<NV, true, false, MULTI, GATE>)
+                           : (p.dy32 ? k_block_norm_bwd<NV, false, true, MULTI, GATE>
+                                     : k_block_norm_bwd<NV, false, false, MULTI, GATE>);
     hipLaunchKernelGGL(k, dim3((unsigned)pl.slots), dim3(MULTI ? 64 * pl.wpr : 64 * kWaves), 0, st, p, pl);
     return hipGetLastError();
 }
 
 template <int NV>
 hipError_t launch_nv(const NormBwdArgs& p, const NormBwdPlan& pl, hipStream_t st) {
-    if constexpr (NV <= 2) {
-        if (pl.wpr == 1)
-            return pl.grouped ? launch_types<NV, false, true>(p, pl, st) : launch_types<NV, false, false>(p, pl, st);
+    if constexpr (NV == 1) {
+        if (pl.wpr == 1) {
+            return pl.grouped ? launch_types<NV, false, kGateSum>(p, pl, st)
+                   : p.gate   ? launch_types<NV, false, kGateRow>(p, pl, st)
+                              : launch_types<NV, false, kGateNone>(p, pl, st);
+        }
     }
-    return pl.grouped ? launch_types<NV, true, true>(p, pl, st) : launch_types<NV, true, false>(p, pl, st);
+    return pl.grouped ? launch_types<NV, true, kGateSum>(p, pl, st)
+           : p.gate   ? launch_types<NV, true, kGateRow>(p, pl, st)
+                      : launch_types<NV, true, kGateNone>(p, pl, st);
 }
 
 }  // namespace
@@ -348,26 +461,30 @@ hipError_t launch_nv(const NormBwdArgs& p, const NormBwdPlan& pl, hipStream_t st
 NormBwdPlan plan_block_norm_bwd(int64_t rows, int64_t cols, int64_t rows_per_gate, bool dw_pre, bool dw_post,
                                 bool dgate) {
     NormBwdPlan pl{};
-    // two chunks per lane where there are rows enough to walk (4096x2560, one
-    // and two chunks: 44.6 and 39.8 us with the reduction; 16384x2048: 130 and
-    // 132); one where every row can have a workgroup and latency counts
-    row_split(cols, rows <= kSlots ? 1 : 2, &pl.wpr, &pl.nv);
+    row_split(cols, &pl.wpr, &pl.nv);
     pl.grouped = dgate && rows_per_gate > 1;
     pl.unit_rows = pl.grouped ? rows_per_gate : (rows > 0 ? rows : 1);
     const int64_t groups = (rows + pl.unit_rows - 1) / pl.unit_rows;
     const int64_t longest = rows < pl.unit_rows ? rows : pl.unit_rows;
-    // gate rows of few rows go to single waves, whole
-    pl.by_wave = pl.wpr == 1 && pl.grouped && rows_per_gate < 64;
-    int64_t splits = groups > 0 && !pl.by_wave ? kSlots / groups : 1;
+    // Workgroups at most: about 2560 waves of one chunk per lane, equally many
+    // per compute unit (4096x2560, five waves: 256 / 512 / 768 workgroups 40.7 /
+    // 32.9 / 39.9 us; 16384x768, two waves: 512 / 1024 61.4 / 41.1; 4096x5120,
+    // five waves with two chunks: 256 / 512 56.0 / 64.5; 16384x2048 gated, four
+    // waves: 512 / 632 132 / 145).  Every workgroup more costs a row of partial
+    // sums.
+    int64_t most = 2560 / (pl.wpr * pl.nv) / kCUs * kCUs;
+    most = pl.wpr == 1 ? 2 * kCUs : most < kCUs ? kCUs : most > 4 * kCUs ? 4 * kCUs : most;
+    // gate rows of few rows go to single waves, whole, where there are enough
+    pl.by_wave = pl.wpr == 1 && pl.grouped && rows_per_gate < 64 && groups >= 2048;
+    int64_t splits = groups > 0 && !pl.by_wave ? most / groups : 1;
     if (splits < 1) splits = 1;
-    if (splits > longest) splits = longest > 0 ? longest : 1;
-    pl.chunk = (longest + splits - 1) / splits;
-    if (pl.chunk < 1) pl.chunk = 1;
-    pl.splits = (longest + pl.chunk - 1) / pl.chunk;
-    if (pl.splits < 1) pl.splits = 1;
+    const int64_t at_once = pl.wpr == 1 && !pl.by_wave ? kWaves : 1;
+    if (splits > (longest + at_once - 1) / at_once) splits = (longest + at_once - 1) / at_once;
+    if (splits < 1) splits = 1;
+    pl.splits = splits;
     pl.units = groups * pl.splits;
     const int64_t want = pl.by_wave ? (pl.units + kWaves - 1) / kWaves : pl.units;
-    pl.slots = (int32_t)(want < kSlots ? want : kSlots);
+    pl.slots = (int32_t)(want < most ? want : most);
     pl.groups = groups;
     size_t f = 0;
     pl.off_pre = f;
@@ -391,16 +508,20 @@ hipError_t launch_block_norm_bwd(const NormBwdArgs& p, float* ws, hipStream_t st
             case 1: e = launch_nv<1>(p, pl, st); break;
             case 2: e = launch_nv<2>(p, pl, st); break;
             case 3: e = launch_nv<3>(p, pl, st); break;
-            case 4: e = launch_nv<4>(p, pl, st); break;
-            default: e = launch_nv<kMaxNv>(p, pl, st); break;
+            default: e = launch_nv<4>(p, pl, st); break;
         }
         if (e != hipSuccess) return e;
     }
-    const bool gate = p.rows > 0 && pl.grouped && pl.splits > 1;
-    if (!p.dw_pre && !p.dw_post && !gate) return e;
+    const bool gate = p.rows > 0 && pl.grouped && pl.splits > 1, few = pl.splits <= kFewUnits;
+    if (gate && few) {
+        hipLaunchKernelGGL(k_gate_reduce, dim3((unsigned)((pl.groups * (p.cols / 4) + 255) / 256)), dim3(256), 0, st, p,
+                           pl);
+        if ((e = hipGetLastError()) != hipSuccess) return e;
+    }
+    if (!p.dw_pre && !p.dw_post && (!gate || few)) return e;
     hipLaunchKernelGGL(k_col_reduce, dim3((unsigned)((p.cols + kRedCols - 1) / kRedCols),
-                                          (unsigned)(2 + (gate ? pl.groups : 0))),
-                       dim3(1024), 0, st, p, pl);
+                                          (unsigned)(2 + (gate && !few ? pl.groups : 0))),
+                       dim3(kRedThreads), 0, st, p, pl);
     return hipGetLastError();
 }
 

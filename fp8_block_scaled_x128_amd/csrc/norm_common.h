@@ -5,28 +5,39 @@
 // the 8-column chunks l, l + 64 wpr, ..., NV of them.  All but the last chunk
 // of a lane are inside the row, so only the last is guarded.
 #pragma once
+#include <type_traits>
+
 #include "device_common.h"
 #include "internal.h"
 #include "reduce.h"
 
 namespace fp8bs {
 
-// Eight elements as loaded.  They stay packed until they are used, so that a
+// Start of a row.  Uniform over the wave: with a 32-bit chunk offset the
+// accesses need no 64-bit address per lane.
+template <bool F32, typename T>
+__device__ __forceinline__ T* row_ptr(T* p, int64_t row, int64_t ld) {
+    using C = std::conditional_t<std::is_const<T>::value, const char, char>;
+    return reinterpret_cast<T*>(reinterpret_cast<C*>(p) + row * ld * (F32 ? 4 : 2));
+}
+
+// Eight elements (chunk c of a row) as loaded.  They stay packed until they are used, so that a
 // row's loads are all in flight before the first conversion waits for one.
 template <bool F32>
 struct Raw8 {
     uint4 r[F32 ? 2 : 1];
-    __device__ __forceinline__ void load(const void* p, int64_t i) {
-        if (F32) {
-            const float* f = static_cast<const float*>(p) + i;
-            r[0] = load_nt16(f);
-            r[F32 ? 1 : 0] = load_nt16(f + 4);
-        } else {
-            r[0] = load_nt16(static_cast<const uint16_t*>(p) + i);
-        }
+    __device__ __forceinline__ void load(const void* row, uint32_t c) {
+        const char* p = static_cast<const char*>(row) + c * (F32 ? 32u : 16u);
+        r[0] = load_nt16(p);
+        if (F32) r[F32 ? 1 : 0] = load_nt16(p + 16);
     }
-    __device__ __forceinline__ void load_shared(const void* p, int64_t i) {     // bf16, cached policy
-        r[0] = *reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i);
+    __device__ __forceinline__ void load_shared(const void* row, uint32_t c) {     // bf16, cached policy
+        r[0] = *reinterpret_cast<const uint4*>(static_cast<const char*>(row) + c * 16u);
+    }
+    // Makes the compiler convert again after this point instead of keeping the
+    // fp32 values of the last get() (twice the registers of bf16) until then.
+    __device__ __forceinline__ void forget() {
+        if (!F32) asm volatile("" : "+v"(r[0].x), "+v"(r[0].y), "+v"(r[0].z), "+v"(r[0].w));
     }
     __device__ __forceinline__ void zero() {
         r[0] = make_uint4(0, 0, 0, 0);
@@ -45,36 +56,36 @@ struct Raw8 {
     }
 };
 
-// Norm weights and gates: rows share them, so they keep the cached policy.
-__device__ __forceinline__ void load8_shared(const void* p, int64_t i, bool f32, float v[8]) {
+// Norm weights: rows share them, so they keep the cached policy.
+__device__ __forceinline__ void load8_shared(const void* row, uint32_t c, bool f32, float v[8]) {
     if (f32) {
-        const float4* f = reinterpret_cast<const float4*>(static_cast<const float*>(p) + i);
+        const float4* f = reinterpret_cast<const float4*>(static_cast<const char*>(row) + c * 32u);
         const float4 a = f[0], b = f[1];
         v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
         v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
     } else {
-        unpack8(*reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(p) + i), v);
+        unpack8(*reinterpret_cast<const uint4*>(static_cast<const char*>(row) + c * 16u), v);
     }
 }
 template <bool F32>
-__device__ __forceinline__ void store8(void* p, int64_t i, const float v[8]) {
+__device__ __forceinline__ void store8(void* row, uint32_t c, const float v[8]) {
+    char* p = static_cast<char*>(row) + c * (F32 ? 32u : 16u);
     if (F32) {
-        float4* f = reinterpret_cast<float4*>(static_cast<float*>(p) + i);
-        f[0] = make_float4(v[0], v[1], v[2], v[3]);
-        f[1] = make_float4(v[4], v[5], v[6], v[7]);
+        reinterpret_cast<float4*>(p)[0] = make_float4(v[0], v[1], v[2], v[3]);
+        reinterpret_cast<float4*>(p)[1] = make_float4(v[4], v[5], v[6], v[7]);
     } else {
-        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p) + i) =
-            make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]), pack_bf16x2(v[4], v[5]),
-                       pack_bf16x2(v[6], v[7]));
+        *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]),
+                                                  pack_bf16x2(v[4], v[5]), pack_bf16x2(v[6], v[7]));
     }
 }
 
+constexpr int kCUs = 256;            // compute units
 constexpr int kMaxRowWaves = 8;      // waves that share a row
-constexpr int kMaxNv = 8;            // chunks per lane: 8 * 8 * 64 chunks of 8 = 32768 columns
-// Chunks that are inside the row for every lane: the host launches NV <= 4
-// only for rows that need the last chunk, and NV 8 for 5 to 8.
+// Chunks per lane: at most 4 (8 waves x 64 lanes x 4 chunks of 8 = 16384
+// columns).  The host launches NV only for rows that need the last chunk, so
+// the others are inside the row for every lane.
 template <int NV>
-constexpr int kSure = NV <= 4 ? NV - 1 : 4;
+constexpr int kSure = NV - 1;
 
 // Sum of squares of eight values, as a tree: three roundings deep.
 __device__ __forceinline__ float sumsq8(const float v[8]) {
@@ -120,14 +131,13 @@ __device__ __forceinline__ void row_sums(float (&v)[K], int wpr, float (*lds)[kM
     }
 }
 
-// Waves per row and chunks per lane: `chunks` per lane if eight waves then
-// hold the row, else the fewest that do.
-inline void row_split(int64_t cols, int chunks, int* wpr, int* nv) {
+// Waves per row and chunks per lane: one chunk per lane while eight waves hold
+// the row, then the fewest chunks that do.  (Forward and backward with one and
+// two chunks per lane, 4096x2560: 21.8 / 23.0 and 37.3 / 38.9 us.)
+inline void row_split(int64_t cols, int* wpr, int* nv) {
     const int64_t groups = (cols / 8 + 63) / 64;            // chunks of 64 lanes
-    int64_t n = (groups + kMaxRowWaves - 1) / kMaxRowWaves;
-    if (n < chunks) n = chunks < groups ? chunks : groups;
-    *wpr = (int)((groups + n - 1) / n);
-    *nv = (int)((groups + *wpr - 1) / *wpr);
+    *nv = (int)((groups + kMaxRowWaves - 1) / kMaxRowWaves);
+    *wpr = (int)((groups + *nv - 1) / *nv);
 }
 
 }  // namespace fp8bs

@@ -53,6 +53,19 @@ __device__ __forceinline__ uint32_t row16_umin(uint32_t v) {
     return v;
 }
 
+// v + v of the lane 16, then 32 lanes away.  The swaps exchange the odd rows
+// (of 16 or 32 lanes) of their first operand with the even rows of the second;
+// given v twice they return the even rows' and the odd rows' values in every
+// row.
+__device__ __forceinline__ float rows_sum(float v) {
+    const uint32_t a = __float_as_uint(v);
+    const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    const uint32_t b = __float_as_uint(v);
+    const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
 // All-reduce over LANES lanes (16: a DPP row, 64: the wave).  The four rows of
 // a wave meet in scalar registers: no LDS crossbar, and the result is uniform.
 // Every lane of the wave must be active.

@@ -87,10 +87,10 @@ __device__ __forceinline__ void block_sums(float (&v)[K], float* lds) {
 }
 
 // LDS of a selecting workgroup: the experts' token masks, and the probability
-// sums of half of its waves [8][E] (the halves take turns: 1024 experts would
+// sums of half of its waves [8][L V] (the halves take turns: 1024 experts would
 // pass 64 KB otherwise).
 constexpr int kHalf = kThreads / 128;
-__host__ __device__ constexpr size_t select_lds(int E) { return (size_t)E * (8 + 4 * kHalf); }
+__host__ __device__ constexpr size_t select_lds(int E, int lv) { return (size_t)E * 8 + (size_t)lv * 4 * kHalf; }
 
 // Selection.  L lanes hold a token's logits, lane l the experts l, l + L, ...
 // Each of the k rounds takes the largest key among the lanes and, of equal
@@ -119,7 +119,8 @@ __device__ __forceinline__ float2 select_tokens(const RouteArgs& p, int64_t t0, 
         uint32_t best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            left[i] = (have && l + i * L < p.E) ? logit_key(z[i]) : 0u;
+            // a mask, not a choice: no branch around each key
+            left[i] = logit_key(z[i]) & ((have && l + i * L < p.E) ? 0xffffffffu : 0u);
             best = max(best, left[i]);
         }
         const uint32_t top = lanes_umax<L>(best);
@@ -183,29 +184,27 @@ __device__ __forceinline__ float2 select_tokens(const RouteArgs& p, int64_t t0, 
             }
         }
     }
-    // the 64 / L groups of a wave by shuffles, waves w and w + 8, then those in
-    // order
+    // the 64 / L groups of a wave in registers, waves w and w + 8, then those
+    // in order
     const int wave = threadIdx.x >> 6;
+    float* mine = psum + (wave & (kHalf - 1)) * (L * V) + l;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        if (L == 16) {
-            acc[i] += __shfl_xor(acc[i], 16, 64);
-            acc[i] += __shfl_xor(acc[i], 32, 64);
-        }
-        const int e = l + i * L;
-        if (wave >= kHalf && (threadIdx.x & 63) < L && e < p.E) psum[(wave - kHalf) * p.E + e] = acc[i];
+    for (int i = 0; i < V; ++i)
+        if (L == 16) acc[i] = rows_sum(acc[i]);
+    if (wave >= kHalf && (threadIdx.x & 63) < L) {
+#pragma unroll
+        for (int i = 0; i < V; ++i) mine[i * L] = acc[i];
     }
     __syncthreads();
+    if (wave < kHalf && (threadIdx.x & 63) < L) {
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int e = l + i * L;
-        if (wave < kHalf && (threadIdx.x & 63) < L && e < p.E) psum[wave * p.E + e] += acc[i];
+        for (int i = 0; i < V; ++i) mine[i * L] += acc[i];
     }
     block_sums(sums, red);                          // its barrier covers psum and mask too
     for (int e = threadIdx.x; e < p.E; e += kThreads) {
         float s = 0.0f;
 #pragma unroll
-        for (int w = 0; w < kHalf; ++w) s += psum[w * p.E + e];
+        for (int w = 0; w < kHalf; ++w) s += psum[w * (L * V) + e];
         psum[e] = s;                                // column e is this thread's alone
     }
     return make_float2(sums[0], sums[1]);
@@ -238,7 +237,7 @@ __global__ void __launch_bounds__(kThreads) k_route_one(RouteArgs p) {
     extern __shared__ __align__(16) unsigned char dyn[];
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(dyn);
     float* psum = reinterpret_cast<float*>(mask + p.E);
-    int* counts = reinterpret_cast<int*>(psum + p.E * kHalf);
+    int* counts = reinterpret_cast<int*>(psum + L * V * kHalf);
     int* base = counts + p.E;                       // [E + 1]
     __shared__ float red[16];
     for (int e = threadIdx.x; e < p.E; e += kThreads) mask[e] = 0;
@@ -294,12 +293,15 @@ __device__ __forceinline__ void add_bytes(uint32_t (&a)[8], const uint4 v) {
     }
 }
 
-// Second launch, up to kDirect workgroups of tokens: every workgroup adds the
-// histograms of all workgroups and of those before it (32 KB from the L2 at
-// 16384 tokens and 128 experts), scans the counts over the experts and places
-// its tokens' rows; one more workgroup forms the counts, offsets and losses.
-// Sums of at most 512 x 64 fit 16 bits.
-constexpr int kDirect = 512;
+// Last launch: every workgroup adds the histograms of all workgroups and of
+// those before it (32 KB from the L2 at 16384 tokens and 128 experts), scans
+// the counts over the experts and places its tokens' rows; one more workgroup
+// forms the counts, offsets and losses.  More than kDirect workgroups of
+// tokens (SUPER) are first added up in runs of kRun by k_route_super, and a
+// workgroup adds the runs and the histograms of its own run.  Sums of at most
+// 512 x 64 fit 16 bits.
+constexpr int kDirect = 512, kRun = 256;
+template <bool SUPER>
 __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs ws, int nblk) {
     extern __shared__ __align__(16) unsigned char dyn[];
     const int epad = ws.epad, nch = epad >> 4;      // chunks of 16 experts: a power of two, at most 64
@@ -322,7 +324,8 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
 #pragma unroll
     for (int i = 0; i < 8; ++i) tot[i] = pre[i] = 0;
     const int ch = threadIdx.x & (nch - 1), rows = kThreads / nch;
-    for (int b = threadIdx.x / nch; b < nblk; b += rows) {
+    const int b1 = SUPER ? max(blk, 0) : nblk, b0 = SUPER ? b1 & ~(kRun - 1) : 0;
+    for (int b = b0 + threadIdx.x / nch; b < b1; b += rows) {
         const uint4 v = *reinterpret_cast<const uint4*>(ws.hist + (int64_t)b * epad + 16 * ch);
         add_bytes(tot, v);
         if (b < blk) add_bytes(pre, v);
@@ -351,6 +354,19 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
     for (int u = 0; u < 2; ++u)
         if (es[u] >= 0) atomicOr(&mask[es[u]], 1ull << ((uint32_t)(threadIdx.x + u * kThreads) / (uint32_t)p.k));
     int before = 0;
+    // an expert's runs: a lane of its own per expert and row lane, met in LDS
+    int* runs = reinterpret_cast<int*>(part + kHalf * epad);          // [2][kThreads]
+    int rtot = 0, rpre = 0;
+    const int nrun = SUPER ? (nblk + kRun - 1) / kRun : 0;
+    if (SUPER) {
+        const int e = threadIdx.x & (epad - 1);
+#pragma unroll 8
+        for (int r = threadIdx.x / epad; r < nrun; r += kThreads / epad) {
+            const int c = ws.run_cnt[(int64_t)r * epad + e];
+            rtot += c;
+            if (r < blk / kRun) rpre += c;
+        }
+    }
     if ((int)threadIdx.x < epad) {
         const int e = threadIdx.x, i = e & 15;
         const int word = 2 * (i >> 2) + (i & 1), sh = (i & 2) * 8;
@@ -360,9 +376,20 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
             c += (int)((src[word] >> sh) & 0xffffu);
             before += (int)((src[8 + word] >> sh) & 0xffffu);
         }
-        counts[e] = c;
+        counts[e] = SUPER ? 0 : c;
     }
     __syncthreads();
+    if (SUPER) {
+        runs[threadIdx.x] = rtot;
+        runs[kThreads + threadIdx.x] = rpre;
+        __syncthreads();
+        if ((int)threadIdx.x < epad) {
+            int c = 0;
+            for (int r = threadIdx.x; r < kThreads; r += epad) { c += runs[r]; before += runs[kThreads + r]; }
+            counts[threadIdx.x] = c;
+        }
+        __syncthreads();
+    }
     scan_experts(counts, base, p.E);
     __syncthreads();
     const int total = base[p.E];
@@ -378,13 +405,13 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
         return;
     }
     __shared__ float red[48];
-    float s[3] = {0.0f, 0.0f, 0.0f};                // counts . probabilities, lse^2, tokens (at most 2^15)
+    float s[3] = {0.0f, 0.0f, 0.0f};                // counts . probabilities, lse^2, tokens (at most 2^22: exact)
     // four experts per thread, every (4096 / epad)-th workgroup's
     const int e4 = (threadIdx.x * 4) & (epad - 1), prows = kThreads * 4 / epad;
     const float c0 = (float)counts[e4], c1 = (float)counts[e4 + 1], c2 = (float)counts[e4 + 2], c3 = (float)counts[e4 + 3];
 #pragma unroll 8
-    for (int b = threadIdx.x * 4 / epad; b < nblk; b += prows) {
-        const float4 v = *reinterpret_cast<const float4*>(ws.psum + (int64_t)b * epad + e4);
+    for (int b = threadIdx.x * 4 / epad; b < (SUPER ? nrun : nblk); b += prows) {
+        const float4 v = *reinterpret_cast<const float4*>((SUPER ? ws.run_psum : ws.psum) + (int64_t)b * epad + e4);
         s[0] += __builtin_fmaf(c0, v.x, c1 * v.y) + __builtin_fmaf(c2, v.z, c3 * v.w);
     }
     for (int b = threadIdx.x; b < nblk; b += kThreads) { s[1] += ws.lse2[b]; s[2] += (float)ws.live[b]; }
@@ -396,111 +423,32 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
     if (threadIdx.x == 0) write_losses(p, s[0], s[1], total, (int)s[2]);
 }
 
-// More workgroups than that, second launch: for 16 experts, the running row
-// count over the workgroups and the sums of counts and probabilities.  Every
-// thread takes a run of workgroups, twice: for its sums, and after their scan
-// over the threads for the counts before each.
-__global__ void __launch_bounds__(kThreads) k_route_scan(RouteArgs p, RouteWs ws, int nblk) {
-    __shared__ int lds[kThreads / 64][16];
-    __shared__ float ldp[16][kThreads / 16 + 1];
-    const int per = (nblk + kThreads - 1) / kThreads, lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    const int b0 = min((int)threadIdx.x * per, nblk), b1 = min(b0 + per, nblk);
-    const uint8_t* src = ws.hist + 16 * blockIdx.x;
-    int sum[16], run[16];
-#pragma unroll
-    for (int i = 0; i < 16; ++i) sum[i] = 0;
-#pragma unroll 2
-    for (int b = b0; b < b1; ++b) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src + (int64_t)b * ws.epad);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-#pragma unroll
-        for (int i = 0; i < 16; ++i) sum[i] += (int)((w[i >> 2] >> (8 * (i & 3))) & 0xffu);
-    }
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        run[i] = sum[i];
-#pragma unroll
-        for (int d = 1; d < 64; d <<= 1) {
-            const int o = __shfl_up(run[i], d, 64);
-            if (lane >= d) run[i] += o;
-        }
-        if (lane == 63) lds[wave][i] = run[i];
-    }
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        int before = 0, all = 0;
-        for (int w = 0; w < kThreads / 64; ++w) {
-            if (w < wave) before += lds[w][i];
-            all += lds[w][i];
-        }
-        run[i] += before - sum[i];
-        const int e = 16 * blockIdx.x + i;
-        if (threadIdx.x == 0 && e < p.E) p.counts[e] = all;
-    }
-#pragma unroll 2
-    for (int b = b0; b < b1; ++b) {
-        const uint4 v = *reinterpret_cast<const uint4*>(src + (int64_t)b * ws.epad);
-        const uint32_t w[4] = {v.x, v.y, v.z, v.w};
-        int4* dst = reinterpret_cast<int4*>(ws.base + (int64_t)b * ws.epad + 16 * blockIdx.x);
-#pragma unroll
-        for (int i = 0; i < 4; ++i) dst[i] = make_int4(run[4 * i], run[4 * i + 1], run[4 * i + 2], run[4 * i + 3]);
-#pragma unroll
-        for (int i = 0; i < 16; ++i) run[i] += (int)((w[i >> 2] >> (8 * (i & 3))) & 0xffu);
-    }
-    // probabilities: thread (e, r) adds every 64th workgroup's, then e's threads in order
-    const int e = 16 * blockIdx.x + (threadIdx.x & 15);
+// Counts and probability sums of runs of kRun workgroups, in order.  A
+// workgroup takes one run and 64 experts; its 16 row lanes take 16 rows each.
+__global__ void __launch_bounds__(kThreads) k_route_super(RouteArgs p, RouteWs ws, int nblk) {
+    __shared__ int cnt[16][64];
+    __shared__ float prob[16][64];
+    const int r = threadIdx.x >> 6, l = threadIdx.x & 63, e = blockIdx.y * 64 + l;
+    const int b0 = blockIdx.x * kRun + r * (kRun / 16);
+    int c = 0;
     float f = 0.0f;
-    if (e < p.E)
-        for (int b = threadIdx.x >> 4; b < nblk; b += kThreads / 16) f += ws.psum[(int64_t)b * ws.epad + e];
-    ldp[threadIdx.x & 15][threadIdx.x >> 4] = f;
+    if (e < ws.epad) {
+#pragma unroll
+        for (int i = 0; i < kRun / 16; ++i) {
+            const int64_t at = (int64_t)min(b0 + i, nblk - 1) * ws.epad + e;
+            const int h = ws.hist[at];
+            const float v = ws.psum[at];
+            c += b0 + i < nblk ? h : 0;
+            f += b0 + i < nblk ? v : 0.0f;
+        }
+    }
+    cnt[r][l] = c;
+    prob[r][l] = f;
     __syncthreads();
-    if (threadIdx.x < 16 && e < p.E) {
-        float s = 0.0f;
-        for (int r = 0; r < kThreads / 16; ++r) s += ldp[threadIdx.x][r];
-        ws.total[e] = s;
-    }
-}
-
-// ... and third launch: as k_route_place from the scanned counts.
-__global__ void __launch_bounds__(kThreads) k_route_place_scanned(RouteArgs p, RouteWs ws, int nblk) {
-    extern __shared__ __align__(16) unsigned char dyn[];
-    unsigned long long* mask = reinterpret_cast<unsigned long long*>(dyn);
-    int* counts = reinterpret_cast<int*>(mask + p.E);
-    int* base = counts + p.E;                       // [E + 1]
-    __shared__ float red[32];
-    __shared__ int s_live;
-    const int64_t t0 = (int64_t)blockIdx.x * kTok;
-    const bool tokens = (int)blockIdx.x < nblk;
-    const int n = tokens ? (int)min((int64_t)kTok, p.T - t0) * p.k : 0;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) { mask[e] = 0; counts[e] = p.counts[e]; }
-    if (threadIdx.x == 0) s_live = 0;
-    __syncthreads();
-    scan_experts(counts, base, p.E);
-    for (int i = threadIdx.x; i < n; i += kThreads) {
-        const int e = p.experts[t0 * p.k + i];
-        if (e >= 0) atomicOr(&mask[e], 1ull << ((uint32_t)i / (uint32_t)p.k));
-    }
-    __syncthreads();
-    const int total = base[p.E];
-    if (tokens) {
-        __syncthreads();
-        if ((int)threadIdx.x < p.E) base[threadIdx.x] += ws.base[(int64_t)blockIdx.x * ws.epad + threadIdx.x];
-        __syncthreads();
-        for (int i = threadIdx.x; i < n; i += kThreads) place_row(p, t0, i, p.experts[t0 * p.k + i], mask, base, total);
-        return;
-    }
-    float s[2] = {0.0f, 0.0f};
-    int live = 0;
-    for (int e = threadIdx.x; e < p.E; e += kThreads) s[0] = __builtin_fmaf((float)counts[e], ws.total[e], s[0]);
-    for (int b = threadIdx.x; b < nblk; b += kThreads) { s[1] += ws.lse2[b]; live += ws.live[b]; }
-    atomicAdd(&s_live, live);                       // whole numbers: any order gives the same
-    block_sums(s, red);                             // its barrier covers s_live too
-    for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = base[e];
-    if (threadIdx.x == 0) {
-        p.counts[p.E] = s_live;
-        write_losses(p, s[0], s[1], total, s_live);
-    }
+    if (r > 0 || e >= ws.epad) return;
+    for (int i = 1; i < 16; ++i) { c += cnt[i][l]; f += prob[i][l]; }
+    ws.run_cnt[(int64_t)blockIdx.x * ws.epad + e] = c;
+    ws.run_psum[(int64_t)blockIdx.x * ws.epad + e] = f;
 }
 
 // Backward.  Each term of the gradient at z_te:
@@ -563,7 +511,7 @@ __global__ void __launch_bounds__(256) k_route_bwd(RouteBwdArgs p) {
         uint32_t key[V], best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
-            key[i] = (live && l + i * L < p.E) ? logit_key(z[i]) : 0u;
+            key[i] = logit_key(z[i]) & ((live && l + i * L < p.E) ? 0xffffffffu : 0u);
             best = max(best, key[i]);
         }
         const float m = key_logit(lanes_umax<L>(best));
@@ -614,7 +562,7 @@ hipError_t by_experts(int E, A&&... a) {
     if (E <= 32) return F<16, 2>::run(a...);
     if (E <= 64) return F<16, 4>::run(a...);
     if (E <= 128) return F<16, 8>::run(a...);
-    if (E <= 256) return F<64, 4>::run(a...);
+    if (E <= 256) return F<16, 16>::run(a...);
     if (E <= 512) return F<64, 8>::run(a...);
     return F<64, 16>::run(a...);
 }
@@ -623,11 +571,11 @@ template <int L, int V>
 struct Select {
     static hipError_t run(const RouteArgs& p, const RouteWs& ws, int nblk, hipStream_t st) {
         if (nblk <= 1) {
-            const size_t lds = select_lds(p.E) + (size_t)p.E * 8 + 8;
+            const size_t lds = select_lds(p.E, L * V) + (size_t)p.E * 8 + 8;
             if (p.logits32) hipLaunchKernelGGL((k_route_one<L, V, true>), dim3(1), dim3(kThreads), lds, st, p);
             else hipLaunchKernelGGL((k_route_one<L, V, false>), dim3(1), dim3(kThreads), lds, st, p);
         } else {
-            const size_t lds = select_lds(p.E);
+            const size_t lds = select_lds(p.E, L * V);
             if (p.logits32) hipLaunchKernelGGL((k_route_select<L, V, true>), dim3(nblk), dim3(kThreads), lds, st, p, ws);
             else hipLaunchKernelGGL((k_route_select<L, V, false>), dim3(nblk), dim3(kThreads), lds, st, p, ws);
         }
@@ -652,7 +600,7 @@ struct Backward {
 
 // Workspace: per workgroup of tokens the histogram bytes [epad] and the
 // probability sums [epad]; per workgroup the loss terms; for more than kDirect of
-// them the scanned counts [epad] and the sums [E].
+// them the runs' counts and probability sums [epad].
 static RouteWs route_ws(int64_t T, int32_t E, void* base, size_t* bytes) {
     const int64_t nblk = (T + kTok - 1) / kTok;
     RouteWs ws{};
@@ -667,8 +615,9 @@ static RouteWs route_ws(int64_t T, int32_t E, void* base, size_t* bytes) {
         ws.live = reinterpret_cast<int32_t*>(take((size_t)nblk * 4));
     }
     if (nblk > kDirect) {
-        ws.base = reinterpret_cast<int32_t*>(take((size_t)nblk * ws.epad * 4));
-        ws.total = reinterpret_cast<float*>(take((size_t)E * 4));
+        const size_t n = (size_t)((nblk + kRun - 1) / kRun) * ws.epad * 4;
+        ws.run_cnt = reinterpret_cast<int32_t*>(take(n));
+        ws.run_psum = reinterpret_cast<float*>(take(n));
     }
     *bytes = off;
     return ws;
@@ -686,14 +635,15 @@ hipError_t launch_moe_route(const RouteArgs& p, void* wsp, hipStream_t st) {
     const RouteWs ws = route_ws(p.T, p.E, wsp, &bytes);
     hipError_t e = by_experts<Select>(p.E, p, ws, nblk, st);
     if (e != hipSuccess || nblk <= 1) return e;
+    const size_t lds = (size_t)ws.epad * 16 + 16 + (size_t)kThreads * 8 + (size_t)kHalf * ws.epad * 4;
     if (nblk <= kDirect) {
-        const size_t lds = (size_t)ws.epad * 16 + 16 + (size_t)kHalf * ws.epad * 4;
-        hipLaunchKernelGGL(k_route_place, dim3(nblk + 1), dim3(kThreads), lds, st, p, ws, nblk);
+        hipLaunchKernelGGL(k_route_place<false>, dim3(nblk + 1), dim3(kThreads), lds, st, p, ws, nblk);
         return hipGetLastError();
     }
-    hipLaunchKernelGGL(k_route_scan, dim3((p.E + 15) / 16), dim3(kThreads), 0, st, p, ws, nblk);
+    hipLaunchKernelGGL(k_route_super, dim3((nblk + kRun - 1) / kRun, (ws.epad + 63) / 64), dim3(kThreads), 0, st, p, ws,
+                       nblk);
     if ((e = hipGetLastError()) != hipSuccess) return e;
-    hipLaunchKernelGGL(k_route_place_scanned, dim3(nblk + 1), dim3(kThreads), (size_t)p.E * 16 + 8, st, p, ws, nblk);
+    hipLaunchKernelGGL(k_route_place<true>, dim3(nblk + 1), dim3(kThreads), lds, st, p, ws, nblk);
     return hipGetLastError();
 }
 

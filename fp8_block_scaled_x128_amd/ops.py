@@ -112,20 +112,21 @@ def load():
         return lib
 
 
+# Pointers and streams go to ctypes as plain integers (the argument types are
+# c_void_p): building a c_void_p and a torch Stream object per argument cost
+# more than the smallest kernels run.
 def _p(t):
-    if t is None:
-        return None
-    if isinstance(t, int):
-        return ctypes.c_void_p(t)
-    return ctypes.c_void_p(t.data_ptr())
+    if t is None or isinstance(t, int):
+        return t
+    return t.data_ptr()
 
 
 def _stream(stream=None):
     if stream is None:
-        stream = torch.cuda.current_stream()
+        return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
     if isinstance(stream, int):
-        return ctypes.c_void_p(stream)
-    return ctypes.c_void_p(stream.cuda_stream)
+        return stream
+    return stream.cuda_stream
 
 
 def _check(name, status, raise_on_error=True):
@@ -603,22 +604,25 @@ def _on_device(*tensors):
     live elsewhere are refused."""
     cur = torch.cuda.current_device()
     for t in tensors:
-        if t is not None and (not t.is_cuda or t.get_device() != cur):
+        if t is not None and t.get_device() != cur:            # -1: host memory
             raise ValueError("tensor on %s; the current device is cuda:%d" % (t.device, cur))
 
 
 def _matrix(name, t, rows, cols, *dtypes):
+    """The leading dimension of a [rows, cols] tensor with unit column stride
+    (0 without a tensor)."""
     if t is None:
         return 0
-    if t.dtype not in dtypes or t.dim() != 2 or tuple(t.shape) != (rows, cols) or (t.stride(1) != 1 and cols > 1):
-        raise ValueError("%s: [%d, %d] of %s with unit column stride expected, got %s %s, strides %s"
-                         % (name, rows, cols, "/".join(str(d) for d in dtypes), tuple(t.shape), t.dtype, t.stride()))
-    # a single row's stride is never used: torch may leave anything there
-    return t.stride(0) if rows > 1 else max(t.stride(0), cols)
+    if t.dtype in dtypes and t.shape == (rows, cols):
+        s0, s1 = t.stride()
+        if s1 == 1 or cols <= 1:
+            return s0 if rows > 1 else cols                    # the stride of a single row is never used
+    raise ValueError("%s: [%d, %d] of %s with unit column stride expected, got %s %s, strides %s"
+                     % (name, rows, cols, "/".join(str(d) for d in dtypes), tuple(t.shape), t.dtype, t.stride()))
 
 
 def _vector(name, t, n, *dtypes):
-    if t is not None and (t.dtype not in dtypes or tuple(t.shape) != (n,) or not t.is_contiguous()):
+    if t is not None and (t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous()):
         raise ValueError("%s: contiguous [%d] of %s expected, got %s %s"
                          % (name, n, "/".join(str(d) for d in dtypes), tuple(t.shape), t.dtype))
 
@@ -725,9 +729,9 @@ def block_norm_backward(dy=None, dh=None, h=None, x=None, *, w_pre=None, w_post=
     for name, v in (("w_pre", w_pre), ("w_post", w_post)):
         _vector(name, v, cols, _BF if w is None else w.dtype)
     dev = ref.device
-    need = fp8_block_norm_backward_ws_size(rows, cols, rows_per_gate, w_post is not None, w_pre is not None,
-                                           gate is not None)
     if out is None:
+        need = fp8_block_norm_backward_ws_size(rows, cols, rows_per_gate, w_post is not None, w_pre is not None,
+                                               gate is not None)
         e = lambda n, dt: torch.empty((n, cols), dtype=dt, device=dev)
         out = BlockNormGrads(e(rows, stream_dt) if dres else None, e(rows, _BF) if x is not None else None,
                              e(ngate, dgate_dtype) if gate is not None else None,
@@ -784,9 +788,9 @@ def moe_route(logits, top_k, *, renorm=True, mask=None, out: Optional[Routing] =
     T, E = logits.shape
     ld = _matrix("logits", logits, T, E, _BF, _F32)
     mask = _mask_bytes(mask, T)
-    need = fp8_moe_route_ws_size(T, E)
     dev, i32 = logits.device, torch.int32
     if out is None:
+        need = fp8_moe_route_ws_size(T, E)
         e = lambda *s, dtype=i32: torch.empty(s, dtype=dtype, device=dev)
         out = Routing(e(T, top_k), e(T, top_k, dtype=_F32), e(E + 1), e(E + 1), e(T * top_k), e(T, top_k),
                       e(T, dtype=_F32), e(2, dtype=_F32), _u8((need,), dev) if need else None)

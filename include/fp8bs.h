@@ -539,9 +539,9 @@ fp8bs_status fp8_moe_combine_backward(const void* dout, int64_t ld_dout, fp8bs_o
  * ws : device workspace of fp8_moe_route_ws_size bytes, 16-byte aligned
  *      (nullable when that is 0); its contents on entry are ignored.  Calls
  *      that overlap in time need separate workspaces.
- * The results are the same bits every time.  Requirements: 0 <= T <= 2^26,
- * 1 <= E <= 1024, 1 <= k <= min(E, 32), T * k < 2^31, ld >= E; pointers
- * aligned to their element.
+ * The results are the same bits every time.  Requirements: 0 <= T <= 2^22,
+ * 1 <= E <= 1024, 1 <= k <= min(E, 32), ld >= E; pointers aligned to their
+ * element.
  * ------------------------------------------------------------------------ */
 fp8bs_status fp8_moe_route(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k,
                            int32_t renorm, const uint8_t* mask, int32_t* experts, float* weights, int32_t* counts,
@@ -597,7 +597,7 @@ fp8bs_status fp8_moe_route_backward(const void* logits, int64_t T, int32_t E, in
  * y        : nullable bf16 [rows][ld_y].
  * q, s     : nullable together; codes [rows][ld_q], the scale of (row r,
  *            group g) at s[r * s_stride_row + g * s_stride_group].
- * Requirements: rows, cols >= 0, cols % 8 == 0, cols <= 32768, rows < 2^31;
+ * Requirements: rows, cols >= 0, cols % 8 == 0, cols <= 16384, rows < 2^31;
  * residual or x; w_post and gate only with x; y and q only with w_pre, and
  * w_pre only with one of them; at least one output; eps > 0 and scale finite;
  * leading dimensions >= cols and % 8 == 0; bf16, fp32 and weight pointers

@@ -17,7 +17,7 @@ def norm(rows=4, cols=256, x=A, ld=None, res=A, st=0, gate=None, R=1, scale=1.0,
 
 
 @pytest.mark.parametrize("args,status", [
-    (dict(rows=-1), 2), (dict(cols=100), 2), (dict(cols=32776), 2), (dict(rows=1 << 31), 2), (dict(gate=A, R=0), 2),
+    (dict(rows=-1), 2), (dict(cols=100), 2), (dict(cols=16392), 2), (dict(rows=1 << 31), 2), (dict(gate=A, R=0), 2),
     (dict(st=2), 5), (dict(wt=7), 5), (dict(eps=0.0), 5), (dict(eps=NAN), 5), (dict(eps=INF), 5),
     (dict(scale=NAN), 5), (dict(scale=INF), 5),
     (dict(x=None, res=None, w_post=None), 1), (dict(x=None), 1), (dict(x=None, w_post=None, gate=A), 1),
@@ -75,7 +75,7 @@ def route(T=100, E=16, ld=None, t=1, k=2, renorm=1, z=A, mask=None, experts=A, c
 
 
 @pytest.mark.parametrize("args,status", [
-    (dict(T=-1), 2), (dict(T=(1 << 26) + 1), 2), (dict(T=1 << 26, E=64, k=32), 2), (dict(E=0), 2), (dict(E=1025), 2),
+    (dict(T=-1), 2), (dict(T=(1 << 22) + 1), 2), (dict(E=0), 2), (dict(E=1025), 2),
     (dict(k=0), 2), (dict(k=17), 2), (dict(E=64, k=33), 2), (dict(wsb=8), 2), (dict(t=2), 5), (dict(renorm=2), 5),
     (dict(ld=15), 3), (dict(z=None), 1), (dict(experts=None), 1), (dict(counts=None), 1), (dict(loss=None), 1),
     (dict(lse=None), 1), (dict(ws=None), 1), (dict(z=A + 2), 4), (dict(t=0, z=A + 1), 4), (dict(counts=A + 2), 4),

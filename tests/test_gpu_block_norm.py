@@ -2,7 +2,7 @@
 quantization (fp8_block_norm) and their gradient (fp8_block_norm_backward)
 against 64-bit references.
 
-Bounds: a row's sum of squares is a chain of at most 32 FMAs per lane, 6 lane
+Bounds: a row's sum of squares is a chain of at most 32 terms per lane, 6 lane
 steps and 16 waves, so its relative error is below 54 U and that of its rsqrt
 below 30 U; with the products around it fewer than 64 roundings enter any
 value, on the magnitude of its terms.  In the backward pass two such sums
@@ -38,8 +38,8 @@ def make(rows, cols, kind, stream, wt, gate_rows, seed, pad=0):
     return t
 
 
-SHAPES = [(1, 8), (1, 2560), (3, 128), (5, 1000), (67, 136), (130, 2048), (33, 4104), (9, 9728), (4, 16392),
-          (2, 32768), (1, 512), (700, 64)]
+SHAPES = [(1, 8), (1, 2560), (3, 128), (5, 1000), (67, 136), (130, 2048), (33, 4104), (9, 9728), (4, 12296),
+          (2, 16384), (1, 512), (700, 64)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -61,7 +61,7 @@ def test_forward(rows, cols, kind, stream, wt, gate_rows):
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 8), (1, 2560), (5, 1000), (67, 136), (130, 2048), (33, 4104), (6, 9728),
-                                       (3, 16392), (2, 32768), (2500, 64), (3000, 520)])
+                                       (3, 12296), (2, 16384), (2500, 64), (3000, 520)])
 @pytest.mark.parametrize("kind,stream,wt,gate_rows,dy_dt,dg_dt", [
     ("both", BF, BF, 0, F32, F32), ("both", F32, F32, 1, BF, BF), ("both", F32, BF, 7, BF, F32),
     ("both", BF, F32, 10 ** 9, F32, F32), ("pre", BF, F32, 0, BF, F32), ("pre", F32, F32, 0, F32, F32),

@@ -72,11 +72,12 @@ def test_route_and_gradient(T, E, k, dt, renorm):
         R.close(out, want, mag, 96 + 8 * dist + k, "dlogits")
 
 
-@pytest.mark.parametrize("T", [40000, 70001])
-def test_many_tokens(T):
-    z = logits_of(T, 128, F32, T, disabled=3)
-    r = ops.moe_route(z, 8)
-    check(z, 8, True, None, r)
+@pytest.mark.parametrize("T,E,k", [(32768, 16, 2), (32769, 128, 8), (70001, 128, 8), (50000, 300, 4), (40000, 1000, 3)])
+def test_many_tokens(T, E, k):
+    """Up to and past the workgroups that one launch adds up directly."""
+    z = logits_of(T, E, F32, T, disabled=3)
+    r = ops.moe_route(z, k)
+    check(z, k, True, None, r)
 
 
 @pytest.mark.parametrize("T", [5, 64, 200, 777])
