@@ -66,6 +66,41 @@ __device__ __forceinline__ float rows_sum(float v) {
     return __uint_as_float(q[0]) + __uint_as_float(q[1]);
 }
 
+// Sums over the lanes with the same index modulo n (a power of two, uniform).
+template <int K>
+__device__ __forceinline__ void lanes_sum_mod(uint32_t (&v)[K], int n) {
+#pragma unroll
+    for (int i = 0; i < K; ++i) {
+        if (n <= 8) v[i] += dpp_mov<0x128>(v[i]);        // rotate the 16-lane rows by 8, 4, 2, 1
+        if (n <= 4) v[i] += dpp_mov<0x124>(v[i]);
+        if (n <= 2) v[i] += dpp_mov<0x122>(v[i]);
+        if (n <= 1) v[i] += dpp_mov<0x121>(v[i]);
+        if (n <= 16) {
+            const auto p = __builtin_amdgcn_permlane16_swap(v[i], v[i], false, false);
+            v[i] = p[0] + p[1];
+        }
+        if (n <= 32) {
+            const auto p = __builtin_amdgcn_permlane32_swap(v[i], v[i], false, false);
+            v[i] = p[0] + p[1];
+        }
+    }
+}
+
+// Inclusive prefix sum over the wave: shifts inside the 16-lane rows, then the
+// last lane of a row to the rows behind it.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ int dpp_add(int v) {
+    return v + __builtin_amdgcn_update_dpp(0, v, CTRL, ROWS, 0xf, false);
+}
+__device__ __forceinline__ int wave_scan(int v) {
+    v = dpp_add<0x111, 0xf>(v);                          // row_shr 1, 2, 4, 8
+    v = dpp_add<0x112, 0xf>(v);
+    v = dpp_add<0x114, 0xf>(v);
+    v = dpp_add<0x118, 0xf>(v);
+    v = dpp_add<0x142, 0xa>(v);                          // lane 15 of rows 0, 2 to rows 1, 3
+    return dpp_add<0x143, 0xc>(v);                       // lane 31 to rows 2, 3
+}
+
 // All-reduce over LANES lanes (16: a DPP row, 64: the wave).  The four rows of
 // a wave meet in scalar registers: no LDS crossbar, and the result is uniform.
 // Every lane of the wave must be active.

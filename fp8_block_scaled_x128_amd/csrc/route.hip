@@ -58,14 +58,9 @@ __device__ __forceinline__ void scan_experts(const int* counts, int* excl, int E
         for (int b = 0; b < E; b += 64) {
             const int e = b + threadIdx.x;
             const int c = e < E ? counts[e] : 0;
-            int v = c;
-#pragma unroll
-            for (int d = 1; d < 64; d <<= 1) {
-                const int o = __shfl_up(v, d, 64);
-                if ((int)threadIdx.x >= d) v += o;
-            }
+            const int v = wave_scan(c);
             if (e < E) excl[e] = carry + v - c;
-            carry += __shfl(v, 63, 64);
+            carry += (int)lane_value((uint32_t)v, 63);
         }
         if (threadIdx.x == 0) excl[E] = carry;
     }
@@ -126,12 +121,12 @@ __device__ __forceinline__ float2 select_tokens(const RouteArgs& p, int64_t t0, 
         const uint32_t top = lanes_umax<L>(best);
         const bool live = top > kKeyNegInf;
         const float m = live ? key_logit(top) : 0.0f;
-        float ex[V], sum = 0.0f;
+        float sum = 0.0f;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float v = __builtin_amdgcn_exp2f((z[i] - m) * kLog2e);
-            ex[i] = left[i] ? v : 0.0f;
-            sum += ex[i];
+            z[i] = left[i] ? z[i] : -INFINITY;
+            sum += left[i] ? v : 0.0f;
         }
         sum = lanes_sum<L>(sum);
         uint32_t ksel[2] = {0, 0}, esel[2] = {0, 0};
@@ -175,9 +170,14 @@ __device__ __forceinline__ float2 select_tokens(const RouteArgs& p, int64_t t0, 
             if (l == 0) p.lse[t] = lse;
         }
         if (live) {
+            // exp again, from an m the compiler cannot match with the first
+            // time: V values held through the rounds cost more
             const float inv = 1.0f / sum;
+            float m2 = m;
+            asm volatile("" : "+v"(m2));
 #pragma unroll
-            for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(ex[i], inv, acc[i]);
+            for (int i = 0; i < V; ++i)
+                acc[i] = __builtin_fmaf(__builtin_amdgcn_exp2f((z[i] - m2) * kLog2e), inv, acc[i]);
             if (l == 0) {
                 sums[0] = __builtin_fmaf(lse, lse, sums[0]);
                 sums[1] += 1.0f;
@@ -320,24 +320,41 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
         const int i = threadIdx.x + u * kThreads;
         es[u] = i < n ? p.experts[t0 * p.k + i] : -1;
     }
+    // the losses' probability sums, four experts per thread and every
+    // (4096 / epad)-th workgroup's (or run's); the counts come later
+    const int e4 = (threadIdx.x * 4) & (epad - 1), prows = kThreads * 4 / epad;
+    float4 ps = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    float s[3] = {0.0f, 0.0f, 0.0f};                // counts . probabilities, lse^2, tokens (at most 2^22: exact)
+    if (!tokens) {
+        const float* src = SUPER ? ws.run_psum : ws.psum;
+        const int n = SUPER ? (nblk + kRun - 1) / kRun : nblk;
+#pragma unroll 8
+        for (int b = threadIdx.x * 4 / epad; b < n; b += prows) {
+            const float4 v = *reinterpret_cast<const float4*>(src + (int64_t)b * epad + e4);
+            ps.x += v.x; ps.y += v.y; ps.z += v.z; ps.w += v.w;
+        }
+        for (int b = threadIdx.x; b < nblk; b += kThreads) { s[1] += ws.lse2[b]; s[2] += (float)ws.live[b]; }
+    }
     uint32_t tot[8], pre[8];
 #pragma unroll
     for (int i = 0; i < 8; ++i) tot[i] = pre[i] = 0;
     const int ch = threadIdx.x & (nch - 1), rows = kThreads / nch;
     const int b1 = SUPER ? max(blk, 0) : nblk, b0 = SUPER ? b1 & ~(kRun - 1) : 0;
-    for (int b = b0 + threadIdx.x / nch; b < b1; b += rows) {
-        const uint4 v = *reinterpret_cast<const uint4*>(ws.hist + (int64_t)b * epad + 16 * ch);
-        add_bytes(tot, v);
-        if (b < blk) add_bytes(pre, v);
-    }
-    for (int e = threadIdx.x; e < epad; e += kThreads) mask[e] = 0;
-    for (int d = nch; d < 64; d <<= 1) {
+    // four rows in flight; rows past the last are loaded again and not added
+    for (int b = b0 + threadIdx.x / nch; b < b1; b += 4 * rows) {
+        uint4 v[4];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            tot[i] += (uint32_t)__shfl_xor((int)tot[i], d, 64);
-            pre[i] += (uint32_t)__shfl_xor((int)pre[i], d, 64);
+        for (int u = 0; u < 4; ++u)
+            v[u] = *reinterpret_cast<const uint4*>(ws.hist + (int64_t)min(b + u * rows, b1 - 1) * epad + 16 * ch);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (b + u * rows < b1) add_bytes(tot, v[u]);
+            if (b + u * rows < min(b1, blk)) add_bytes(pre, v[u]);
         }
     }
+    for (int e = threadIdx.x; e < epad; e += kThreads) mask[e] = 0;
+    lanes_sum_mod(tot, nch);
+    lanes_sum_mod(pre, nch);
     const int wave = threadIdx.x >> 6;
     uint32_t* dst = part + ((wave & (kHalf - 1)) * nch + ch) * 16;
     if (wave >= kHalf && (int)(threadIdx.x & 63) < nch) {
@@ -405,16 +422,8 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
         return;
     }
     __shared__ float red[48];
-    float s[3] = {0.0f, 0.0f, 0.0f};                // counts . probabilities, lse^2, tokens (at most 2^22: exact)
-    // four experts per thread, every (4096 / epad)-th workgroup's
-    const int e4 = (threadIdx.x * 4) & (epad - 1), prows = kThreads * 4 / epad;
-    const float c0 = (float)counts[e4], c1 = (float)counts[e4 + 1], c2 = (float)counts[e4 + 2], c3 = (float)counts[e4 + 3];
-#pragma unroll 8
-    for (int b = threadIdx.x * 4 / epad; b < (SUPER ? nrun : nblk); b += prows) {
-        const float4 v = *reinterpret_cast<const float4*>((SUPER ? ws.run_psum : ws.psum) + (int64_t)b * epad + e4);
-        s[0] += __builtin_fmaf(c0, v.x, c1 * v.y) + __builtin_fmaf(c2, v.z, c3 * v.w);
-    }
-    for (int b = threadIdx.x; b < nblk; b += kThreads) { s[1] += ws.lse2[b]; s[2] += (float)ws.live[b]; }
+    s[0] = __builtin_fmaf((float)counts[e4], ps.x, (float)counts[e4 + 1] * ps.y) +
+           __builtin_fmaf((float)counts[e4 + 2], ps.z, (float)counts[e4 + 3] * ps.w);
     block_sums(s, red);
     for (int e = threadIdx.x; e <= p.E; e += kThreads) {
         p.offsets[e] = base[e];
@@ -555,7 +564,10 @@ __global__ void __launch_bounds__(256) k_route_bwd(RouteBwdArgs p) {
     }
 }
 
-// Lanes and values per token by the number of experts.
+// Lanes and values per token by the number of experts.  Sixteen lanes of many
+// values beat a wave of few in the selection, whose rounds then serve four
+// tokens at once (16384 tokens of 512 experts: 39.5 against 43.8 us); the
+// gradient has no rounds and more to hold (26.4 against 16.3 us).
 template <template <int, int> class F, typename... A>
 hipError_t by_experts(int E, A&&... a) {
     if (E <= 16) return F<16, 1>::run(a...);
@@ -563,12 +575,13 @@ hipError_t by_experts(int E, A&&... a) {
     if (E <= 64) return F<16, 4>::run(a...);
     if (E <= 128) return F<16, 8>::run(a...);
     if (E <= 256) return F<16, 16>::run(a...);
-    if (E <= 512) return F<64, 8>::run(a...);
+    if (E <= 512) return F<F<64, 8>::kLanes512, 512 / F<64, 8>::kLanes512>::run(a...);
     return F<64, 16>::run(a...);
 }
 
 template <int L, int V>
 struct Select {
+    static constexpr int kLanes512 = 16;
     static hipError_t run(const RouteArgs& p, const RouteWs& ws, int nblk, hipStream_t st) {
         if (nblk <= 1) {
             const size_t lds = select_lds(p.E, L * V) + (size_t)p.E * 8 + 8;
@@ -585,6 +598,7 @@ struct Select {
 
 template <int L, int V>
 struct Backward {
+    static constexpr int kLanes512 = 64;
     static hipError_t run(const RouteBwdArgs& p, hipStream_t st) {
         constexpr int kGroups = 256 / L;
         const int64_t blocks = (p.T + kGroups - 1) / kGroups;
