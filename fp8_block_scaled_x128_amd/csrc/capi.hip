@@ -665,7 +665,8 @@ static fp8bs_status norm_common(int64_t rows, int64_t cols, fp8bs_out stream_typ
     if (rows < 0 || cols < 0 || rows > INT32_MAX) return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
     if (cols % 8 || cols > 16384) return fail(FP8BS_ERR_SHAPE, "cols %% 8 != 0 or cols > 16384 (cols=%lld)", (long long)cols);
     // comparisons that a NaN fails
-    if (!(eps > 0.0f && eps <= 3.0e38f)) return fail(FP8BS_ERR_UNSUPPORTED, "eps must be positive and finite");
+    if (!(eps >= 1.17549435e-38f && eps <= 3.0e38f))
+        return fail(FP8BS_ERR_UNSUPPORTED, "eps must be a positive normal fp32 value");
     if (!(scale >= -3.0e38f && scale <= 3.0e38f)) return fail(FP8BS_ERR_UNSUPPORTED, "scale must be finite");
     return FP8BS_OK;
 }

@@ -99,13 +99,15 @@ __device__ __forceinline__ float dot8(const float u[8], const float v[8]) {
     return (a + b) + (c + d);
 }
 
-// 1 / sqrt(v) for v > 0: the hardware approximation and one Newton step with
-// the rounding error of v r kept (fma), within an ulp of the exact value.
+// 1 / sqrt(v) for normal v > 0: the hardware approximation and one Newton step
+// with the rounding error of v r kept (fma), within an ulp of the exact value;
+// 0 for infinity.
 __device__ __forceinline__ float inv_sqrt(float v) {
     const float r = __builtin_amdgcn_rsqf(v);
     const float t = v * r, tl = __builtin_fmaf(v, r, -t);
     const float e = __builtin_fmaf(-tl, r, __builtin_fmaf(-t, r, 1.0f));
-    return __builtin_fmaf(0.5f * r, e, r);
+    const float n = __builtin_fmaf(0.5f * r, e, r);
+    return v <= 3.4028235e38f ? n : r;
 }
 
 // Sums of K values over the waves that share a row (one: no barrier).  `buf`

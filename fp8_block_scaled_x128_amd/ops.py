@@ -50,6 +50,8 @@ def library_path() -> str:
 def load():
     """Load libfp8bs.so (raises if it is missing: there is no fallback)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib

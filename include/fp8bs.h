@@ -599,7 +599,8 @@ fp8bs_status fp8_moe_route_backward(const void* logits, int64_t T, int32_t E, in
  *            group g) at s[r * s_stride_row + g * s_stride_group].
  * Requirements: rows, cols >= 0, cols % 8 == 0, cols <= 16384, rows < 2^31;
  * residual or x; w_post and gate only with x; y and q only with w_pre, and
- * w_pre only with one of them; at least one output; eps > 0 and scale finite;
+ * w_pre only with one of them; at least one output; eps > 0 (a normal fp32
+ * value) and scale finite;
  * leading dimensions >= cols and % 8 == 0; bf16, fp32 and weight pointers
  * 16-byte aligned, q 8-byte, s 4-byte.  Inputs are expected to be finite with
  * mean squares in fp32's range.

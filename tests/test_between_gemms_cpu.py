@@ -18,7 +18,7 @@ def norm(rows=4, cols=256, x=A, ld=None, res=A, st=0, gate=None, R=1, scale=1.0,
 
 @pytest.mark.parametrize("args,status", [
     (dict(rows=-1), 2), (dict(cols=100), 2), (dict(cols=16392), 2), (dict(rows=1 << 31), 2), (dict(gate=A, R=0), 2),
-    (dict(st=2), 5), (dict(wt=7), 5), (dict(eps=0.0), 5), (dict(eps=NAN), 5), (dict(eps=INF), 5),
+    (dict(st=2), 5), (dict(wt=7), 5), (dict(eps=0.0), 5), (dict(eps=1e-40), 5), (dict(eps=NAN), 5), (dict(eps=INF), 5),
     (dict(scale=NAN), 5), (dict(scale=INF), 5),
     (dict(x=None, res=None, w_post=None), 1), (dict(x=None), 1), (dict(x=None, w_post=None, gate=A), 1),
     (dict(s=None), 1), (dict(q=None), 1), (dict(w_pre=None), 1), (dict(y=None, q=None, s=None), 1),

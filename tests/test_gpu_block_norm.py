@@ -133,6 +133,24 @@ def test_rows_of_zeros_and_large_values():
     assert (o.q[0] == 0).all() and (o.s[0] == 0).all()
 
 
+def test_infinities_and_nan_stay_in_their_rows():
+    """An infinity makes its row's factor 0 (so 0 beside it, NaN at it), as in
+    the formula; other rows are as without it."""
+    rows, cols = 6, 520
+    t = make(rows, cols, "both", BF, BF, 0, 8)
+    clean = ops.block_norm(t["residual"], t["x"], w_pre=t["w_pre"], w_post=t["w_post"])
+    x = t["x"].clone()
+    x[1, 5] = torch.inf
+    x[3, 7] = torch.nan
+    o = ops.block_norm(t["residual"], x, w_pre=t["w_pre"], w_post=t["w_post"])
+    ok = [0, 2, 4, 5]
+    for a, b in zip(o, clean):
+        assert torch.equal(a[ok], b[ok])
+    assert torch.isnan(o.h[1, 5]) and torch.isnan(o.h[3]).all()
+    rest = [c for c in range(cols) if c != 5]
+    assert torch.equal(o.h[1, rest], t["residual"][1, rest])
+
+
 def test_in_place_strides_and_untouched_columns():
     """h over residual in place, outputs as views of wider tensors: columns
     past the view keep their bytes."""

@@ -88,6 +88,19 @@ def test_block_forward_and_backward(layer, masked):
     R.close(dz, wz, mz, 104 + 8 * dist, "dlogits")
 
 
+def test_no_tokens_and_no_live_tokens(layer):
+    """A batch of no tokens, and one whose every token is masked: no expert
+    runs, the output is zeros."""
+    d, weights = layer
+    H = d["x"].shape[1]
+    q, s = ops.quant_rowblock(dev_bf16(d["x"]))
+    out, r, _ = ops.moe_forward_routed((q[:0], s[:0]), torch.empty(0, 8, device="cuda"), 2, *weights)
+    assert out.shape == (0, H) and (r.counts == 0).all()
+    z = torch.randn(300, 8, device="cuda")
+    out, r, _ = ops.moe_forward_routed((q, s), z, 2, *weights, mask=torch.zeros(300, dtype=torch.bool, device="cuda"))
+    assert (out == 0).all() and (r.counts == 0).all()
+
+
 def test_serving_block_replays_in_a_graph(layer):
     """One decode step's block (norm, routing, routed combine) captured at a
     padded batch and replayed with other masks and logits: the maps stay on

@@ -213,3 +213,74 @@ def test_combine_without_rows():
     dw = torch.full((3, 2), 5.0, device="cuda")
     ops.fp8_moe_combine_backward(out, 64, ops.OUT_FP32, None, 0, 64, 0, pos, w, 3, 2, None, 0, dw)
     assert (dw == 0).all()
+
+
+@pytest.mark.parametrize("T", [40, 1000, 33000])
+def test_route_graph_replays_and_streams(T):
+    """Routing and its gradient captured once and replayed on new logits, eager
+    calls between; then the same on two streams at once, each with tensors and
+    workspace of its own."""
+    E, k = 60, 4
+    z = logits_of(T, E, F32, 1).contiguous()
+    dw, dl = torch.randn(T, k, device="cuda"), torch.tensor([0.3, 0.2], device="cuda")
+
+    def both(z, r=None, o=None):
+        r = ops.moe_route(z, k, out=r)
+        return r, ops.moe_route_backward(z, r.experts, r.weights, r.counts, r.lse, dweights=dw, dloss=dl, out=o)
+    r, o = both(z)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        both(z, r, o)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        both(z, r, o)
+    for rep in range(4):
+        z.normal_()
+        for v in (*r[:8], o):
+            v.fill_(0)
+        graph.replay()
+        torch.cuda.synchronize()
+        er, eo = both(z)
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip((*r[:8], o), (*er[:8], eo))), rep
+    zs = [logits_of(T, E, F32, s).contiguous() for s in (5, 6)]
+    want = [both(v) for v in zs]
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream() for _ in range(2)], []
+    for rep in range(3):
+        for i, st in enumerate(streams):
+            with torch.cuda.stream(st):
+                got.append((i, both(zs[i])))
+    torch.cuda.synchronize()
+    for i, (er, eo) in got:
+        assert all(torch.equal(a, b) for a, b in zip((*er[:8], eo), (*want[i][0][:8], want[i][1])))
+
+
+def test_refusals():
+    z = torch.randn(10, 16, device="cuda")
+    with pytest.raises(ValueError):
+        ops.moe_route(z.cpu(), 2)
+    with pytest.raises(ValueError):
+        ops.moe_route(z.half(), 2)
+    with pytest.raises(ValueError):
+        ops.moe_route(z.t(), 2)
+    with pytest.raises(ValueError):
+        ops.moe_route(z, 2, mask=torch.ones(9, dtype=torch.bool, device="cuda"))
+    with pytest.raises(ops.Fp8bsError):
+        ops.moe_route(z, 17)
+    with pytest.raises(ops.Fp8bsError):
+        ops.moe_route(z[:1].expand(10, 16), 2)
+    r = ops.moe_route(z, 2)
+    with pytest.raises(ValueError):
+        ops.moe_route(z[:9], 2, out=r)
+    with pytest.raises(ops.Fp8bsError):
+        ops.moe_route_backward(z, r.experts, r.weights, r.counts, r.lse)
+    with pytest.raises(ValueError):
+        ops.moe_route_backward(z, r.experts, r.weights, r.counts[:-1], r.lse, dloss=torch.ones(2, device="cuda"))
+    y = torch.randn(20, 64, device="cuda").to(BF)
+    with pytest.raises(ValueError):
+        ops.moe_combine_backward(y[:10], y[:, :56], r.token_rows, r.weights)
+    with pytest.raises(ValueError):
+        ops.moe_combine_backward(y[:10], y, r.token_rows.long(), r.weights)
