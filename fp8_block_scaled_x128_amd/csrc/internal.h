@@ -85,14 +85,15 @@ struct NormBwdArgs {
     void* dgate; int64_t ld_dgate; bool dgate32;
     float* dw_post; float* dw_pre;
 };
-// How the rows are dealt: `splits` units per gate row (or over all rows), every
-// splits-th row each, walked by `slots` workgroups; the column sums'
+// How the rows are dealt: `splits` units per gate row, a run of `chunk` rows
+// each (or over all rows, every splits-th row each), walked by `slots`
+// workgroups; the column sums'
 // partials lie at the three offsets (in floats) of the workspace.
 struct NormBwdPlan {
     int wpr, nv;
     bool grouped, by_wave;
     int32_t slots;
-    int64_t units, splits, unit_rows, groups;
+    int64_t units, splits, chunk, unit_rows, groups;
     size_t off_pre, off_post, off_gate, ws_floats;
     float *ws_pre, *ws_post, *ws_gate;
 };

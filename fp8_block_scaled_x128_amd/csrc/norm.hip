@@ -62,17 +62,19 @@ struct RowIn {
     }
 };
 
-// MULTI: a workgroup has one row at a time, else each of its waves has one.
+// LPR lanes have a row; kMulti: a workgroup has one row at a time.
 // One or two chunks per lane (AHEAD): the next row is loaded while this one is
 // reduced and stored, and the weights stay in registers: a weight load from
 // the L2 behind the next row's loads would wait for them, since loads return
 // in order.  More chunks have no registers left for it.
-template <int NV, bool RES32, bool MULTI>
+template <int NV, bool RES32, int LPR>
 __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
+    constexpr bool MULTI = LPR == kMulti, SHARED = LPR == 16 || LPR == 32;     // SHARED: a wave has several rows
     constexpr bool AHEAD = NV <= 2;
     constexpr int KEPT = AHEAD ? NV : 1;
     __shared__ float lds[2][kMaxRowWaves][4];
-    const int tid = MULTI ? threadIdx.x : (threadIdx.x & 63);
+    const int tid = MULTI ? threadIdx.x : threadIdx.x % (MULTI ? 64 : LPR);
+    const int sub = SHARED ? (threadIdx.x & 63) / (MULTI ? 64 : LPR) : 0;
     const int nc = p.cols >> 3, step = MULTI ? wpr * 64 : 64;
     const float inv_n = 1.0f / (float)p.cols;
     int turn = 0;
@@ -85,22 +87,28 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
         if (AHEAD && p.w_pre) load8_shared(p.w_pre, c, p.w32, wpre[i]);
         if (AHEAD && p.w_post) load8_shared(p.w_post, c, p.w32, wpost[i]);
     }
-    const int64_t per = MULTI ? 1 : kRowWaves;              // rows a workgroup has at a time
+    constexpr int kWaveRows = MULTI ? 1 : 64 / (MULTI ? 64 : LPR);
+    const int64_t per = MULTI ? 1 : kRowWaves * kWaveRows;  // rows a workgroup has at a time
     const int64_t first = MULTI ? (int64_t)blockIdx.x
-                                : (int64_t)blockIdx.x * per + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+                                : (int64_t)blockIdx.x * per + __builtin_amdgcn_readfirstlane(threadIdx.x >> 6) * kWaveRows;
+    // chunks of this lane's row: none past the last row (the lane stays for
+    // the reductions)
+    auto chunks = [&](int64_t row) { return !SHARED || row < p.rows ? nc : 0; };
     const int64_t stride = (int64_t)gridDim.x * per;
     RowIn<NV, RES32> in, ahead;
     in.zero();
     if (AHEAD) {
         ahead.zero();
-        if (first < p.rows) ahead.load(p, first, tid, step, nc);
+        if (first < p.rows) ahead.load(p, first + sub, tid, step, chunks(first + sub));
     }
-    for (int64_t row = first; row < p.rows; row += stride) {
+    for (int64_t row0 = first; row0 < p.rows; row0 += stride) {
+        const int64_t row = row0 + sub;
+        const int ncr = chunks(row);
         if (AHEAD) {
             in = ahead;
-            if (row + stride < p.rows) ahead.load(p, row + stride, tid, step, nc);
+            if (row0 + stride < p.rows) ahead.load(p, row + stride, tid, step, chunks(row + stride));
         } else {
-            in.load(p, row, tid, step, nc);
+            in.load(p, row, tid, step, ncr);
         }
         float r = 1.0f;
         if (p.w_post) {
@@ -111,7 +119,7 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
                 in.x[i].get(v);
                 ss[0] += sumsq8(v);
             }
-            row_sums<MULTI>(ss, wpr, lds, turn);
+            row_sums<LPR>(ss, wpr, lds, turn);
             r = inv_sqrt(__builtin_fmaf(ss[0], inv_n, p.eps));
         }
         float h[NV][8];
@@ -132,18 +140,18 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
             }
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = __builtin_fmaf(v[e], p.scale, h[i][e]);
-            if (p.h && (i < kSure<NV> || c < nc)) store8<RES32>(row_ptr<RES32>(p.h, row, p.ld_h), c, h[i]);
+            if (p.h && (i < kSure<NV> || c < ncr)) store8<RES32>(row_ptr<RES32>(p.h, row, p.ld_h), c, h[i]);
             ss[0] += sumsq8(h[i]);
         }
         if (!p.w_pre) continue;
         // y from the unrounded h: the bf16 rounding of the stored stream does
         // not enter y, its scales or its codes
-        row_sums<MULTI>(ss, wpr, lds, turn);
+        row_sums<LPR>(ss, wpr, lds, turn);
         r = inv_sqrt(__builtin_fmaf(ss[0], inv_n, p.eps));
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * step;
-            const bool in_row = i < kSure<NV> || c < nc;
+            const bool in_row = i < kSure<NV> || c < ncr;
             if (!AHEAD) load8_shared(p.w_pre, min(c, nc - 1), p.w32, wpre[i % KEPT]);
 #pragma unroll
             for (int e = 0; e < 8; ++e) h[i][e] = h[i][e] * r * wpre[i % KEPT][e];
@@ -162,13 +170,12 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
     }
 }
 
-template <int NV, bool MULTI>
+template <int NV, int LPR>
 hipError_t launch_types(const NormArgs& p, int wpr, hipStream_t st) {
-    const int per = MULTI ? 1 : kRowWaves;
-    const int64_t blocks = (p.rows + per - 1) / per, most = workgroups(MULTI ? wpr : per, NV);
-    hipLaunchKernelGGL((p.res32 ? k_block_norm<NV, true, MULTI> : k_block_norm<NV, false, MULTI>),
-                       dim3((unsigned)(blocks < most ? blocks : most)), dim3(MULTI ? 64 * wpr : 64 * kRowWaves), 0,
-                       st, p, wpr);
+    const int per = LPR == kMulti ? 1 : kRowWaves * 64 / (LPR == kMulti ? 64 : LPR), waves = LPR == kMulti ? wpr : kRowWaves;
+    const int64_t blocks = (p.rows + per - 1) / per, most = workgroups(waves, NV);
+    hipLaunchKernelGGL((p.res32 ? k_block_norm<NV, true, LPR> : k_block_norm<NV, false, LPR>),
+                       dim3((unsigned)(blocks < most ? blocks : most)), dim3(64 * waves), 0, st, p, wpr);
     return hipGetLastError();
 }
 
@@ -177,11 +184,18 @@ hipError_t launch_types(const NormArgs& p, int wpr, hipStream_t st) {
 hipError_t launch_block_norm(const NormArgs& p, hipStream_t st) {
     int wpr, nv;
     row_split(p.cols, &wpr, &nv);
+    if (wpr == 1) {
+        switch (row_lanes(p.cols)) {
+            case 16: return launch_types<1, 16>(p, wpr, st);
+            case 32: return launch_types<1, 32>(p, wpr, st);
+            default: return launch_types<1, 64>(p, wpr, st);
+        }
+    }
     switch (nv) {
-        case 1: return wpr == 1 ? launch_types<1, false>(p, wpr, st) : launch_types<1, true>(p, wpr, st);
-        case 2: return launch_types<2, true>(p, wpr, st);
-        case 3: return launch_types<3, true>(p, wpr, st);
-        default: return launch_types<4, true>(p, wpr, st);
+        case 1: return launch_types<1, kMulti>(p, wpr, st);
+        case 2: return launch_types<2, kMulti>(p, wpr, st);
+        case 3: return launch_types<3, kMulti>(p, wpr, st);
+        default: return launch_types<4, kMulti>(p, wpr, st);
     }
 }
 

@@ -37,6 +37,13 @@ __device__ __forceinline__ void combine_waves(float (&a)[8], float (*comb)[8], i
     __syncthreads();
 }
 
+// Adds the sums of a wave's rows.
+template <int LPR>
+__device__ __forceinline__ void add_rows(float (&a)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; ++e) a[e] = LPR == 16 ? rows_sum(a[e]) : LPR == 32 ? halves_sum(a[e]) : a[e];
+}
+
 // Adds eight values to a lane's sums in LDS.
 __device__ __forceinline__ void add_lds(float4* a, const float v[8]) {
     float4* b = a + 64 * kMaxRowWaves;
@@ -136,7 +143,7 @@ struct RowIn {
     }
 };
 
-// MULTI: a workgroup has one row at a time, else each of its waves has one.
+// LPR lanes have a row; kMulti: a workgroup has one row at a time.
 //
 // The next row is loaded while this one is reduced and stored, as far as the
 // registers go (AHEAD).  Loads return in order, so a weight load from the L2 behind the next row's loads would
@@ -146,8 +153,9 @@ struct RowIn {
 // registers would spill (measured with 2048x10240: 99 us), and each lane keeps
 // its columns' sums in LDS, 16 bytes a column (halves of a chunk 16 bytes
 // apart from lane to lane: no bank conflicts).
-template <int NV, bool RES32, bool DY32, bool MULTI, int GATE>
+template <int NV, bool RES32, bool DY32, int LPR, int GATE>
 __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPlan pl) {
+    constexpr bool MULTI = LPR == kMulti, SHARED = LPR == 16 || LPR == 32;     // SHARED: a wave has several rows
     constexpr bool GACC = GATE == kGateSum;
     constexpr bool KEEP = NV <= 2;
     constexpr bool AHEAD = NV <= 2 || (NV == 3 && GATE == kGateNone);
@@ -157,7 +165,8 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
     __shared__ float4 lacc[KEEP ? 1 : NV * 4][KEEP ? 1 : 64 * kMaxRowWaves];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wpr = pl.wpr;
-    const int tid = MULTI ? threadIdx.x : (threadIdx.x & 63);
+    const int tid = MULTI ? threadIdx.x : threadIdx.x % (MULTI ? 64 : LPR);
+    const int sub = SHARED ? (threadIdx.x & 63) / (MULTI ? 64 : LPR) : 0;
     const int nc = p.cols >> 3, step = MULTI ? wpr * 64 : 64;
     const float inv_n = 1.0f / (float)p.cols;
     int turn = 0;
@@ -188,14 +197,19 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
     const bool by_wave = !MULTI && pl.by_wave;
     const int64_t u0 = by_wave ? (int64_t)blockIdx.x * kWaves + wave : blockIdx.x;
     const int64_t ustep = by_wave ? (int64_t)gridDim.x * kWaves : gridDim.x;
-    // a unit's rows: every splits-th of its gate row's, eight at a time where
-    // each wave has one
-    const int lanes = MULTI || by_wave ? 1 : kWaves;
-    const int64_t rstep = pl.splits * lanes;
+    // a unit's rows: a run of a gate row's rows, or every splits-th of all
+    // rows, as many at a time as the workgroup (or wave) holds
+    constexpr int kWaveRows = MULTI ? 1 : 64 / (MULTI ? 64 : LPR);
+    const int at_once = MULTI ? 1 : by_wave ? kWaveRows : kWaves * kWaveRows;
+    const int64_t rstep = GACC ? at_once : pl.splits * at_once;
     for (int64_t u = u0; u < pl.units; u += ustep) {
         const int64_t g = u / pl.splits;
-        const int64_t r0 = g * pl.unit_rows + (u - g * pl.splits) * lanes + (lanes == 1 ? 0 : wave);
-        const int64_t r1 = min((g + 1) * pl.unit_rows, p.rows);
+        const int64_t s = u - g * pl.splits;
+        const int64_t r0 = g * pl.unit_rows + s * (GACC ? pl.chunk : at_once) + (MULTI || by_wave ? 0 : wave * kWaveRows);
+        const int64_t r1 = min(min((g + 1) * pl.unit_rows, GACC ? g * pl.unit_rows + (s + 1) * pl.chunk : p.rows), p.rows);
+        // chunks of this lane's row: none past the last row (the lane stays
+        // for the reductions)
+        auto chunks = [&](int64_t row) { return !SHARED || row < r1 ? nc : 0; };
         if (GACC) {
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -209,16 +223,23 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
         in.zero();
         if (AHEAD) {
             ahead.zero();
-            if (r0 < r1) ahead.load(p, r0, tid, step, nc);
+            if (r0 < r1) ahead.load(p, r0 + sub, tid, step, chunks(r0 + sub));
         }
-        for (int64_t row = r0; row < r1; row += rstep) {
+        for (int64_t row0 = r0; row0 < r1; row0 += rstep) {
+            const int64_t row = row0 + sub;
+            const int ncr = chunks(row);
+            // a lane whose row is past the last keeps zeros
             if (AHEAD) in = ahead;
             if (!KEEP) {
                 if (p.w_pre) rpre.load(p.w_pre, p.w32, tid, step, nc);
                 if (p.w_post) rpost.load(p.w_post, p.w32, tid, step, nc);
             }
-            if (!AHEAD) in.load(p, row, tid, step, nc);
-            else if (row + rstep < r1) ahead.load(p, row + rstep, tid, step, nc);
+            if (!AHEAD) {
+                in.load(p, row, tid, step, ncr);
+            } else if (row0 + rstep < r1) {
+                if (SHARED) ahead.zero();
+                ahead.load(p, row + rstep, tid, step, chunks(row + rstep));
+            }
             float sums[3] = {0.0f, 0.0f, 0.0f};     // sum h^2, sum dy w_pre h, sum x^2
             if (p.w_pre) {
 #pragma unroll
@@ -239,7 +260,7 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
                 in.x[i].get(x);
                 sums[2] += sumsq8(x);
             }
-            row_sums<MULTI>(sums, wpr, lds, turn);
+            row_sums<LPR>(sums, wpr, lds, turn);
 #pragma unroll
             for (int i = 0; i < NV; ++i) { in.h[i].forget(); in.dy[i].forget(); in.x[i].forget(); }
             float dh[NV][8];
@@ -267,7 +288,7 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = tid + i * step;
-                    if (i < kSure<NV> || c < nc) store8<RES32>(row_ptr<RES32>(p.dres, row, p.ld_dres), c, dh[i]);
+                    if (i < kSure<NV> || c < ncr) store8<RES32>(row_ptr<RES32>(p.dres, row, p.ld_dres), c, dh[i]);
                 }
             }
             if (!p.x) continue;
@@ -300,7 +321,7 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
                     dh[i][e] = dn;                      // the gradient at xh from here on
                 }
                 if (!KEEP) add_lds(&lacc[KEEP ? 0 : i * 4 + 2][tid], aw);
-                if (GATE == kGateRow && p.dgate && (i < kSure<NV> || tid + i * step < nc)) {
+                if (GATE == kGateRow && p.dgate && (i < kSure<NV> || tid + i * step < ncr)) {
                     if (p.dgate32) store8<true>(row_ptr<true>(p.dgate, row, p.ld_dgate), tid + i * step, dg);
                     else store8<false>(row_ptr<false>(p.dgate, row, p.ld_dgate), tid + i * step, dg);
                 }
@@ -308,7 +329,7 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
             if (!p.dx) continue;
             float m = 0.0f;
             if (p.w_post) {
-                row_sums<MULTI>(dot, wpr, lds, turn);
+                row_sums<LPR>(dot, wpr, lds, turn);
 #pragma unroll
                 for (int i = 0; i < NV; ++i) in.x[i].forget();
                 m = dot[0] * inv_n * rx * rx;           // mean(g xh) r': times x
@@ -320,19 +341,19 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
                 in.x[i].get(x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) d[e] = __builtin_fmaf(-m, x[e], dh[i][e] * rx);
-                if (i < kSure<NV> || c < nc) store8<false>(row_ptr<false>(p.dx, row, p.ld_dx), c, d);
+                if (i < kSure<NV> || c < ncr) store8<false>(row_ptr<false>(p.dx, row, p.ld_dx), c, d);
             }
         }
         if (GACC) {
-            if (!MULTI && !by_wave) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i) combine_waves(agate[GACC ? i : 0], comb, wave);
+            if (!MULTI) {
+                add_rows<LPR>(agate[0]);
+                if (!by_wave) combine_waves(agate[0], comb, wave);
             }
             if (MULTI || by_wave || wave == kWaves - 1) {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = tid + i * step;
-                    if (i >= kSure<NV> && c >= nc) continue;
+                    if ((i >= kSure<NV> && c >= nc) || sub > 0) continue;
                     if (pl.splits > 1) store8<true>(row_ptr<true>(pl.ws_gate, u, p.cols), c, agate[GACC ? i : 0]);
                     else if (p.dgate32) store8<true>(row_ptr<true>(p.dgate, g, p.ld_dgate), c, agate[GACC ? i : 0]);
                     else store8<false>(row_ptr<false>(p.dgate, g, p.ld_dgate), c, agate[GACC ? i : 0]);
@@ -341,12 +362,11 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
         }
     }
     if (!MULTI) {
-#pragma unroll
-        for (int i = 0; i < NV; ++i) {
-            if (p.dw_pre) combine_waves(awpre[i % KEPT], comb, wave);
-            if (p.dw_post) combine_waves(awpost[i % KEPT], comb, wave);
-        }
-        if (wave != kWaves - 1) return;
+        add_rows<LPR>(awpre[0]);
+        add_rows<LPR>(awpost[0]);
+        if (p.dw_pre) combine_waves(awpre[0], comb, wave);
+        if (p.dw_post) combine_waves(awpost[0], comb, wave);
+        if (wave != kWaves - 1 || sub > 0) return;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -432,28 +452,37 @@ __global__ void __launch_bounds__(256) k_gate_reduce(NormBwdArgs p, NormBwdPlan 
     store_dgate(p, g, c, a);
 }
 
-template <int NV, bool MULTI, int GATE>
+template <int NV, int LPR, int GATE>
 hipError_t launch_types(const NormBwdArgs& p, const NormBwdPlan& pl, hipStream_t st) {
-    const auto k = p.res32 ? (p.dy32 ? k_block_norm_bwd<NV, true, true, MULTI, GATE>
-                                     : k_block_norm_bwd<NV, true, false, MULTI, GATE>)
-                           : (p.dy32 ? k_block_norm_bwd<NV, false, true, MULTI, GATE>
-                                     : k_block_norm_bwd<NV, false, false, MULTI, GATE>);
-    hipLaunchKernelGGL(k, dim3((unsigned)pl.slots), dim3(MULTI ? 64 * pl.wpr : 64 * kWaves), 0, st, p, pl);
+    const auto k = p.res32 ? (p.dy32 ? k_block_norm_bwd<NV, true, true, LPR, GATE>
+                                     : k_block_norm_bwd<NV, true, false, LPR, GATE>)
+                           : (p.dy32 ? k_block_norm_bwd<NV, false, true, LPR, GATE>
+                                     : k_block_norm_bwd<NV, false, false, LPR, GATE>);
+    hipLaunchKernelGGL(k, dim3((unsigned)pl.slots), dim3(LPR == kMulti ? 64 * pl.wpr : 64 * kWaves), 0, st, p, pl);
     return hipGetLastError();
 }
 
-template <int NV>
-hipError_t launch_nv(const NormBwdArgs& p, const NormBwdPlan& pl, hipStream_t st) {
-    if constexpr (NV == 1) {
-        if (pl.wpr == 1) {
-            return pl.grouped ? launch_types<NV, false, kGateSum>(p, pl, st)
-                   : p.gate   ? launch_types<NV, false, kGateRow>(p, pl, st)
-                              : launch_types<NV, false, kGateNone>(p, pl, st);
+template <int NV, int LPR>
+hipError_t launch_gate(const NormBwdArgs& p, const NormBwdPlan& pl, hipStream_t st) {
+    return pl.grouped ? launch_types<NV, LPR, kGateSum>(p, pl, st)
+           : p.gate   ? launch_types<NV, LPR, kGateRow>(p, pl, st)
+                      : launch_types<NV, LPR, kGateNone>(p, pl, st);
+}
+
+hipError_t launch_rows(const NormBwdArgs& p, const NormBwdPlan& pl, hipStream_t st) {
+    if (pl.wpr == 1) {
+        switch (row_lanes(p.cols)) {
+            case 16: return launch_gate<1, 16>(p, pl, st);
+            case 32: return launch_gate<1, 32>(p, pl, st);
+            default: return launch_gate<1, 64>(p, pl, st);
         }
     }
-    return pl.grouped ? launch_types<NV, true, kGateSum>(p, pl, st)
-           : p.gate   ? launch_types<NV, true, kGateRow>(p, pl, st)
-                      : launch_types<NV, true, kGateNone>(p, pl, st);
+    switch (pl.nv) {
+        case 1: return launch_gate<1, kMulti>(p, pl, st);
+        case 2: return launch_gate<2, kMulti>(p, pl, st);
+        case 3: return launch_gate<3, kMulti>(p, pl, st);
+        default: return launch_gate<4, kMulti>(p, pl, st);
+    }
 }
 
 }  // namespace
@@ -478,10 +507,11 @@ NormBwdPlan plan_block_norm_bwd(int64_t rows, int64_t cols, int64_t rows_per_gat
     pl.by_wave = pl.wpr == 1 && pl.grouped && rows_per_gate < 64 && groups >= 2048;
     int64_t splits = groups > 0 && !pl.by_wave ? most / groups : 1;
     if (splits < 1) splits = 1;
-    const int64_t at_once = pl.wpr == 1 && !pl.by_wave ? kWaves : 1;
+    const int64_t at_once = pl.wpr == 1 && !pl.by_wave ? kWaves * 64 / row_lanes(cols) : 1;
     if (splits > (longest + at_once - 1) / at_once) splits = (longest + at_once - 1) / at_once;
     if (splits < 1) splits = 1;
     pl.splits = splits;
+    pl.chunk = (longest + splits - 1) / splits;
     pl.units = groups * pl.splits;
     const int64_t want = pl.by_wave ? (pl.units + kWaves - 1) / kWaves : pl.units;
     pl.slots = (int32_t)(want < most ? want : most);
@@ -504,12 +534,7 @@ hipError_t launch_block_norm_bwd(const NormBwdArgs& p, float* ws, hipStream_t st
     pl.ws_gate = ws + pl.off_gate;
     hipError_t e = hipSuccess;
     if (p.rows > 0) {
-        switch (pl.nv) {
-            case 1: e = launch_nv<1>(p, pl, st); break;
-            case 2: e = launch_nv<2>(p, pl, st); break;
-            case 3: e = launch_nv<3>(p, pl, st); break;
-            default: e = launch_nv<4>(p, pl, st); break;
-        }
+        e = launch_rows(p, pl, st);
         if (e != hipSuccess) return e;
     }
     const bool gate = p.rows > 0 && pl.grouped && pl.splits > 1, few = pl.splits <= kFewUnits;

@@ -1,9 +1,11 @@
 // What the forward and backward block-norm kernels share: element access, the
 // row layout over lanes, and a row's reduction and factor.
 //
-// Layout: a row belongs to `wpr` waves of a workgroup; lane l of them holds
-// the 8-column chunks l, l + 64 wpr, ..., NV of them.  All but the last chunk
-// of a lane are inside the row, so only the last is guarded.
+// Layout: a row belongs to `wpr` waves of a workgroup (kMulti), or to 64, 32 or
+// 16 lanes of one wave (rows of at most 512, 256, 128 columns: head norms);
+// lane l of them holds the 8-column chunks l, l + (lanes), ..., NV of them.
+// All but the last chunk of a lane are inside the row, so only the last is
+// guarded.
 #pragma once
 #include <type_traits>
 
@@ -80,6 +82,7 @@ __device__ __forceinline__ void store8(void* row, uint32_t c, const float v[8]) 
 }
 
 constexpr int kCUs = 256;            // compute units
+constexpr int kMulti = 0;            // lanes per row: the workgroup's
 constexpr int kMaxRowWaves = 8;      // waves that share a row
 // Chunks per lane: at most 4 (8 waves x 64 lanes x 4 chunks of 8 = 16384
 // columns).  The host launches NV only for rows that need the last chunk, so
@@ -110,14 +113,15 @@ __device__ __forceinline__ float inv_sqrt(float v) {
     return v <= 3.4028235e38f ? n : r;
 }
 
-// Sums of K values over the waves that share a row (one: no barrier).  `buf`
-// alternates between two LDS buffers from call to call: a wave can be at most
-// one barrier behind, so the buffer it still reads is not the one written.
-template <bool MULTI, int K>
+// Sums of K values over the lanes that share a row.  Over several waves (one:
+// no barrier) `buf` alternates between two LDS buffers from call to call: a
+// wave can be at most one barrier behind, so the buffer it still reads is not
+// the one written.
+template <int LPR, int K>
 __device__ __forceinline__ void row_sums(float (&v)[K], int wpr, float (*lds)[kMaxRowWaves][4], int& turn) {
 #pragma unroll
-    for (int i = 0; i < K; ++i) v[i] = lanes_sum<64>(v[i]);
-    if (!MULTI) return;
+    for (int i = 0; i < K; ++i) v[i] = lanes_sum<LPR == kMulti ? 64 : LPR>(v[i]);
+    if (LPR != kMulti) return;
     float (*buf)[4] = lds[turn & 1];
     turn++;
     if ((threadIdx.x & 63) == 0) {
@@ -141,5 +145,7 @@ inline void row_split(int64_t cols, int* wpr, int* nv) {
     *nv = (int)((groups + kMaxRowWaves - 1) / kMaxRowWaves);
     *wpr = (int)((groups + *nv - 1) / *nv);
 }
+// Lanes per row of a row that one wave holds in one chunk per lane.
+inline int row_lanes(int64_t cols) { return cols <= 128 ? 16 : cols <= 256 ? 32 : 64; }
 
 }  // namespace fp8bs

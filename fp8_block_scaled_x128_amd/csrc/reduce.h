@@ -53,6 +53,13 @@ __device__ __forceinline__ uint32_t row16_umin(uint32_t v) {
     return v;
 }
 
+// v + v of the lane 32 lanes away.
+__device__ __forceinline__ float halves_sum(float v) {
+    const uint32_t b = __float_as_uint(v);
+    const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
+    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+}
+
 // v + v of the lane 16, then 32 lanes away.  The swaps exchange the odd rows
 // (of 16 or 32 lanes) of their first operand with the even rows of the second;
 // given v twice they return the even rows' and the odd rows' values in every
@@ -60,10 +67,7 @@ __device__ __forceinline__ uint32_t row16_umin(uint32_t v) {
 __device__ __forceinline__ float rows_sum(float v) {
     const uint32_t a = __float_as_uint(v);
     const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
-    v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
-    const uint32_t b = __float_as_uint(v);
-    const auto q = __builtin_amdgcn_permlane32_swap(b, b, false, false);
-    return __uint_as_float(q[0]) + __uint_as_float(q[1]);
+    return halves_sum(__uint_as_float(p[0]) + __uint_as_float(p[1]));
 }
 
 // Sums over the lanes with the same index modulo n (a power of two, uniform).
@@ -101,7 +105,8 @@ __device__ __forceinline__ int wave_scan(int v) {
     return dpp_add<0x143, 0xc>(v);                       // lane 31 to rows 2, 3
 }
 
-// All-reduce over LANES lanes (16: a DPP row, 64: the wave).  The four rows of
+// All-reduce over LANES lanes (16: a DPP row, 32: two of them, sums only, 64:
+// the wave).  The four rows of
 // a wave meet in scalar registers: no LDS crossbar, and the result is uniform.
 // Every lane of the wave must be active.
 __device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
@@ -110,6 +115,11 @@ __device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
 template <int LANES>
 __device__ __forceinline__ float lanes_sum(float v) {
     v = row16_sum(v);
+    if (LANES == 32) {
+        const uint32_t a = __float_as_uint(v);
+        const auto p = __builtin_amdgcn_permlane16_swap(a, a, false, false);
+        v = __uint_as_float(p[0]) + __uint_as_float(p[1]);
+    }
     if (LANES == 64) {
         const uint32_t u = __float_as_uint(v);
         v = (__uint_as_float(lane_value(u, 0)) + __uint_as_float(lane_value(u, 16))) +

@@ -39,7 +39,7 @@ def make(rows, cols, kind, stream, wt, gate_rows, seed, pad=0):
 
 
 SHAPES = [(1, 8), (1, 2560), (3, 128), (5, 1000), (67, 136), (130, 2048), (33, 4104), (9, 9728), (4, 12296),
-          (2, 16384), (1, 512), (700, 64)]
+          (2, 16384), (1, 512), (700, 64), (1001, 128), (333, 256), (50, 200), (77, 24)]
 
 
 @pytest.mark.parametrize("rows,cols", SHAPES)
@@ -61,7 +61,8 @@ def test_forward(rows, cols, kind, stream, wt, gate_rows):
 
 
 @pytest.mark.parametrize("rows,cols", [(1, 8), (1, 2560), (5, 1000), (67, 136), (130, 2048), (33, 4104), (6, 9728),
-                                       (3, 12296), (2, 16384), (2500, 64), (3000, 520)])
+                                       (3, 12296), (2, 16384), (2500, 64), (3000, 520), (1001, 128), (9000, 128), (333, 256), (50, 200),
+                                       (77, 24)])
 @pytest.mark.parametrize("kind,stream,wt,gate_rows,dy_dt,dg_dt", [
     ("both", BF, BF, 0, F32, F32), ("both", F32, F32, 1, BF, BF), ("both", F32, BF, 7, BF, F32),
     ("both", BF, F32, 10 ** 9, F32, F32), ("pre", BF, F32, 0, BF, F32), ("pre", F32, F32, 0, F32, F32),
