@@ -592,44 +592,55 @@ def moe_forward_routed(codes, logits, top_k, qgu, sgu, qdt, sdt, *, renorm=True,
 
 
 # ---------------------------------- between the GEMMs: norms and the router
-def _otype(t_or_dtype):
-    dt = t_or_dtype.dtype if isinstance(t_or_dtype, torch.Tensor) else t_or_dtype
-    if dt == torch.bfloat16:
-        return OUT_BF16
-    if dt == torch.float32:
-        return OUT_FP32
-    raise TypeError("bfloat16 or float32 expected, got %s" % dt)
+# The smallest of these kernels run for 4 to 6 us and a launch costs 3, so the
+# conveniences below keep their own part short: one check per tensor, pointers
+# passed as plain integers.
+_BF, _F32, _I32 = torch.bfloat16, torch.float32, torch.int32
+_OTYPES = {_BF: OUT_BF16, _F32: OUT_FP32}
 
 
-def _on_device(*tensors):
-    """Every call runs on the current device's current stream: tensors that
-    live elsewhere are refused."""
-    cur = torch.cuda.current_device()
-    for t in tensors:
-        if t is not None and t.get_device() != cur:            # -1: host memory
-            raise ValueError("tensor on %s; the current device is cuda:%d" % (t.device, cur))
-
-
-def _matrix(name, t, rows, cols, *dtypes):
-    """The leading dimension of a [rows, cols] tensor with unit column stride
-    (0 without a tensor)."""
+def _otype(dtype):
+    t = _OTYPES.get(dtype)
     if t is None:
-        return 0
-    if t.dtype in dtypes and t.shape == (rows, cols):
+        raise TypeError("bfloat16 or float32 expected, got %s" % dtype)
+    return t
+
+
+def _device():
+    return torch.cuda.current_device()
+
+
+def _mat(name, t, rows, cols, dev, dt, dt2=None):
+    """(pointer, leading dimension) of a [rows, cols] tensor of type dt or dt2
+    with unit column stride on the current device; (None, 0) without one."""
+    if t is None:
+        return None, 0
+    d = t.dtype
+    if (d is dt or d is dt2) and t.shape == (rows, cols) and t.get_device() == dev:
         s0, s1 = t.stride()
         if s1 == 1 or cols <= 1:
-            return s0 if rows > 1 else cols                    # the stride of a single row is never used
-    raise ValueError("%s: [%d, %d] of %s with unit column stride expected, got %s %s, strides %s"
-                     % (name, rows, cols, "/".join(str(d) for d in dtypes), tuple(t.shape), t.dtype, t.stride()))
+            return t.data_ptr(), s0 if rows > 1 else cols      # the stride of a single row is never used
+    raise ValueError("%s: [%d, %d] of %s with unit column stride on cuda:%d expected, got %s %s, strides %s, on %s"
+                     % (name, rows, cols, dt if dt2 is None else "%s or %s" % (dt, dt2), dev, tuple(t.shape), d,
+                        t.stride(), t.device))
 
 
-def _vector(name, t, n, *dtypes):
-    if t is not None and (t.dtype not in dtypes or t.shape != (n,) or not t.is_contiguous()):
-        raise ValueError("%s: contiguous [%d] of %s expected, got %s %s"
-                         % (name, n, "/".join(str(d) for d in dtypes), tuple(t.shape), t.dtype))
+def _arr(name, t, shape, dev, dt):
+    """Pointer of a contiguous tensor of this shape and type on the current
+    device; None without one."""
+    if t is None:
+        return None
+    if t.dtype is dt and t.shape == shape and t.get_device() == dev and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError("%s: contiguous %s %s on cuda:%d expected, got %s %s on %s"
+                     % (name, dt, list(shape), dev, t.dtype, tuple(t.shape), t.device))
 
 
-_BF, _F32 = torch.bfloat16, torch.float32
+def _workspace(ws, dev):
+    """(pointer, bytes) of a workspace; the call itself checks its size."""
+    if ws is None:
+        return None, 0
+    return _arr("ws", ws, ws.shape, dev, torch.uint8), ws.numel()
 
 
 class BlockNorm(NamedTuple):
@@ -654,38 +665,40 @@ def block_norm(residual=None, x=None, *, w_pre=None, w_post=None, gate=None, row
     if ref is None:
         raise ValueError("residual or x is required")
     rows, cols = ref.shape
+    dev, ng = _device(), (cols + 127) // 128
     stream_dt = _BF if residual is None else residual.dtype
     stype = _otype(stream_dt)
-    ld_r, ld_x = _matrix("residual", residual, rows, cols, _BF, _F32), _matrix("x", x, rows, cols, _BF)
-    ld_g = 0
+    rp, ld_r = _mat("residual", residual, rows, cols, dev, stream_dt)
+    xp, ld_x = _mat("x", x, rows, cols, dev, _BF)
+    gp = ld_g = None
     if gate is not None:
         if rows_per_gate < 1:
             raise ValueError("rows_per_gate must be >= 1")
-        ld_g = _matrix("gate", gate, -(-rows // rows_per_gate), cols, _BF)
-    w = w_pre if w_pre is not None else w_post
-    wt = OUT_BF16 if w is None else _otype(w)
-    for name, v in (("w_pre", w_pre), ("w_post", w_post)):
-        _vector(name, v, cols, _BF if w is None else w.dtype)
+        gp, ld_g = _mat("gate", gate, -(-rows // rows_per_gate), cols, dev, _BF)
+    w = w_post if w_pre is None else w_pre
+    wdt = _BF if w is None else w.dtype
+    pre, post = _arr("w_pre", w_pre, (cols,), dev, wdt), _arr("w_post", w_post, (cols,), dev, wdt)
     if w_pre is None:
         y = quant = False
-    dev = ref.device
     if out is None:
-        ng = (cols + 127) // 128
-        out = BlockNorm(torch.empty((rows, cols), dtype=stream_dt, device=dev) if h else None,
-                        torch.empty((rows, cols), dtype=_BF, device=dev) if y else None,
-                        _u8((rows, cols), dev) if quant else None,
-                        torch.empty((ng, rows), dtype=_F32, device=dev).t() if quant else None)
+        e = lambda *shape, dt: torch.empty(shape, dtype=dt, device=ref.device)
+        out = BlockNorm(e(rows, cols, dt=stream_dt) if h else None, e(rows, cols, dt=_BF) if y else None,
+                        e(rows, cols, dt=torch.uint8) if quant else None, e(ng, rows, dt=_F32).t() if quant else None)
     ho, yo, qo, so = out
-    if (ho is not None) != bool(h) or (yo is not None) != bool(y) or (qo is not None) != bool(quant):
+    if (ho is None) is bool(h) or (yo is None) is bool(y) or (qo is None) is bool(quant):
         raise ValueError("out does not hold the outputs asked for")
-    ld_h, ld_y = _matrix("out.h", ho, rows, cols, stream_dt), _matrix("out.y", yo, rows, cols, _BF)
-    ld_q = _matrix("out.q", qo, rows, cols, torch.uint8)
-    if qo is not None and (so is None or so.dtype != _F32 or tuple(so.shape) != (rows, (cols + 127) // 128)):
-        raise ValueError("out.s: float32 [%d, %d] expected" % (rows, (cols + 127) // 128))
-    _on_device(residual, x, gate, w_pre, w_post, ho, yo, qo, so)
-    fp8_block_norm(rows, cols, x, ld_x, residual, ld_r, stype, gate, ld_g, rows_per_gate, scale, w_post, w_pre, wt,
-                   eps, ho, ld_h, yo, ld_y, qo, ld_q, so, 0 if so is None else so.stride(0),
-                   0 if so is None else so.stride(1))
+    hp, ld_h = _mat("out.h", ho, rows, cols, dev, stream_dt)
+    yp, ld_y = _mat("out.y", yo, rows, cols, dev, _BF)
+    qp, ld_q = _mat("out.q", qo, rows, cols, dev, torch.uint8)
+    sp = ssr = ssg = 0
+    if qo is not None:
+        if so is None or so.dtype is not _F32 or so.shape != (rows, ng) or so.get_device() != dev:
+            raise ValueError("out.s: float32 [%d, %d] on cuda:%d expected" % (rows, ng, dev))
+        sp, (ssr, ssg) = so.data_ptr(), so.stride()
+    st = load().fp8_block_norm(rows, cols, xp, ld_x, rp, ld_r, stype, gp, ld_g or 0, rows_per_gate, scale, post, pre,
+                               _otype(wdt), eps, hp, ld_h, yp, ld_y, qp, ld_q, sp or None, ssr, ssg, _stream())
+    if st:
+        _check("fp8_block_norm", st)
     return out
 
 
@@ -712,48 +725,50 @@ def block_norm_backward(dy=None, dh=None, h=None, x=None, *, w_pre=None, w_post=
     if ref is None:
         raise ValueError("dh, or dy with h, is required")
     rows, cols = ref.shape
+    dev = _device()
     stream_dt = ref.dtype
     stype = _otype(stream_dt)
-    if (dy is None) != (w_pre is None) or (dy is None) != (h is None):
+    if (dy is None) is not (w_pre is None) or (dy is None) is not (h is None):
         raise ValueError("dy, h and w_pre go together")
     if x is None and (w_post is not None or gate is not None):
         raise ValueError("w_post and gate need x")
-    ld_dy, ld_dh = _matrix("dy", dy, rows, cols, _BF, _F32), _matrix("dh", dh, rows, cols, stream_dt)
-    ld_h, ld_x = _matrix("h", h, rows, cols, stream_dt), _matrix("x", x, rows, cols, _BF)
-    ld_g = ngate = 0
+    dyp, ld_dy = _mat("dy", dy, rows, cols, dev, _BF, _F32)
+    dhp, ld_dh = _mat("dh", dh, rows, cols, dev, stream_dt)
+    hp, ld_h = _mat("h", h, rows, cols, dev, stream_dt)
+    xp, ld_x = _mat("x", x, rows, cols, dev, _BF)
+    gp, ld_g, ngate = None, 0, 0
     if gate is not None:
         if rows_per_gate < 1:
             raise ValueError("rows_per_gate must be >= 1")
         ngate = -(-rows // rows_per_gate)
-        ld_g = _matrix("gate", gate, ngate, cols, _BF)
-    w = w_pre if w_pre is not None else w_post
-    wt = OUT_BF16 if w is None else _otype(w)
-    for name, v in (("w_pre", w_pre), ("w_post", w_post)):
-        _vector(name, v, cols, _BF if w is None else w.dtype)
-    dev = ref.device
+        gp, ld_g = _mat("gate", gate, ngate, cols, dev, _BF)
+    w = w_post if w_pre is None else w_pre
+    wdt = _BF if w is None else w.dtype
+    pre, post = _arr("w_pre", w_pre, (cols,), dev, wdt), _arr("w_post", w_post, (cols,), dev, wdt)
     if out is None:
         need = fp8_block_norm_backward_ws_size(rows, cols, rows_per_gate, w_post is not None, w_pre is not None,
                                                gate is not None)
-        e = lambda n, dt: torch.empty((n, cols), dtype=dt, device=dev)
-        out = BlockNormGrads(e(rows, stream_dt) if dres else None, e(rows, _BF) if x is not None else None,
-                             e(ngate, dgate_dtype) if gate is not None else None,
-                             torch.empty(cols, dtype=_F32, device=dev) if w_post is not None else None,
-                             torch.empty(cols, dtype=_F32, device=dev) if w_pre is not None else None,
-                             _u8((need,), dev) if need else None)
-    o = out
-    for name, t, asked in (("dres", o.dres, dres), ("dx", o.dx, x is not None), ("dgate", o.dgate, gate is not None),
-                           ("dw_post", o.dw_post, w_post is not None), ("dw_pre", o.dw_pre, w_pre is not None)):
-        if (t is not None) != bool(asked):
-            raise ValueError("out.%s does not fit the call" % name)
-    ld_dres, ld_dx = _matrix("out.dres", o.dres, rows, cols, stream_dt), _matrix("out.dx", o.dx, rows, cols, _BF)
-    ld_dg = _matrix("out.dgate", o.dgate, ngate, cols, dgate_dtype)
-    _vector("out.dw_post", o.dw_post, cols, _F32)
-    _vector("out.dw_pre", o.dw_pre, cols, _F32)
-    _on_device(dy, dh, h, x, gate, w_pre, w_post, *o)
-    fp8_block_norm_backward(rows, cols, dy, ld_dy, OUT_BF16 if dy is None else _otype(dy), dh, ld_dh, h, ld_h, stype,
-                            x, ld_x, gate, ld_g, rows_per_gate, scale, w_post, w_pre, wt, eps, o.dx, ld_dx, o.dres,
-                            ld_dres, o.dgate, ld_dg, _otype(dgate_dtype), o.dw_post, o.dw_pre, o.ws,
-                            0 if o.ws is None else o.ws.numel())
+        e = lambda *shape, dt: torch.empty(shape, dtype=dt, device=ref.device)
+        out = BlockNormGrads(e(rows, cols, dt=stream_dt) if dres else None,
+                             None if x is None else e(rows, cols, dt=_BF),
+                             None if gate is None else e(ngate, cols, dt=dgate_dtype),
+                             None if w_post is None else e(cols, dt=_F32), None if w_pre is None else e(cols, dt=_F32),
+                             e(need, dt=torch.uint8) if need else None)
+    o_dres, o_dx, o_dgate, o_post, o_pre, ws = out
+    if ((o_dres is None) is bool(dres) or (o_dx is None) is not (x is None) or (o_dgate is None) is not (gate is None)
+            or (o_post is None) is not (w_post is None) or (o_pre is None) is not (w_pre is None)):
+        raise ValueError("out does not hold the outputs of this call")
+    drp, ld_dres = _mat("out.dres", o_dres, rows, cols, dev, stream_dt)
+    dxp, ld_dx = _mat("out.dx", o_dx, rows, cols, dev, _BF)
+    dgp, ld_dg = _mat("out.dgate", o_dgate, ngate, cols, dev, dgate_dtype)
+    dpost, dpre = _arr("out.dw_post", o_post, (cols,), dev, _F32), _arr("out.dw_pre", o_pre, (cols,), dev, _F32)
+    wsp, wsn = _workspace(ws, dev)
+    st = load().fp8_block_norm_backward(rows, cols, dyp, ld_dy, OUT_FP32 if dy is not None and dy.dtype is _F32 else
+                                        OUT_BF16, dhp, ld_dh, hp, ld_h, stype, xp, ld_x, gp, ld_g, rows_per_gate,
+                                        scale, post, pre, _otype(wdt), eps, dxp, ld_dx, drp, ld_dres, dgp, ld_dg,
+                                        _otype(dgate_dtype), dpost, dpre, wsp, wsn, _stream())
+    if st:
+        _check("fp8_block_norm_backward", st)
     return out
 
 
@@ -773,14 +788,6 @@ class Routing(NamedTuple):
     ws: Optional[torch.Tensor]
 
 
-def _mask_bytes(mask, T):
-    if mask is None:
-        return None
-    if mask.dtype not in (torch.bool, torch.uint8) or tuple(mask.shape) != (T,) or not mask.is_contiguous():
-        raise ValueError("mask: contiguous bool or uint8 [%d] expected" % T)
-    return mask
-
-
 def moe_route(logits, top_k, *, renorm=True, mask=None, out: Optional[Routing] = None) -> Routing:
     """Top-k routing of router logits [T, E] (bf16 or fp32): experts, weights,
     counts, the expert-sorted row maps of moe_forward and the grouped GEMMs,
@@ -788,25 +795,25 @@ def moe_route(logits, top_k, *, renorm=True, mask=None, out: Optional[Routing] =
     uint8): tokens with False are not routed.  `out` is an earlier result for
     the same sizes whose tensors are written again."""
     T, E = logits.shape
-    ld = _matrix("logits", logits, T, E, _BF, _F32)
-    mask = _mask_bytes(mask, T)
-    dev, i32 = logits.device, torch.int32
+    dev, tk = _device(), (T, top_k)
+    zp, ld = _mat("logits", logits, T, E, dev, _BF, _F32)
+    mp = None if mask is None else _arr("mask", mask, (T,), dev, mask.dtype if mask.dtype is torch.bool else torch.uint8)
     if out is None:
         need = fp8_moe_route_ws_size(T, E)
-        e = lambda *s, dtype=i32: torch.empty(s, dtype=dtype, device=dev)
-        out = Routing(e(T, top_k), e(T, top_k, dtype=_F32), e(E + 1), e(E + 1), e(T * top_k), e(T, top_k),
-                      e(T, dtype=_F32), e(2, dtype=_F32), _u8((need,), dev) if need else None)
-    o = out
-    for name, t, shape, dt in (("experts", o.experts, (T, top_k), i32), ("weights", o.weights, (T, top_k), _F32),
-                               ("counts", o.counts, (E + 1,), i32), ("offsets", o.offsets, (E + 1,), i32),
-                               ("row_token", o.row_token, (T * top_k,), i32),
-                               ("token_rows", o.token_rows, (T, top_k), i32), ("lse", o.lse, (T,), _F32),
-                               ("loss", o.loss, (2,), _F32)):
-        if t.shape != shape or t.dtype != dt or not t.is_contiguous():
-            raise ValueError("out.%s: contiguous %s %s expected" % (name, dt, list(shape)))
-    _on_device(logits, mask, *o)
-    fp8_moe_route(logits, T, E, ld, _otype(logits), top_k, int(bool(renorm)), mask, o.experts, o.weights, o.counts,
-                  o.offsets, o.row_token, o.token_rows, o.lse, o.loss, o.ws, 0 if o.ws is None else o.ws.numel())
+        e = lambda *shape, dt=_I32: torch.empty(shape, dtype=dt, device=logits.device)
+        out = Routing(e(*tk), e(*tk, dt=_F32), e(E + 1), e(E + 1), e(T * top_k), e(*tk), e(T, dt=_F32), e(2, dt=_F32),
+                      e(need, dt=torch.uint8) if need else None)
+    experts, weights, counts, offsets, row_token, token_rows, lse, loss, ws = out
+    wsp, wsn = _workspace(ws, dev)
+    st = load().fp8_moe_route(zp, T, E, ld, _OTYPES[logits.dtype], top_k, 1 if renorm else 0, mp,
+                              _arr("out.experts", experts, tk, dev, _I32), _arr("out.weights", weights, tk, dev, _F32),
+                              _arr("out.counts", counts, (E + 1,), dev, _I32),
+                              _arr("out.offsets", offsets, (E + 1,), dev, _I32),
+                              _arr("out.row_token", row_token, (T * top_k,), dev, _I32),
+                              _arr("out.token_rows", token_rows, tk, dev, _I32), _arr("out.lse", lse, (T,), dev, _F32),
+                              _arr("out.loss", loss, (2,), dev, _F32), wsp, wsn, _stream())
+    if st:
+        _check("fp8_moe_route", st)
     return out
 
 
@@ -814,19 +821,19 @@ def moe_route_backward(logits, experts, weights, counts, lse, *, dweights=None, 
     """dlogits [T, E] (the logits' type) of sum(weights * dweights) +
     dloss . loss, from moe_route's outputs (see fp8_moe_route_backward)."""
     T, E = logits.shape
-    k = experts.shape[1]
-    ld = _matrix("logits", logits, T, E, _BF, _F32)
-    for name, t, shape, dt in (("experts", experts, (T, k), torch.int32), ("weights", weights, (T, k), _F32),
-                               ("counts", counts, (E + 1,), torch.int32), ("lse", lse, (T,), _F32),
-                               ("dweights", dweights, (T, k), _F32), ("dloss", dloss, (2,), _F32)):
-        if t is not None and (t.shape != shape or t.dtype != dt or not t.is_contiguous()):
-            raise ValueError("%s: contiguous %s %s expected" % (name, dt, list(shape)))
+    dev, k, dt = _device(), experts.shape[1], logits.dtype
+    tk = (T, k)
+    zp, ld = _mat("logits", logits, T, E, dev, _BF, _F32)
     if out is None:
-        out = torch.empty((T, E), dtype=logits.dtype, device=logits.device)
-    ld_d = _matrix("out", out, T, E, logits.dtype)
-    _on_device(logits, experts, weights, counts, lse, dweights, dloss, out)
-    fp8_moe_route_backward(logits, T, E, ld, _otype(logits), k, int(bool(renorm)), experts, weights, counts, lse,
-                           dweights, dloss, out, ld_d)
+        out = torch.empty((T, E), dtype=dt, device=logits.device)
+    op, ld_d = _mat("out", out, T, E, dev, dt)
+    st = load().fp8_moe_route_backward(zp, T, E, ld, _OTYPES[dt], k, 1 if renorm else 0,
+                                       _arr("experts", experts, tk, dev, _I32), _arr("weights", weights, tk, dev, _F32),
+                                       _arr("counts", counts, (E + 1,), dev, _I32), _arr("lse", lse, (T,), dev, _F32),
+                                       _arr("dweights", dweights, tk, dev, _F32), _arr("dloss", dloss, (2,), dev, _F32),
+                                       op, ld_d, _stream())
+    if st:
+        _check("fp8_moe_route_backward", st)
     return out
 
 
@@ -835,21 +842,20 @@ def moe_combine_backward(dout, y, token_rows, weights, *, out=None):
     [T, H] (bf16 or fp32) and the y [rows, H] it read.  Rows of dy without a
     slot are not written."""
     T, H = dout.shape
-    k = token_rows.shape[1]
-    rows = y.shape[0]
-    ld_do, ld_y = _matrix("dout", dout, T, H, _BF, _F32), _matrix("y", y, rows, H, _BF)
-    for name, t, dt in (("token_rows", token_rows, torch.int32), ("weights", weights, _F32)):
-        if t.shape != (T, k) or t.dtype != dt or not t.is_contiguous():
-            raise ValueError("%s: contiguous %s [%d, %d] expected" % (name, dt, T, k))
+    dev, k, rows = _device(), token_rows.shape[1], y.shape[0]
+    dop, ld_do = _mat("dout", dout, T, H, dev, _BF, _F32)
+    yp, ld_y = _mat("y", y, rows, H, dev, _BF)
     if out is None:
         out = (torch.empty((rows, H), dtype=_BF, device=dout.device),
                torch.empty((T, k), dtype=_F32, device=dout.device))
     dy, dw = out
-    ld_dy = _matrix("out[0]", dy, rows, H, _BF)
-    if dw.shape != (T, k) or dw.dtype != _F32 or not dw.is_contiguous():
-        raise ValueError("out[1]: contiguous float32 [%d, %d] expected" % (T, k))
-    _on_device(dout, y, token_rows, weights, dy, dw)
-    fp8_moe_combine_backward(dout, ld_do, _otype(dout), y, rows, H, ld_y, token_rows, weights, T, k, dy, ld_dy, dw)
+    dyp, ld_dy = _mat("out[0]", dy, rows, H, dev, _BF)
+    st = load().fp8_moe_combine_backward(dop, ld_do, _OTYPES[dout.dtype], yp, rows, H, ld_y,
+                                         _arr("token_rows", token_rows, (T, k), dev, _I32),
+                                         _arr("weights", weights, (T, k), dev, _F32), T, k, dyp, ld_dy,
+                                         _arr("out[1]", dw, (T, k), dev, _F32), _stream())
+    if st:
+        _check("fp8_moe_combine_backward", st)
     return out
 
 
