@@ -81,6 +81,8 @@ __global__ void __launch_bounds__(kThreads) k_moe_combine(const uint16_t* __rest
 // in runs of 512 each (8 per lane): per run, dout is loaded once and up to
 // eight y rows are in flight, each giving its part of a dot product and
 // taking its dy row at once, so nothing of a row stays in registers.
+// HBM-bound: 16384 tokens x 2048, top-8, 1.14 GB in 205 us (5.6 TB/s, the rate
+// of a large copy).
 template <bool DO32, int WPT>
 __global__ void __launch_bounds__(kThreads) k_moe_combine_bwd(const void* __restrict__ dout, int64_t ld_do,
                                                               const uint16_t* __restrict__ y, int32_t rows,

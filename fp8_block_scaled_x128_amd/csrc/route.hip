@@ -9,6 +9,14 @@
 //   w_tj      exp(z_j - m) / sum over the selected, or p of the selected
 //   balance   E sum_e f_e P_e, f_e = counts_e / sum counts, P_e = mean_t p_te
 //   z loss    mean_t lse_t^2
+//
+// 10.6 MB move for 16384 tokens of 128 experts, 2 us at the rate of a copy; what
+// bounds the routing is the selection's rounds (850 vector instructions a
+// wave, 6 us of issue) and the latency of two dependent launches.  Measured,
+// top-8: 16384 tokens 9.6 us (selection) and 9.1 (placement); 32 tokens 6.0 in
+// one launch; 262144 tokens 137 in three.  The gradient at 16384 tokens 7.2.
+// A third launch that scanned the histograms made it 30.7 us, logits loaded one
+// after the other 26, placement sums by LDS shuffles 21.
 #include "device_common.h"
 #include "internal.h"
 #include "reduce.h"

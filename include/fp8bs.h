@@ -34,6 +34,10 @@
  *    their layout: the scale of (row r, group g) lives at
  *    s[r * s_stride_row + g * s_stride_group].  The GEMMs read activation
  *    scales fastest when s_stride_row == 1 ("M-major", [groups][rows]).
+ *  - Between the layer's GEMMs stand fp8_block_norm (the norms around a block
+ *    with its gate, residual add and the next layer's 1x128 codes) and
+ *    fp8_moe_route (the experts' rows from router logits), with their
+ *    gradients; these keep to the same conventions.
  *  - Calls are thread-safe and keep no state between calls apart from the
  *    per-device code-object load on first use.  The one exception is
  *    fp8_blockscaled_gemm_splitk_noalloc: its partials live in a device array
