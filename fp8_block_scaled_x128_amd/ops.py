@@ -542,8 +542,9 @@ def _moe_experts(qx, sx, T, qgu, sgu, qdt, sdt, offsets, row_token):
     dev = qx.device
     qh = _u8((rows, I), dev)
     shb = torch.empty((I // 128, rows), dtype=torch.float32, device=dev)
-    fp8_grouped_gemm_swiglu_quant(rows, I, H, G, offsets, row_token, T, qx, H, sx, sx.stride(0), sx.stride(1), qgu, H,
-                                  N2 * H, sgu, sgu.stride(0), sgu.stride(1), sgu.stride(2), qh, I, shb, 1, rows)
+    fp8_grouped_gemm_swiglu_quant(rows, I, H, G, offsets, row_token, T, qx, qx.stride(0) if T > 1 else H, sx,
+                                  sx.stride(0), sx.stride(1), qgu, H, N2 * H, sgu, sgu.stride(0), sgu.stride(1),
+                                  sgu.stride(2), qh, I, shb, 1, rows)
     y = torch.empty((rows, H), dtype=torch.bfloat16, device=dev)
     fp8_grouped_gemm(rows, H, I, G, offsets, None, rows, qh, I, shb, 1, rows, qdt, I, H * I, sdt, sdt.stride(0),
                      sdt.stride(2), sdt.stride(1), y, H, OUT_BF16)
@@ -575,15 +576,22 @@ def moe_forward(x, qgu, sgu, qdt, sdt, offsets, row_token, token_rows, weights, 
 def moe_forward_routed(codes, logits, top_k, qgu, sgu, qdt, sdt, *, renorm=True, mask=None,
                        out_dtype=torch.bfloat16):
     """One block-wise FP8 MoE layer from router logits [T, G]: moe_route, the
-    experts on the activation's codes, the combine.  codes = (q [T, H], s
-    [T, H/128]) as quant_rowblock or block_norm give them; weights as in
-    moe_forward.  Masked tokens reach no expert and get zeros.  Returns (out
+    experts on the activation's codes, the combine.  codes = (q [T, H] with
+    unit column stride, s [T, H/128]) as quant_rowblock or block_norm give
+    them; weights as in moe_forward.  Masked tokens reach no expert and get zeros.  Returns (out
     [T, H], routing, y): y is the experts' output, which
     moe_combine_backward reads."""
     qx, sx = codes
     T, H = qx.shape
-    if tuple(logits.shape) != (T, qgu.shape[0]):
-        raise ValueError("logits: [%d, %d] expected, got %s" % (T, qgu.shape[0], tuple(logits.shape)))
+    G, N2, Hw = qgu.shape
+    if logits.shape != (T, G):
+        raise ValueError("logits: [%d, %d] expected, got %s" % (T, G, tuple(logits.shape)))
+    if H != Hw or qdt.shape != (G, H, N2 // 2):
+        raise ValueError("codes of %d columns, experts of %s and %s" % (H, tuple(qgu.shape), tuple(qdt.shape)))
+    _mat("codes", qx, T, H, _device(), torch.uint8)
+    if sx.dtype is not _F32 or sx.shape != (T, (H + 127) // 128) or sx.get_device() != _device():
+        raise ValueError("scales of the codes: float32 [%d, %d] on cuda:%d expected, got %s %s on %s"
+                         % (T, (H + 127) // 128, _device(), sx.dtype, tuple(sx.shape), sx.device))
     r = moe_route(logits, top_k, renorm=renorm, mask=mask)
     y = _moe_experts(qx, sx, T, qgu, sgu, qdt, sdt, r.offsets, r.row_token)
     out = torch.empty((T, H), dtype=out_dtype, device=qx.device)

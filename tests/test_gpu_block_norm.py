@@ -289,3 +289,76 @@ def test_refusals():
         ops.block_norm_backward(t["x"], None, None, t["x"], w_pre=w)
     with pytest.raises(ValueError):
         ops.block_norm_backward(None, t["x"], None, None, w_post=w)
+
+
+@pytest.mark.parametrize("rows,cols", [(70, 128), (9, 1000), (5, 10240)])
+@pytest.mark.parametrize("gate_rows", [0, 1, 3])
+def test_without_residual_and_single_outputs(rows, cols, gate_rows):
+    """x alone (h = scale gate N(x)); each forward output alone has the bytes
+    it has beside the others."""
+    t = make(rows, cols, "both", BF, BF, gate_rows, rows + cols)
+    a = dict(w_pre=t["w_pre"], w_post=t["w_post"], gate=t["gate"], rows_per_gate=max(1, gate_rows), scale=0.7)
+    o = ops.block_norm(None, t["x"], **a)
+    h, mh, y, my = R.norm(None, t["x"], t["w_pre"], t["w_post"], t["gate"], max(1, gate_rows), 0.7, EPS)
+    R.close(o.h, h, mh, 64, "h")
+    R.close(o.y, y, my, 64, "y")
+    R.check_codes(o.q, o.s, y, my, 64, "codes")
+    for keep in ("h", "y", "quant"):
+        only = dict(a, h=keep == "h", y=keep == "y", quant=keep == "quant")
+        if keep == "h":
+            only["w_pre"] = None
+        b = ops.block_norm(None, t["x"], **only)
+        for n, v in zip(b._fields, b):
+            assert (v is not None) == (n in {"h": "h", "y": "y", "quant": "qs"}[keep])
+            assert v is None or torch.equal(v, getattr(o, n)), n
+
+
+@pytest.mark.parametrize("rows,cols", [(70, 128), (300, 64), (9, 1000), (5, 10240), (600, 2560)])
+@pytest.mark.parametrize("gate_rows", [0, 1, 3, 200])
+def test_gradients_one_at_a_time(rows, cols, gate_rows):
+    """Each gradient asked for alone, and without a gradient past y: bounds as
+    in test_backward."""
+    t = make(rows, cols, "both", BF, BF, gate_rows, rows + cols)
+    g = torch.Generator().manual_seed(7)
+    dy = (1e-2 * torch.randn(rows, cols, generator=g)).cuda()
+    Rg, ngate = max(1, gate_rows), -(-rows // max(1, gate_rows))
+    ref = R.norm_grad(dy, None, t["residual"], t["x"], t["w_pre"], t["w_post"], t["gate"], Rg, 0.7, EPS)
+    full = ops.block_norm_backward(dy, None, t["residual"], t["x"], w_pre=t["w_pre"], w_post=t["w_post"],
+                                   gate=t["gate"], rows_per_gate=Rg, scale=0.7, eps=EPS)
+    for name, (v, mag) in ref.items():
+        R.close(getattr(full, name), v, mag, 128 if name in ("dres", "dx") else 192 + rows, name)
+        o = torch.full_like(getattr(full, name), 9)
+        need = ops.fp8_block_norm_backward_ws_size(rows, cols, Rg, name == "dw_post", name == "dw_pre", name == "dgate")
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        pick = lambda n: o if n == name else None
+        ops.fp8_block_norm_backward(rows, cols, dy, cols, ops.OUT_FP32, None, 0, t["residual"], cols, ops.OUT_BF16,
+                                    t["x"], cols, t["gate"], cols, Rg, 0.7, t["w_post"], t["w_pre"], ops.OUT_BF16, EPS,
+                                    pick("dx"), cols, pick("dres"), cols, pick("dgate"), cols, ops.OUT_FP32,
+                                    pick("dw_post"), pick("dw_pre"), ws, need)
+        R.close(o, v, mag, 128 if name in ("dres", "dx") else 192 + rows, name + " alone")
+
+
+def test_rows_past_32_bit_offsets():
+    """Three rows 2^30 + 8 elements apart in every tensor: the last one starts
+    past 2^31 elements (and 2^32 bytes) from the first."""
+    rows, cols, ld = 3, 1000, 2 ** 30 + 8
+    t = make(rows, cols, "both", BF, BF, 1, 12)
+    g = torch.Generator().manual_seed(3)
+    dy, dh = [(1e-2 * torch.randn(rows, cols, generator=g)).to(BF).cuda() for _ in range(2)]
+    big = torch.empty(2 * ld + 8 * 1024, dtype=BF, device="cuda")
+    codes = torch.empty(2 * ld + 1024, dtype=torch.uint8, device="cuda")
+    at = lambda i: big[i * 1024:i * 1024 + 2 * ld + 1024].as_strided((rows, cols), (ld, 1))
+    a = dict(w_pre=t["w_pre"], w_post=t["w_post"], scale=0.7)
+    near = ops.block_norm(t["residual"], t["x"], gate=t["gate"], **a)
+    res, x, gate = at(0), at(1), at(2)
+    for far, v in ((res, "residual"), (x, "x"), (gate, "gate")):
+        far.copy_(t[v])
+    o = ops.block_norm(res, x, gate=gate, out=ops.BlockNorm(at(3), at(4), codes.as_strided((rows, cols), (ld, 1)), near.s.clone()), **a)
+    assert all(torch.equal(p, q) for p, q in zip(o, near))
+    ng = ops.block_norm_backward(dy, dh, near.h, t["x"], gate=t["gate"], dgate_dtype=BF, **a)
+    fdy, fdh = at(0), at(5)
+    fdy.copy_(dy)
+    fdh.copy_(dh)
+    out = ng._replace(dres=at(6), dx=at(7), dgate=at(4), dw_post=ng.dw_post.clone(), dw_pre=ng.dw_pre.clone(), ws=ng.ws.clone())
+    fg = ops.block_norm_backward(fdy, fdh, o.h, x, gate=gate, dgate_dtype=BF, out=out, **a)
+    assert all(torch.equal(p, q) for p, q in zip(fg[:5], ng[:5]))

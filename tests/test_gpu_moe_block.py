@@ -141,3 +141,65 @@ def test_serving_block_replays_in_a_graph(layer):
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(got, (*eo, *er[:8], out))), live
         assert int(r.counts[-1]) == live
+
+
+def test_codes_in_a_wider_buffer(layer):
+    """Codes whose rows lie in a wider buffer, as the norm writes them through
+    `out`, give the same block; codes that do not fit the experts are refused."""
+    d, weights = layer
+    x = dev_bf16(d["x"])
+    T, H = x.shape
+    z = torch.from_numpy(np.ascontiguousarray(d["logits"])).cuda()
+    w = torch.ones(H, dtype=BF, device="cuda")
+    ref = ops.block_norm(x, None, w_pre=w, h=False, y=False)
+    wide = torch.full((T, H + 128), 0x55, dtype=torch.uint8, device="cuda")
+    n = ops.block_norm(x, None, w_pre=w, h=False, y=False, out=ref._replace(q=wide[:, :H], s=torch.empty_like(ref.s)))
+    a, ra, _ = ops.moe_forward_routed((ref.q, ref.s), z, 2, *weights)
+    b, rb, _ = ops.moe_forward_routed((n.q, n.s), z, 2, *weights)
+    assert torch.equal(a, b) and torch.equal(ra.row_token, rb.row_token)
+    for q, s, zz in ((ref.q[:, :128], ref.s[:, :1], z), (ref.q.t().contiguous().t(), ref.s, z),
+                     (ref.q, ref.s[:, :1], z), (ref.q, ref.s.double(), z), (ref.q, ref.s, z[:, :4]),
+                     (ref.q.cpu(), ref.s, z), (ref.q.view(torch.int8), ref.s, z)):
+        with pytest.raises(ValueError):
+            ops.moe_forward_routed((q, s), zz, 2, *weights)
+
+
+def test_whole_block_replays_in_a_graph(layer):
+    """Norm, routing, the experts' products, the combine, the next norm and
+    the gradients back to the logits in one graph, its temporaries included;
+    replayed on new inputs and masks against the eager run."""
+    d, weights = layer
+    T, H = d["x"].shape
+    gen = torch.Generator(device="cuda").manual_seed(4)
+    stream, dy, dh = [torch.randn(T, H, device="cuda", generator=gen) for _ in range(3)]
+    w = torch.ones(H, device="cuda")
+    z = torch.randn(T, 8, device="cuda", generator=gen)
+    mask = torch.ones(T, dtype=torch.bool, device="cuda")
+    dl = torch.tensor([1e-2, 1e-3], device="cuda")
+
+    def step():
+        n1 = ops.block_norm(stream, None, w_pre=w, h=False, y=False)
+        out, r, y = ops.moe_forward_routed((n1.q, n1.s), z, 2, *weights, mask=mask)
+        n2 = ops.block_norm(stream, out, w_pre=w, w_post=w)
+        g = ops.block_norm_backward(dy, dh, n2.h, out, w_pre=w, w_post=w)
+        dyr, dw = ops.moe_combine_backward(g.dx, y, r.token_rows, r.weights)
+        dz = ops.moe_route_backward(z, r.experts, r.weights, r.counts, r.lse, dweights=dw, dloss=dl)
+        return (*n1[2:], out, *r[:8], *n2, *g[:2], *g[3:5], dw, dz)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        step()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        held = step()
+    for live in (T, 1, 0, 77):
+        stream.normal_()
+        z.normal_()
+        mask.copy_(torch.arange(T, device="cuda") < live)
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [v.clone() for v in held]
+        want = step()
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), live

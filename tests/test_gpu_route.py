@@ -284,3 +284,53 @@ def test_refusals():
         ops.moe_combine_backward(y[:10], y[:, :56], r.token_rows, r.weights)
     with pytest.raises(ValueError):
         ops.moe_combine_backward(y[:10], y, r.token_rows.long(), r.weights)
+
+
+def test_rows_past_32_bit_offsets():
+    """Logits, their gradient, the experts' rows and the combine's gradient in
+    rows 2^30 + 8 elements apart: the last one starts past 2^31 elements."""
+    T, E, k, H, ld = 3, 24, 1, 264, 2 ** 30 + 8
+    g = torch.Generator().manual_seed(6)
+    big = torch.empty(2 * ld + 5 * 512, dtype=BF, device="cuda")
+    at = lambda i, c: big[i * 512:i * 512 + 2 * ld + 512].as_strided((T, c), (ld, 1))
+    z, y, dout = torch.randn(T, E, generator=g), torch.randn(T, H, generator=g), torch.randn(T, H, generator=g)
+    z, y, dout = [v.to(BF).cuda() for v in (z, y, dout)]
+    fz, fy, fdout = at(0, E), at(1, H), at(2, H)
+    for far, near in ((fz, z), (fy, y), (fdout, dout)):
+        far.copy_(near)
+    r, f = ops.moe_route(z, k, renorm=False), ops.moe_route(fz, k, renorm=False)
+    assert all(torch.equal(p, q) for p, q in zip(r[:8], f[:8]))
+    dy, dw = ops.moe_combine_backward(dout, y, r.token_rows, r.weights)
+    fdy, fdw = ops.moe_combine_backward(fdout, fy, f.token_rows, f.weights, out=(at(3, H), torch.empty_like(dw)))
+    assert torch.equal(dy, fdy) and torch.equal(dw, fdw)
+    a, b = torch.empty(T, H, dtype=BF, device="cuda"), at(4, H)
+    ops.fp8_moe_combine_routed(y, T, H, H, r.token_rows, r.weights, T, k, a, H, ops.OUT_BF16)
+    ops.fp8_moe_combine_routed(fy, T, H, ld, r.token_rows, r.weights, T, k, b, ld, ops.OUT_BF16)
+    assert torch.equal(a, b)
+    arg = (r.experts, r.weights, r.counts, r.lse)
+    dz = ops.moe_route_backward(z, *arg, dweights=dw, renorm=False)
+    fdz = ops.moe_route_backward(fz, *arg, dweights=dw, renorm=False, out=at(3, E))
+    assert torch.equal(dz, fdz)
+
+
+def test_the_largest_router():
+    """2^22 tokens, the documented limit: 65536 workgroups' histograms in 256
+    runs.  The maps against torch's stable sort, the counts exactly."""
+    T, E, k = 2 ** 22, 8, 2
+    z = torch.randn(T, E, device="cuda", generator=torch.Generator(device="cuda").manual_seed(2))
+    z = (torch.floor(z * 2.0 ** 16) * 8 + torch.arange(E, device="cuda")) * 2.0 ** -19      # whole multiples: no ties
+    r = ops.moe_route(z, k)
+    top = torch.topk(z, k, dim=1)
+    assert torch.equal(r.experts.long(), top.indices)
+    flat = r.experts.reshape(-1).long()
+    order = torch.sort(flat, stable=True).indices
+    assert torch.equal(r.row_token.long(), order // k)
+    assert torch.equal(r.token_rows.reshape(-1).long()[order], torch.arange(T * k, device="cuda"))
+    counts = torch.stack([(flat == e).sum() for e in range(E)])
+    assert torch.equal(r.counts[:E].long(), counts) and int(r.counts[E]) == T
+    assert torch.equal(r.offsets[1:].long(), counts.cumsum(0))
+    p = torch.softmax(z.double(), 1)
+    want = E * float((counts.double() / (T * k) * p.mean(0)).sum())
+    # exp 32 and its sum 16; chains over 64 tokens, 16 waves, 256 workgroups,
+    # 256 runs and 16 waves again; the product with the counts and its sum 16
+    assert abs(float(r.loss[0]) - want) <= (32 + 16 + 64 + 16 + 256 + 256 + 16 + 16) * R.U * want
