@@ -87,8 +87,8 @@ struct NormBwdArgs {
 };
 // How the rows are dealt: `splits` units per gate row, a run of `chunk` rows
 // each (or over all rows, every splits-th row each), walked by `slots`
-// workgroups; the column sums'
-// partials lie at the three offsets (in floats) of the workspace.
+// workgroups (by_wave: by their waves); the column sums' partials lie at the
+// three offsets (in floats) of the workspace.
 struct NormBwdPlan {
     int wpr, nv;
     bool grouped, by_wave;

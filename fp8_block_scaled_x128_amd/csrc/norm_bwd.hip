@@ -23,8 +23,8 @@ namespace {
 
 constexpr int kWaves = 8;                // waves of a workgroup whose rows need one wave each
 
-// Adds the waves' register sums in wave order (one wave per row: 8 rows at a
-// time); the last wave's registers hold the result.
+// Adds the waves' register sums in wave order (rows that one wave holds); the
+// last wave's registers have the result.
 __device__ __forceinline__ void combine_waves(float (&a)[8], float (*comb)[8], int wave) {
     const int lane = threadIdx.x & 63;
     for (int w = 0; w < kWaves; ++w) {
@@ -510,11 +510,20 @@ NormBwdPlan plan_block_norm_bwd(int64_t rows, int64_t cols, int64_t rows_per_gat
     // sums.
     int64_t most = 2560 / (pl.wpr * pl.nv) / kCUs * kCUs;
     most = pl.wpr == 1 ? 2 * kCUs : most < kCUs ? kCUs : most > 4 * kCUs ? 4 * kCUs : most;
-    // gate rows of few rows go to single waves, whole, where there are enough
-    pl.by_wave = pl.wpr == 1 && pl.grouped && rows_per_gate < 64 && groups >= 2048;
+    // Many gate rows of few rows each go to single waves, whole: no barrier
+    // and no sum over waves for each.  A wave walks its gate row in `passes`
+    // alone, so few gate rows or long ones are faster by workgroup (us by wave
+    // / by workgroup, 128 columns: 600 gate rows of 6 / 16 / 48 rows 13.4 / 15.3
+    // / 28.5 against 19.7 / 21.4 / 26.1, 4200 26.0 / 36.6 / 85.8 against 65.0 /
+    // 69.6 / 92.9, 2100 of 100 105 against 88; 512 columns, a row at a time: 600
+    // of 2 16.8 against 14.8, 2100 of 6 / 16 29.8 / 59.5 against 32.7 / 49.1,
+    // 8192 of 8 95.5 against 103).
+    const int64_t wave_rows = 64 / row_lanes(cols), passes = (pl.unit_rows + wave_rows - 1) / wave_rows;
+    pl.by_wave = pl.wpr == 1 && pl.grouped &&
+                 (wave_rows > 1 ? passes <= 12 && groups >= 64 * passes : passes <= 8 && groups >= 320 * passes);
     int64_t splits = groups > 0 && !pl.by_wave ? most / groups : 1;
     if (splits < 1) splits = 1;
-    const int64_t at_once = pl.wpr == 1 && !pl.by_wave ? kWaves * 64 / row_lanes(cols) : 1;
+    const int64_t at_once = pl.wpr == 1 && !pl.by_wave ? kWaves * wave_rows : 1;
     if (splits > (longest + at_once - 1) / at_once) splits = (longest + at_once - 1) / at_once;
     if (splits < 1) splits = 1;
     pl.splits = splits;

@@ -1,7 +1,8 @@
 // Lane reductions shared by the norm and router kernels (64-wide waves).
-// The first four steps of every butterfly are DPP moves, which cost a VALU
-// instruction each; only the 16- and 32-lane steps go through LDS crossbar
-// shuffles.  Sums have a fixed order, so results do not depend on scheduling.
+// Inside the 16-lane rows the steps are DPP moves, which cost a VALU
+// instruction each or none; between the rows they are row swaps or reads into
+// scalar registers, so nothing goes through the LDS crossbar.  Sums have a
+// fixed order: results do not depend on scheduling.
 #pragma once
 #include <hip/hip_runtime.h>
 #include <stdint.h>
@@ -105,9 +106,8 @@ __device__ __forceinline__ int wave_scan(int v) {
     return dpp_add<0x143, 0xc>(v);                       // lane 31 to rows 2, 3
 }
 
-// All-reduce over LANES lanes (16: a DPP row, 32: two of them, sums only, 64:
-// the wave).  The four rows of
-// a wave meet in scalar registers: no LDS crossbar, and the result is uniform.
+// All-reduce over LANES lanes (16: a DPP row; 32: two of them, sums only; 64:
+// the wave, whose rows meet in scalar registers, so the result is uniform).
 // Every lane of the wave must be active.
 __device__ __forceinline__ uint32_t lane_value(uint32_t v, int lane) {
     return (uint32_t)__builtin_amdgcn_readlane((int)v, lane);

@@ -362,3 +362,18 @@ def test_rows_past_32_bit_offsets():
     out = ng._replace(dres=at(6), dx=at(7), dgate=at(4), dw_post=ng.dw_post.clone(), dw_pre=ng.dw_pre.clone(), ws=ng.ws.clone())
     fg = ops.block_norm_backward(fdy, fdh, o.h, x, gate=gate, dgate_dtype=BF, out=out, **a)
     assert all(torch.equal(p, q) for p, q in zip(fg[:5], ng[:5]))
+
+
+@pytest.mark.parametrize("rows,cols,gate_rows", [(1500, 64, 5), (2403, 128, 33), (3001, 128, 48), (6401, 256, 24),
+                                                 (4002, 512, 2), (2600, 512, 4), (5000, 264, 2)])
+def test_many_gate_rows(rows, cols, gate_rows):
+    """Gate rows that go to single waves, whole, and the last one short."""
+    t = make(rows, cols, "both", F32, BF, gate_rows, rows + cols)
+    g = torch.Generator().manual_seed(5)
+    dy, dh = [(1e-2 * torch.randn(rows, cols, generator=g)).cuda() for _ in range(2)]
+    o = ops.block_norm_backward(dy, dh, t["residual"], t["x"], w_pre=t["w_pre"], w_post=t["w_post"], gate=t["gate"],
+                                rows_per_gate=gate_rows, scale=0.7, eps=EPS)
+    ref = R.norm_grad(dy, dh, t["residual"], t["x"], t["w_pre"], t["w_post"], t["gate"], gate_rows, 0.7, EPS)
+    for name, (v, mag) in ref.items():
+        c = 128 if name in ("dres", "dx") else 192 + (gate_rows if name == "dgate" else rows)
+        R.close(getattr(o, name), v, mag, c, name)
