@@ -97,8 +97,9 @@ struct NormBwdPlan {
     size_t off_pre, off_post, off_gate, ws_floats;
     float *ws_pre, *ws_post, *ws_gate;
 };
+// bf16 rows (the default) need the largest workspace.
 NormBwdPlan plan_block_norm_bwd(int64_t rows, int64_t cols, int64_t rows_per_gate, bool dw_pre, bool dw_post,
-                                bool dgate);
+                                bool dgate, bool res32 = false, bool dy32 = false);
 hipError_t launch_block_norm_bwd(const NormBwdArgs& p, float* ws, hipStream_t st);
 
 // route.hip

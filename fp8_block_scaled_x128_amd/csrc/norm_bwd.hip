@@ -7,9 +7,10 @@
 //   xh = x r';  dn = scale gate dH;  dgate = sum scale dH xh w_post
 //   dw_post = sum_rows dn xh;  dx = r' (dn w_post - xh mean(dn w_post xh))
 //
-// HBM-bound.  A workgroup walks units of rows that share a gate row; its column sums of dw_pre and dw_post stay in registers over all its
-// rows and leave one partial row each, which k_col_reduce adds in workgroup
-// order (no atomics: the same bits every time).
+// HBM-bound.  A workgroup walks units of rows that share a gate row; its column
+// sums of dw_pre and dw_post stay in registers over all its rows and leave one
+// partial row each, which k_col_reduce adds in workgroup order (no atomics: the
+// same bits every time).
 //
 // Measured: 4096x2560 with an fp32 dy, 147 MB, 30.8 us (4.8 TB/s) and 4.7 us
 // for the column sums; 16384x2048 over an fp32 stream with the gradient of a
@@ -21,28 +22,34 @@
 namespace fp8bs {
 namespace {
 
-constexpr int kWaves = 8;                // waves of a workgroup whose rows need one wave each
+// Waves of a workgroup whose rows need one wave each: a gradient summed over gate
+// rows has no registers for two workgroups of eight on a compute unit, three of
+// four fit (28800x128 with a gate per 48 rows 24.2 -> 19.4 us); without it four
+// cost more (32768x512 41.0 -> 39.2 with eight).
+constexpr int row_waves(bool gate_sum) { return gate_sum ? 4 : 8; }
 
-// Adds the waves' register sums in wave order (rows that one wave holds); the
-// last wave's registers have the result.
-__device__ __forceinline__ void combine_waves(float (&a)[8], float (*comb)[8], int wave) {
-    const int lane = threadIdx.x & 63;
-    for (int w = 0; w < kWaves; ++w) {
-        __syncthreads();
-        if (wave == w) {
-            float4* s = reinterpret_cast<float4*>(comb[lane]);
-            if (w > 0) {
-                const float4 u = s[0], v = s[1];
-                a[0] += u.x; a[1] += u.y; a[2] += u.z; a[3] += u.w;
-                a[4] += v.x; a[5] += v.y; a[6] += v.z; a[7] += v.w;
-            }
-            s[0] = make_float4(a[0], a[1], a[2], a[3]);
-            s[1] = make_float4(a[4], a[5], a[6], a[7]);
-        }
+// Sums over the waves (rows that one wave holds), added in wave order: thread t
+// returns those of columns 2 t and 2 t + 1, from the sums that lanes 0 .. LPR -
+// 1 of each wave hold.
+template <int LPR, int WAVES>
+__device__ __forceinline__ float2 column_sums(const float (&a)[8], float (*comb)[512], int wave) {
+    const int lane = threadIdx.x & 63, t = threadIdx.x & (4 * LPR - 1);
+    __syncthreads();                                // the last call's sums have been read
+    if (lane < LPR) {
+        float4* s = reinterpret_cast<float4*>(&comb[wave][8 * lane]);
+        s[0] = make_float4(a[0], a[1], a[2], a[3]);
+        s[1] = make_float4(a[4], a[5], a[6], a[7]);
     }
     __syncthreads();
+    float2 v = *reinterpret_cast<const float2*>(&comb[0][2 * t]);
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) {
+        const float2 u = *reinterpret_cast<const float2*>(&comb[w][2 * t]);
+        v.x += u.x;
+        v.y += u.y;
+    }
+    return v;
 }
-
 // Adds the sums of a wave's rows.
 template <int LPR>
 __device__ __forceinline__ void add_rows(float (&a)[8]) {
@@ -152,23 +159,25 @@ struct RowIn {
 // LPR lanes have a row; kMulti: a workgroup has one row at a time.
 //
 // The next row is loaded while this one is reduced and stored, as far as the
-// registers go (AHEAD).  Loads return in order, so a weight load from the L2 behind the next row's loads would
-// wait for them: up to two chunks per lane the weights stay in registers
-// (KEEP), above that each row's are loaded ahead of the next row's data.
+// registers go (AHEAD).  Loads return in order, so a weight load from the L2
+// behind the next row's loads would wait for them: up to two chunks per lane
+// the weights stay in registers (KEEP), above that each row's are loaded ahead
+// of the next row's data.
 // Column sums are in registers too up to two chunks per lane; above that the
 // registers would spill (2048x10240: 99 us, 71 now), and each lane keeps its
 // columns' sums in LDS, 8 bytes a column and weight (halves of a chunk 16 bytes
 // apart from lane to lane: no bank conflicts).  Four chunks per lane (more than
 // 12288 columns) still spill: 2048x16384 runs at 2.6 TB/s.
 template <int NV, bool RES32, bool DY32, int LPR, int GATE>
-__global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPlan pl) {
+__global__ void __launch_bounds__(64 * (LPR == kMulti ? kMaxRowWaves : row_waves(GATE == kGateSum))) k_block_norm_bwd(NormBwdArgs p, NormBwdPlan pl) {
     constexpr bool MULTI = LPR == kMulti, SHARED = LPR == 16 || LPR == 32;     // SHARED: a wave has several rows
     constexpr bool GACC = GATE == kGateSum;
+    constexpr int WAVES = row_waves(GACC);          // of a workgroup whose rows need one wave each
     constexpr bool KEEP = NV <= 2;
     constexpr bool AHEAD = NV <= 2 || (NV == 3 && GATE == kGateNone);
     constexpr int KEPT = KEEP ? NV : 1;
     __shared__ float lds[2][kMaxRowWaves][4];
-    __shared__ float comb[MULTI ? 1 : 64][8];
+    __shared__ __align__(16) float comb[MULTI ? 1 : WAVES][512];
     __shared__ float4 lacc[KEEP ? 1 : NV * 4][KEEP ? 1 : 64 * kMaxRowWaves];
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wpr = pl.wpr;
@@ -202,12 +211,12 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
     // units by workgroup, its waves taking rows in turn; or (short gate rows)
     // by wave
     const bool by_wave = !MULTI && pl.by_wave;
-    const int64_t u0 = by_wave ? (int64_t)blockIdx.x * kWaves + wave : blockIdx.x;
-    const int64_t ustep = by_wave ? (int64_t)gridDim.x * kWaves : gridDim.x;
+    const int64_t u0 = by_wave ? (int64_t)blockIdx.x * WAVES + wave : blockIdx.x;
+    const int64_t ustep = by_wave ? (int64_t)gridDim.x * WAVES : gridDim.x;
     // a unit's rows: a run of a gate row's rows, or every splits-th of all
     // rows, as many at a time as the workgroup (or wave) holds
     constexpr int kWaveRows = MULTI ? 1 : 64 / (MULTI ? 64 : LPR);
-    const int at_once = MULTI ? 1 : by_wave ? kWaveRows : kWaves * kWaveRows;
+    const int at_once = MULTI ? 1 : by_wave ? kWaveRows : WAVES * kWaveRows;
     const int64_t rstep = GACC ? at_once : pl.splits * at_once;
     for (int64_t u = u0; u < pl.units; u += ustep) {
         const int64_t g = u / pl.splits;
@@ -352,18 +361,24 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
             }
         }
         if (GACC) {
-            if (!MULTI) {
-                add_rows<LPR>(agate[0]);
-                if (!by_wave) combine_waves(agate[0], comb, wave);
-            }
-            if (MULTI || by_wave || wave == kWaves - 1) {
+            void* dst = pl.splits > 1 ? (void*)row_ptr<true>(pl.ws_gate, u, p.cols)
+                        : p.dgate32   ? (void*)row_ptr<true>(p.dgate, g, p.ld_dgate)
+                                      : (void*)row_ptr<false>(p.dgate, g, p.ld_dgate);
+            const bool f32 = pl.splits > 1 || p.dgate32;
+            if (!MULTI) add_rows<LPR>(agate[0]);
+            if (!MULTI && !by_wave) {
+                const float2 v = column_sums<MULTI ? 64 : LPR, WAVES>(agate[0], comb, wave);
+                if (2 * (int)threadIdx.x < p.cols) {
+                    if (f32) static_cast<float2*>(dst)[threadIdx.x] = v;
+                    else static_cast<uint32_t*>(dst)[threadIdx.x] = pack_bf16x2(v.x, v.y);
+                }
+            } else {
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
                     const int c = tid + i * step;
                     if ((i >= kSure<NV> && c >= nc) || sub > 0) continue;
-                    if (pl.splits > 1) store8<true>(row_ptr<true>(pl.ws_gate, u, p.cols), c, agate[GACC ? i : 0]);
-                    else if (p.dgate32) store8<true>(row_ptr<true>(p.dgate, g, p.ld_dgate), c, agate[GACC ? i : 0]);
-                    else store8<false>(row_ptr<false>(p.dgate, g, p.ld_dgate), c, agate[GACC ? i : 0]);
+                    if (f32) store8<true>(dst, c, agate[GACC ? i : 0]);
+                    else store8<false>(dst, c, agate[GACC ? i : 0]);
                 }
             }
         }
@@ -371,9 +386,16 @@ __global__ void __launch_bounds__(512) k_block_norm_bwd(NormBwdArgs p, NormBwdPl
     if (!MULTI) {
         add_rows<LPR>(awpre[0]);
         add_rows<LPR>(awpost[0]);
-        if (p.dw_pre) combine_waves(awpre[0], comb, wave);
-        if (p.dw_post) combine_waves(awpost[0], comb, wave);
-        if (wave != kWaves - 1 || sub > 0) return;
+        const int64_t at = (int64_t)blockIdx.x * p.cols;
+        if (p.dw_pre) {
+            const float2 v = column_sums<MULTI ? 64 : LPR, WAVES>(awpre[0], comb, wave);
+            if (2 * (int)threadIdx.x < p.cols) reinterpret_cast<float2*>(pl.ws_pre + at)[threadIdx.x] = v;
+        }
+        if (p.dw_post) {
+            const float2 v = column_sums<MULTI ? 64 : LPR, WAVES>(awpost[0], comb, wave);
+            if (2 * (int)threadIdx.x < p.cols) reinterpret_cast<float2*>(pl.ws_post + at)[threadIdx.x] = v;
+        }
+        return;
     }
 #pragma unroll
     for (int i = 0; i < NV; ++i) {
@@ -465,7 +487,7 @@ hipError_t launch_types(const NormBwdArgs& p, const NormBwdPlan& pl, hipStream_t
                                      : k_block_norm_bwd<NV, true, false, LPR, GATE>)
                            : (p.dy32 ? k_block_norm_bwd<NV, false, true, LPR, GATE>
                                      : k_block_norm_bwd<NV, false, false, LPR, GATE>);
-    hipLaunchKernelGGL(k, dim3((unsigned)pl.slots), dim3(LPR == kMulti ? 64 * pl.wpr : 64 * kWaves), 0, st, p, pl);
+    hipLaunchKernelGGL(k, dim3((unsigned)pl.slots), dim3(64 * (LPR == kMulti ? pl.wpr : row_waves(GATE == kGateSum))), 0, st, p, pl);
     return hipGetLastError();
 }
 
@@ -495,7 +517,7 @@ hipError_t launch_rows(const NormBwdArgs& p, const NormBwdPlan& pl, hipStream_t 
 }  // namespace
 
 NormBwdPlan plan_block_norm_bwd(int64_t rows, int64_t cols, int64_t rows_per_gate, bool dw_pre, bool dw_post,
-                                bool dgate) {
+                                bool dgate, bool res32, bool dy32) {
     NormBwdPlan pl{};
     row_split(cols, &pl.wpr, &pl.nv);
     pl.grouped = dgate && rows_per_gate > 1;
@@ -507,29 +529,34 @@ NormBwdPlan plan_block_norm_bwd(int64_t rows, int64_t cols, int64_t rows_per_gat
     // 32.9 / 39.9 us; 16384x768, two waves: 512 / 1024 61.4 / 41.1; 4096x5120,
     // five waves with two chunks: 256 / 512 56.0 / 64.5; 16384x2048 gated, four
     // waves: 512 / 632 132 / 145).  Every workgroup more costs a row of partial
-    // sums.
+    // sums.  Rows of one wave or less: three workgroups of four waves per
+    // compute unit with gate sums; else two of eight, or one where the
+    // registers of fp32 rows leave room for no second (16384x128, fp32 stream:
+    // 17.7 / 14.9 us, fp32 dy 16.1 / 12.8; 32768x512, fp32 stream 63.7 / 60.4,
+    // fp32 dy, which leaves room, 45.6 / 46.5).
+    const int waves = row_waves(pl.grouped);
+    const bool single = res32 || (dy32 && row_lanes(cols) < 64);
     int64_t most = 2560 / (pl.wpr * pl.nv) / kCUs * kCUs;
-    most = pl.wpr == 1 ? 2 * kCUs : most < kCUs ? kCUs : most > 4 * kCUs ? 4 * kCUs : most;
+    most = pl.wpr == 1 ? (pl.grouped ? 3 : single ? 1 : 2) * kCUs : most < kCUs ? kCUs : most > 4 * kCUs ? 4 * kCUs : most;
     // Many gate rows of few rows each go to single waves, whole: no barrier
     // and no sum over waves for each.  A wave walks its gate row in `passes`
     // alone, so few gate rows or long ones are faster by workgroup (us by wave
-    // / by workgroup, 128 columns: 600 gate rows of 6 / 16 / 48 rows 13.4 / 15.3
-    // / 28.5 against 19.7 / 21.4 / 26.1, 4200 26.0 / 36.6 / 85.8 against 65.0 /
-    // 69.6 / 92.9, 2100 of 100 105 against 88; 512 columns, a row at a time: 600
-    // of 2 16.8 against 14.8, 2100 of 6 / 16 29.8 / 59.5 against 32.7 / 49.1,
-    // 8192 of 8 95.5 against 103).
+    // / by workgroup, 128 columns: 100 and 300 gate rows of 8 rows 8.4 / 7.7 and
+    // 8.9 / 9.4; 600, 2100, 6000 of 16 13.1 / 12.3, 20.0 / 22.2, 34.6 / 42.1;
+    // 1100 and 6000 of 32 22.7 / 20.7 and 60.7 / 65.4, of 48 28.6 / 24.6 and 98.2
+    // / 96.0; 512 columns, a row per pass: 1100 of 4 and 8 16.7 / 17.1 and 23.7 /
+    // 21.3, 6000 36.8 / 43.5 and 68.8 / 69.2).
     const int64_t wave_rows = 64 / row_lanes(cols), passes = (pl.unit_rows + wave_rows - 1) / wave_rows;
-    pl.by_wave = pl.wpr == 1 && pl.grouped &&
-                 (wave_rows > 1 ? passes <= 12 && groups >= 64 * passes : passes <= 8 && groups >= 320 * passes);
+    pl.by_wave = pl.wpr == 1 && pl.grouped && passes <= 8 && groups >= 256 * passes;
     int64_t splits = groups > 0 && !pl.by_wave ? most / groups : 1;
     if (splits < 1) splits = 1;
-    const int64_t at_once = pl.wpr == 1 && !pl.by_wave ? kWaves * wave_rows : 1;
+    const int64_t at_once = pl.wpr == 1 && !pl.by_wave ? waves * wave_rows : 1;
     if (splits > (longest + at_once - 1) / at_once) splits = (longest + at_once - 1) / at_once;
     if (splits < 1) splits = 1;
     pl.splits = splits;
     pl.chunk = (longest + splits - 1) / splits;
     pl.units = groups * pl.splits;
-    const int64_t want = pl.by_wave ? (pl.units + kWaves - 1) / kWaves : pl.units;
+    const int64_t want = pl.by_wave ? (pl.units + waves - 1) / waves : pl.units;
     pl.slots = (int32_t)(want < most ? want : most);
     pl.groups = groups;
     size_t f = 0;
@@ -544,7 +571,8 @@ NormBwdPlan plan_block_norm_bwd(int64_t rows, int64_t cols, int64_t rows_per_gat
 }
 
 hipError_t launch_block_norm_bwd(const NormBwdArgs& p, float* ws, hipStream_t st) {
-    NormBwdPlan pl = plan_block_norm_bwd(p.rows, p.cols, p.rows_per_gate, p.dw_pre, p.dw_post, p.dgate);
+    NormBwdPlan pl = plan_block_norm_bwd(p.rows, p.cols, p.rows_per_gate, p.dw_pre, p.dw_post, p.dgate, p.res32,
+                                         p.dy32);
     pl.ws_pre = ws + pl.off_pre;
     pl.ws_post = ws + pl.off_post;
     pl.ws_gate = ws + pl.off_gate;

@@ -365,7 +365,8 @@ def test_rows_past_32_bit_offsets():
 
 
 @pytest.mark.parametrize("rows,cols,gate_rows", [(1500, 64, 5), (2403, 128, 33), (3001, 128, 48), (6401, 256, 24),
-                                                 (4002, 512, 2), (2600, 512, 4), (5000, 264, 2)])
+                                                 (4002, 512, 2), (2600, 512, 4), (5000, 264, 2),
+                                                 (2600, 64, 5), (20001, 128, 16), (9000, 256, 6)])
 def test_many_gate_rows(rows, cols, gate_rows):
     """Gate rows that go to single waves, whole, and the last one short."""
     t = make(rows, cols, "both", F32, BF, gate_rows, rows + cols)
