@@ -218,15 +218,16 @@ __device__ __forceinline__ float2 select_tokens(const RouteArgs& p, int64_t t0, 
     return make_float2(sums[0], sums[1]);
 }
 
-// The rows of a workgroup's tokens, given in LDS the masks and the first row
-// of each expert for them, and the zeros of row_token behind the last row.
+// The row of a workgroup's slot i with expert e, given the masks in LDS and the
+// expert's first row for the workgroup, and the zeros of row_token behind the
+// last row.
 __device__ __forceinline__ void place_row(const RouteArgs& p, int64_t t0, int64_t i, int e,
-                                          const unsigned long long* mask, const int* base, int total) {
+                                          const unsigned long long* mask, int first, int total) {
     const int64_t at = t0 * p.k + i;
     const int tt = (int)((uint32_t)i / (uint32_t)p.k);
     int row = -1;
     if (e >= 0) {
-        row = base[e] + __popcll(mask[e] & ((1ull << tt) - 1));
+        row = first + __popcll(mask[e] & ((1ull << tt) - 1));
         p.row_token[row] = (int32_t)(t0 + tt);
     }
     p.token_rows[at] = row;
@@ -262,8 +263,10 @@ __global__ void __launch_bounds__(kThreads) k_route_one(RouteArgs p) {
     scan_experts(counts, base, p.E);
     __syncthreads();
     for (int e = threadIdx.x; e <= p.E; e += kThreads) p.offsets[e] = base[e];
-    for (int64_t i = threadIdx.x; i < p.T * p.k; i += kThreads)
-        place_row(p, 0, i, p.experts[i], mask, base, base[p.E]);
+    for (int64_t i = threadIdx.x; i < p.T * p.k; i += kThreads) {
+        const int e = p.experts[i];
+        place_row(p, 0, i, e, mask, base[max(e, 0)], base[p.E]);
+    }
     if (threadIdx.x == 0) {
         p.counts[p.E] = (int)s.y;
         write_losses(p, f[0], s.x, base[p.E], (int)s.y);
@@ -315,8 +318,9 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
     const int epad = ws.epad, nch = epad >> 4;      // chunks of 16 experts: a power of two, at most 64
     unsigned long long* mask = reinterpret_cast<unsigned long long*>(dyn);
     int* counts = reinterpret_cast<int*>(mask + epad);
-    int* base = counts + epad;                      // [epad + 1], then the waves' sums
-    uint32_t* part = reinterpret_cast<uint32_t*>(base + epad + 4);     // [8 waves][nch][16]
+    int* base = counts + epad;                      // [epad + 1], padded to 16 bytes
+    int* earlier = base + epad + 4;                 // [epad] rows of workgroups before this one
+    uint32_t* part = reinterpret_cast<uint32_t*>(earlier + epad);      // [8 waves][nch][16]
     // the workgroup without tokens goes first: it has the longest way
     const int blk = (int)blockIdx.x - 1;
     const int64_t t0 = (int64_t)blk * kTok;
@@ -348,14 +352,14 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
     for (int i = 0; i < 8; ++i) tot[i] = pre[i] = 0;
     const int ch = threadIdx.x & (nch - 1), rows = kThreads / nch;
     const int b1 = SUPER ? max(blk, 0) : nblk, b0 = SUPER ? b1 & ~(kRun - 1) : 0;
-    // four rows in flight; rows past the last are loaded again and not added
-    for (int b = b0 + threadIdx.x / nch; b < b1; b += 4 * rows) {
-        uint4 v[4];
+    // two rows in flight; rows past the last are loaded again and not added
+    for (int b = b0 + threadIdx.x / nch; b < b1; b += 2 * rows) {
+        uint4 v[2];
 #pragma unroll
-        for (int u = 0; u < 4; ++u)
+        for (int u = 0; u < 2; ++u)
             v[u] = *reinterpret_cast<const uint4*>(ws.hist + (int64_t)min(b + u * rows, b1 - 1) * epad + 16 * ch);
 #pragma unroll
-        for (int u = 0; u < 4; ++u) {
+        for (int u = 0; u < 2; ++u) {
             if (b + u * rows < b1) add_bytes(tot, v[u]);
             if (b + u * rows < min(b1, blk)) add_bytes(pre, v[u]);
         }
@@ -364,15 +368,22 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
     lanes_sum_mod(tot, nch);
     lanes_sum_mod(pre, nch);
     const int wave = threadIdx.x >> 6;
-    uint32_t* dst = part + ((wave & (kHalf - 1)) * nch + ch) * 16;
+    uint4* d4 = reinterpret_cast<uint4*>(part + ((wave & (kHalf - 1)) * nch + ch) * 16);
     if (wave >= kHalf && (int)(threadIdx.x & 63) < nch) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) { dst[i] = tot[i]; dst[8 + i] = pre[i]; }
+        for (int i = 0; i < 2; ++i) {
+            d4[i] = make_uint4(tot[4 * i], tot[4 * i + 1], tot[4 * i + 2], tot[4 * i + 3]);
+            d4[2 + i] = make_uint4(pre[4 * i], pre[4 * i + 1], pre[4 * i + 2], pre[4 * i + 3]);
+        }
     }
     __syncthreads();
     if (wave < kHalf && (int)(threadIdx.x & 63) < nch) {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) { dst[i] += tot[i]; dst[8 + i] += pre[i]; }
+        for (int i = 0; i < 2; ++i) {
+            const uint4 a = d4[i], b = d4[2 + i];
+            d4[i] = make_uint4(a.x + tot[4 * i], a.y + tot[4 * i + 1], a.z + tot[4 * i + 2], a.w + tot[4 * i + 3]);
+            d4[2 + i] = make_uint4(b.x + pre[4 * i], b.y + pre[4 * i + 1], b.z + pre[4 * i + 2], b.w + pre[4 * i + 3]);
+        }
     }
     __syncthreads();
 #pragma unroll
@@ -402,6 +413,7 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
             before += (int)((src[8 + word] >> sh) & 0xffffu);
         }
         counts[e] = SUPER ? 0 : c;
+        earlier[e] = before;
     }
     __syncthreads();
     if (SUPER) {
@@ -412,6 +424,7 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
             int c = 0;
             for (int r = threadIdx.x; r < kThreads; r += epad) { c += runs[r]; before += runs[kThreads + r]; }
             counts[threadIdx.x] = c;
+            earlier[threadIdx.x] = before;
         }
         __syncthreads();
     }
@@ -419,13 +432,10 @@ __global__ void __launch_bounds__(kThreads) k_route_place(RouteArgs p, RouteWs w
     __syncthreads();
     const int total = base[p.E];
     if (tokens) {
-        __syncthreads();
-        if ((int)threadIdx.x < p.E) base[threadIdx.x] += before;
-        __syncthreads();
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
-            const int i = threadIdx.x + u * kThreads;
-            if (i < n) place_row(p, t0, i, es[u], mask, base, total);
+            const int i = threadIdx.x + u * kThreads, e = max(es[u], 0);
+            if (i < n) place_row(p, t0, i, es[u], mask, base[e] + earlier[e], total);
         }
         return;
     }
@@ -657,7 +667,7 @@ hipError_t launch_moe_route(const RouteArgs& p, void* wsp, hipStream_t st) {
     const RouteWs ws = route_ws(p.T, p.E, wsp, &bytes);
     hipError_t e = by_experts<Select>(p.E, p, ws, nblk, st);
     if (e != hipSuccess || nblk <= 1) return e;
-    const size_t lds = (size_t)ws.epad * 16 + 16 + (size_t)kThreads * 8 + (size_t)kHalf * ws.epad * 4;
+    const size_t lds = (size_t)ws.epad * 20 + 16 + (size_t)kThreads * 8 + (size_t)kHalf * ws.epad * 4;
     if (nblk <= kDirect) {
         hipLaunchKernelGGL(k_route_place<false>, dim3(nblk + 1), dim3(kThreads), lds, st, p, ws, nblk);
         return hipGetLastError();
