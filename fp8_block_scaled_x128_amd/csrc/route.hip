@@ -133,8 +133,8 @@ __device__ __forceinline__ float2 select_tokens(const RouteArgs& p, int64_t t0, 
 #pragma unroll
         for (int i = 0; i < V; ++i) {
             const float v = __builtin_amdgcn_exp2f((z[i] - m) * kLog2e);
-            z[i] = left[i] ? z[i] : -INFINITY;
-            sum += left[i] ? v : 0.0f;
+            z[i] = left[i] ? v : 0.0f;              // from here on exp(z - m)
+            sum += z[i];
         }
         sum = lanes_sum<L>(sum);
         uint32_t ksel[2] = {0, 0}, esel[2] = {0, 0};
@@ -178,14 +178,9 @@ __device__ __forceinline__ float2 select_tokens(const RouteArgs& p, int64_t t0, 
             if (l == 0) p.lse[t] = lse;
         }
         if (live) {
-            // exp again, from an m the compiler cannot match with the first
-            // time: V values held through the rounds cost more
             const float inv = 1.0f / sum;
-            float m2 = m;
-            asm volatile("" : "+v"(m2));
 #pragma unroll
-            for (int i = 0; i < V; ++i)
-                acc[i] = __builtin_fmaf(__builtin_amdgcn_exp2f((z[i] - m2) * kLog2e), inv, acc[i]);
+            for (int i = 0; i < V; ++i) acc[i] = __builtin_fmaf(z[i], inv, acc[i]);
             if (l == 0) {
                 sums[0] = __builtin_fmaf(lse, lse, sums[0]);
                 sums[1] += 1.0f;
