@@ -11,10 +11,10 @@
 //   z loss    mean_t lse_t^2
 //
 // 10.6 MB move for 16384 tokens of 128 experts, 2 us at the rate of a copy; what
-// bounds the routing is the selection's rounds (850 vector instructions a
-// wave, 6 us of issue) and the latency of two dependent launches.  Measured,
-// top-8: 16384 tokens 9.6 us (selection) and 9.1 (placement); 32 tokens 6.0 in
-// one launch; 262144 tokens 137 in three.  The gradient at 16384 tokens 7.2.
+// bounds the routing is the selection's rounds (820 vector instructions a
+// wave, 5.5 us of issue) and the latency of two dependent launches.  Measured,
+// top-8: 16384 tokens 9.4 us (selection) and 7.8 (placement); 32 tokens 5.8 in
+// one launch; 262144 tokens 131 in three.  The gradient at 16384 tokens 7.1.
 // A third launch that scanned the histograms made it 30.7 us, logits loaded one
 // after the other 26, placement sums by LDS shuffles 21.
 #include "device_common.h"
@@ -579,8 +579,8 @@ __global__ void __launch_bounds__(256) k_route_bwd(RouteBwdArgs p) {
 
 // Lanes and values per token by the number of experts.  Sixteen lanes of many
 // values beat a wave of few in the selection, whose rounds then serve four
-// tokens at once (16384 tokens of 512 experts: 39.5 against 43.8 us); the
-// gradient has no rounds and more to hold (26.4 against 16.3 us).
+// tokens at once (16384 tokens of 512 experts: 35.1 against 41.4 us); the
+// gradient has no rounds and more to hold (26.9 against 16.3 us).
 template <template <int, int> class F, typename... A>
 hipError_t by_experts(int E, A&&... a) {
     if (E <= 16) return F<16, 1>::run(a...);
