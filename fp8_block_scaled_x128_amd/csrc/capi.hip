@@ -712,6 +712,8 @@ fp8bs_status fp8_block_norm_backward_ws_size(int64_t rows, int64_t cols, int64_t
     if (v != FP8BS_OK) return v;
     if (dgate && rows_per_gate < 1) return fail(FP8BS_ERR_SHAPE, "rows_per_gate must be >= 1");
     if (!bytes) return fail(FP8BS_ERR_NULL, "bytes is required");
+    *bytes = 0;
+    if (cols == 0) return ok();                     // nothing to sum, and no row layout to plan
     const int64_t R = rows_per_gate < rows ? rows_per_gate : (rows > 0 ? rows : 1);
     *bytes = plan_block_norm_bwd(rows, cols, R, dw_pre != 0, dw_post != 0, dgate != 0).ws_floats * 4;
     return ok();
