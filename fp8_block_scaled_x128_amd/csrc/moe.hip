@@ -188,9 +188,19 @@ hipError_t launch_moe_combine_bwd(const void* dout, int64_t ld_do, int do_f32, c
     const auto k_fn =
         do_f32 ? (wpt == 4 ? k_moe_combine_bwd<true, 4> : wpt == 2 ? k_moe_combine_bwd<true, 2> : k_moe_combine_bwd<true, 1>)
                : (wpt == 4 ? k_moe_combine_bwd<false, 4> : wpt == 2 ? k_moe_combine_bwd<false, 2> : k_moe_combine_bwd<false, 1>);
-    hipLaunchKernelGGL(k_fn, dim3((unsigned)((T + per - 1) / per)), dim3(kThreads), 0, st, dout, ld_do, y, (int32_t)rows, (int32_t)(H / 8), ld_y, pos,
-                       w, T, k, dy, ld_dy, dw);
-    return hipGetLastError();
+    // a launch holds fewer than 2^32 threads, with a workgroup per token 2^24
+    // tokens: more go in several
+    constexpr int64_t kMost = 1ll << 23;
+    for (int64_t t = 0; t < T; t += kMost) {
+        const int64_t n = T - t < kMost ? T - t : kMost;
+        const void* d = static_cast<const char*>(dout) + t * ld_do * (do_f32 ? 4 : 2);
+        hipLaunchKernelGGL(k_fn, dim3((unsigned)((n + per - 1) / per)), dim3(kThreads), 0, st, d, ld_do, y,
+                           (int32_t)rows, (int32_t)(H / 8), ld_y, pos + t * k, w + t * k, n, k, dy, ld_dy,
+                           dw ? dw + t * k : nullptr);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess) return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace fp8bs

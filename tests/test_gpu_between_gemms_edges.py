@@ -17,3 +17,35 @@ def test_no_columns():
     assert o.h.shape == (4, 0) and o.y.shape == (4, 0) and o.q.shape == (4, 0) and o.s.shape == (4, 0)
     g = ops.block_norm_backward(e(4, 0), e(4, 0), o.h, e(4, 0), w_pre=w, w_post=w, gate=e(2, 0), rows_per_gate=2)
     assert g.dres.shape == (4, 0) and g.dgate.shape == (2, 0) and g.dw_pre.shape == (0,) and g.ws is None
+
+
+# wide rows have four waves a token, narrower ones two and one: a workgroup of
+# 256 threads per token, per two and per four
+@pytest.mark.parametrize("T,H,k", [(1 << 24, 1544, 4), (1 << 25, 520, 4), ((1 << 26) - 1, 8, 1)])
+def test_combine_gradient_of_many_tokens(T, H, k):
+    """Up to the documented number of tokens (more threads than one launch
+    holds).  Only some tokens have rows; dout of the others is as allocated."""
+    toks = [0, 5, (1 << 23) - 1, 1 << 23, (1 << 23) + 1, T - 2, T - 1]
+    n = len(toks)
+    g = torch.Generator().manual_seed(H)
+    dout = torch.empty(T, H, dtype=BF, device="cuda")
+    pos = torch.full((T, k), -1, dtype=torch.int32, device="cuda")
+    w = torch.zeros(T, k, device="cuda")
+    vals, wv = torch.randn(n, H, generator=g).to(BF), torch.randn(n, k, generator=g)
+    y = torch.randn(n * k, H, generator=g).to(BF)
+    at = torch.tensor(toks, device="cuda")
+    dout[at], w[at] = vals.cuda(), wv.cuda()
+    pos[at] = torch.arange(n * k, dtype=torch.int32).view(n, k).cuda()
+    dy, dw = ops.moe_combine_backward(dout, y.cuda(), pos, w)
+    u = torch.finfo(F32).eps / 2
+    # a dot product: H / 64 terms per lane, the lanes' six steps, four waves
+    terms = vals.double()[:, None, :] * y.double().view(n, k, H)
+    err = (dw[at].cpu().double() - terms.sum(2)).abs()
+    assert (err <= (H / 64 + 16) * u * terms.abs().sum(2)).all()
+    want = wv.double()[:, :, None] * vals.double()[:, None, :]
+    got = dy.cpu().double().view(n, k, H)
+    assert ((got - want).abs() <= (torch.finfo(BF).eps / 2 + u) * want.abs() + 1e-38).all()
+    dw[at] = 0
+    assert int(torch.count_nonzero(dw)) == 0
+    del dout, pos, w, dw
+    torch.cuda.empty_cache()
