@@ -540,6 +540,16 @@ def _moe_experts(qx, sx, T, qgu, sgu, qdt, sdt, offsets, row_token):
     I = N2 // 2
     rows = row_token.numel()
     dev = qx.device
+    # the products walk the experts by these sizes: anything else would be read past its end
+    for name, t, shape in (("qgu", qgu, (G, 2 * I, qx.shape[1])), ("qdt", qdt, (G, H, I))):
+        if t.shape != shape or t.element_size() != 1 or not t.is_contiguous() or t.device != dev:
+            raise ValueError("%s: contiguous codes %s on %s expected, got %s %s, strides %s, on %s"
+                             % (name, list(shape), dev, t.dtype, tuple(t.shape), t.stride(), t.device))
+    ng = lambda n: (n + 127) // 128
+    for name, t, shape in (("sgu", sgu, (G, ng(N2), ng(H))), ("sdt", sdt, (G, ng(I), ng(H)))):
+        if t.shape != shape or t.dtype is not torch.float32 or t.device != dev:
+            raise ValueError("%s: float32 %s on %s expected, got %s %s on %s"
+                             % (name, list(shape), dev, t.dtype, tuple(t.shape), t.device))
     qh = _u8((rows, I), dev)
     shb = torch.empty((I // 128, rows), dtype=torch.float32, device=dev)
     fp8_grouped_gemm_swiglu_quant(rows, I, H, G, offsets, row_token, T, qx, qx.stride(0) if T > 1 else H, sx,

@@ -49,3 +49,47 @@ def test_combine_gradient_of_many_tokens(T, H, k):
     assert int(torch.count_nonzero(dw)) == 0
     del dout, pos, w, dw
     torch.cuda.empty_cache()
+
+
+def _small_layer(T=64, H=256, G=4, I=128):
+    g = torch.Generator().manual_seed(5)
+    bf = lambda *s: (0.1 * torch.randn(*s, generator=g)).to(BF).cuda()
+    x = bf(T, H)
+    qgu, sgu, _ = ops.quant_block2d(bf(G, 2 * I, H))
+    wd = bf(G, I, H)
+    qdt = torch.empty(G, H, I, dtype=torch.uint8, device="cuda")
+    sdt = torch.empty(G, I // 128, H // 128, device="cuda")
+    ops.fp8_quant_block2d(wd, G, I, H, H, None, 0, qdt, I, sdt)
+    return x, [qgu, sgu, qdt, sdt], torch.randn(T, G, generator=g).cuda()
+
+
+def test_expert_weights_that_do_not_fit_are_refused():
+    """Shape, type, layout and device of the experts' codes and scales: a
+    refusal before the products (they walk the experts by the sizes of qgu
+    alone)."""
+    x, w, z = _small_layer()
+    codes = ops.quant_rowblock(x)
+    ops.moe_forward_routed(codes, z, 2, *w)
+    r = ops.moe_route(z, 2)
+    qgu, sgu, qdt, sdt = w
+    bad = [(0, qgu[:, :, ::2].expand(4, 256, 128)), (0, qgu.transpose(1, 2)), (0, qgu.float()), (0, qgu.cpu()),
+           (0, qgu[:, :192].contiguous()), (1, sgu[:3]), (1, sgu[:, :1]), (1, sgu.double()), (1, sgu.cpu()),
+           (1, sgu.reshape(4, 4)), (2, qdt[:3]), (2, qdt.transpose(1, 2).contiguous().transpose(1, 2)),
+           (2, qdt.to(torch.int16)), (2, qdt.cpu()), (3, sdt[:, :, :1]), (3, sdt[0]), (3, sdt.half()), (3, sdt.cpu())]
+    for i, t in bad:
+        v = list(w)
+        v[i] = t
+        with pytest.raises(ValueError):
+            ops.moe_forward_routed(codes, z, 2, *v)
+        with pytest.raises(ValueError):
+            ops.moe_forward(x, *v, r.offsets, r.row_token, r.token_rows, r.weights)
+
+
+def test_scales_with_strides_of_their_own():
+    """The scales' strides are used: a transposed buffer gives the same bytes."""
+    x, w, z = _small_layer()
+    codes = ops.quant_rowblock(x)
+    a, _, _ = ops.moe_forward_routed(codes, z, 2, *w)
+    v = [w[0], w[1].transpose(1, 2).contiguous().transpose(1, 2), w[2], w[3].transpose(0, 2).contiguous().transpose(0, 2)]
+    b, _, _ = ops.moe_forward_routed((codes[0], codes[1].contiguous()), z, 2, *v)
+    assert torch.equal(a, b)
