@@ -126,7 +126,10 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
                 ss[0] += sumsq8(v);
             }
             row_sums<LPR>(ss, wpr, lds, turn);
-            r = inv_sqrt(__builtin_fmaf(ss[0], inv_n, p.eps));
+#pragma unroll
+            for (int i = 0; i < NV; ++i) in.x[i].forget();
+            row_means<LPR, NV>(ss, [&](int, int i, float v[8]) { in.x[i].get(v); }, inv_n, p.eps, wpr, lds, turn);
+            r = inv_sqrt(ss[0]);
         }
         float h[NV][8];
         float ss[1] = {0.0f};
@@ -153,7 +156,12 @@ __global__ void __launch_bounds__(512) k_block_norm(NormArgs p, int wpr) {
         // y from the unrounded h: the bf16 rounding of the stored stream does
         // not enter y, its scales or its codes
         row_sums<LPR>(ss, wpr, lds, turn);
-        r = inv_sqrt(__builtin_fmaf(ss[0], inv_n, p.eps));
+        const auto h_at = [&](int, int i, float v[8]) {
+#pragma unroll
+            for (int e = 0; e < 8; ++e) v[e] = h[i][e];
+        };
+        row_means<LPR, NV>(ss, h_at, inv_n, p.eps, wpr, lds, turn);
+        r = inv_sqrt(ss[0]);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
             const int c = tid + i * step;

@@ -103,6 +103,17 @@ struct Weights {
 // gradient summed over the rows of a gate row.
 enum { kGateNone, kGateRow, kGateSum };
 
+// Waves per SIMD that the registers have to leave room for: what the plan below
+// counts on per compute unit.  Rows of one wave: three workgroups of four waves
+// with gate sums, two of eight without a gate.  Rows of several with one chunk
+// per lane and no gate: ten waves in two workgroups of five, which three waves
+// per SIMD do not hold (4096x2560, all fp32: 48.4 us, 54.2 with three).
+constexpr int min_waves(int nv, int lpr, bool res32, bool dy32, int gate) {
+    if (lpr == kMulti) return nv == 1 && gate == kGateNone ? 4 : 2;
+    if (lpr == 64 && gate == kGateSum) return 3;
+    return gate == kGateNone && !res32 && !(dy32 && lpr < 64) ? 4 : 2;
+}
+
 // One row as loaded.
 template <int NV, bool RES32, bool DY32, int GATE>
 struct RowIn {
@@ -169,7 +180,8 @@ struct RowIn {
 // apart from lane to lane: no bank conflicts).  Four chunks per lane (more than
 // 12288 columns) still spill: 2048x16384 runs at 2.6 TB/s.
 template <int NV, bool RES32, bool DY32, int LPR, int GATE>
-__global__ void __launch_bounds__(64 * (LPR == kMulti ? kMaxRowWaves : row_waves(GATE == kGateSum))) k_block_norm_bwd(NormBwdArgs p, NormBwdPlan pl) {
+__global__ void __launch_bounds__(64 * (LPR == kMulti ? kMaxRowWaves : row_waves(GATE == kGateSum)),
+                                  min_waves(NV, LPR, RES32, DY32, GATE)) k_block_norm_bwd(NormBwdArgs p, NormBwdPlan pl) {
     constexpr bool MULTI = LPR == kMulti, SHARED = LPR == 16 || LPR == 32;     // SHARED: a wave has several rows
     constexpr bool GACC = GATE == kGateSum;
     constexpr int WAVES = row_waves(GACC);          // of a workgroup whose rows need one wave each
@@ -277,13 +289,19 @@ __global__ void __launch_bounds__(64 * (LPR == kMulti ? kMaxRowWaves : row_waves
                 sums[2] += sumsq8(x);
             }
             row_sums<LPR>(sums, wpr, lds, turn);
+            float means[2] = {sums[0], sums[2]};
+            const auto value = [&](int k, int i, float v[8]) {
+                if (k == 0) { auto t = in.h[i]; t.forget(); t.get(v); }
+                else { auto t = in.x[i]; t.forget(); t.get(v); }
+            };
+            row_means<LPR, NV>(means, value, inv_n, p.eps, wpr, lds, turn);
 #pragma unroll
             for (int i = 0; i < NV; ++i) { in.h[i].forget(); in.dy[i].forget(); in.x[i].forget(); }
             float dh[NV][8];
 #pragma unroll
             for (int i = 0; i < NV; ++i) in.dh[i].get(dh[i]);
             if (p.w_pre) {
-                const float r = inv_sqrt(__builtin_fmaf(sums[0], inv_n, p.eps));
+                const float r = inv_sqrt(means[0]);
                 const float m = sums[1] * inv_n * r * r;        // mean(g hh) r: times h, hh mean(g hh)
 #pragma unroll
                 for (int i = 0; i < NV; ++i) {
@@ -308,7 +326,7 @@ __global__ void __launch_bounds__(64 * (LPR == kMulti ? kMaxRowWaves : row_waves
                 }
             }
             if (!p.x) continue;
-            const float rx = p.w_post ? inv_sqrt(__builtin_fmaf(sums[2], inv_n, p.eps)) : 1.0f;
+            const float rx = p.w_post ? inv_sqrt(means[1]) : 1.0f;
             float dot[1] = {0.0f};
 #pragma unroll
             for (int i = 0; i < NV; ++i) {
@@ -349,6 +367,14 @@ __global__ void __launch_bounds__(64 * (LPR == kMulti ? kMaxRowWaves : row_waves
 #pragma unroll
                 for (int i = 0; i < NV; ++i) in.x[i].forget();
                 m = dot[0] * inv_n * rx * rx;           // mean(g xh) r': times x
+                // of rows with very large values the square of the factor would
+                // underflow: a power of two goes from x to it
+                if (__builtin_expect(__builtin_amdgcn_ballot_w64(rx < 0x1p-32f) != 0, 0)) {
+                    const bool large = rx < 0x1p-32f;
+                    m = dot[0] * inv_n * rx * (large ? rx * 0x1p64f : rx);
+#pragma unroll
+                    for (int i = 0; i < NV; ++i) in.x[i].scale(large ? 0x1p-64f : 1.0f);
+                }
             }
 #pragma unroll
             for (int i = 0; i < NV; ++i) {

@@ -45,6 +45,12 @@ struct Raw8 {
         r[0] = make_uint4(0, 0, 0, 0);
         r[F32 ? 1 : 0] = make_uint4(0, 0, 0, 0);
     }
+    __device__ __forceinline__ void scale(float c) {         // bf16 values by a power of two
+        float v[8];
+        unpack8(r[0], v);
+        r[0] = make_uint4(pack_bf16x2(v[0] * c, v[1] * c), pack_bf16x2(v[2] * c, v[3] * c),
+                          pack_bf16x2(v[4] * c, v[5] * c), pack_bf16x2(v[6] * c, v[7] * c));
+    }
     __device__ __forceinline__ void get(float v[8]) const {
         if (F32) {
             const uint4 a = r[0], b = r[F32 ? 1 : 0];
@@ -135,6 +141,42 @@ __device__ __forceinline__ void row_sums(float (&v)[K], int wpr, float (*lds)[kM
 #pragma unroll
         for (int i = 0; i < K; ++i) v[i] += buf[w][i];
     }
+}
+
+// Mean square + eps of K vectors of a row from their sums of squares.  Where a
+// mean square is past 2^128 / cols the sum overflows: such a row is summed again
+// from its values (`get(k, i, v)`: chunk i of vector k) at kDown each, kDown^2
+// being the inverse of the largest number of columns.  All lanes that share the
+// row have the same sums; a wave with several rows goes that way together, and
+// only the sums that need it are replaced.
+constexpr float kDown = 0x1p-7f;
+template <int LPR, int NV, int K, typename Get>
+__device__ __forceinline__ void row_means(float (&sum)[K], const Get& get, float inv_n, float eps, int wpr,
+                                          float (*lds)[kMaxRowWaves][4], int& turn) {
+    bool over[K], any = false;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        over[k] = !(sum[k] <= 3.4028235e38f);               // an infinity or a NaN too: the same sum again
+        any |= over[k];
+        sum[k] = __builtin_fmaf(sum[k], inv_n, eps);
+    }
+    if (__builtin_expect(__builtin_amdgcn_ballot_w64(any) == 0, 1)) return;
+    float s[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+        s[k] = 0.0f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            float v[8];
+            get(k, i, v);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) s[k] = __builtin_fmaf(v[e] * kDown, v[e] * kDown, s[k]);
+        }
+    }
+    row_sums<LPR>(s, wpr, lds, turn);
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+        if (over[k]) sum[k] = __builtin_fmaf(s[k], inv_n / (kDown * kDown), eps);
 }
 
 // Waves per row and chunks per lane: one chunk per lane while eight waves hold

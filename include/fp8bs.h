@@ -607,7 +607,9 @@ fp8bs_status fp8_moe_route_backward(const void* logits, int64_t T, int32_t E, in
  * value) and scale finite;
  * leading dimensions >= cols and % 8 == 0; bf16, fp32 and weight pointers
  * 16-byte aligned, q 8-byte, s 4-byte.  Inputs are expected to be finite with
- * mean squares in fp32's range.
+ * mean squares in fp32's range (a row's sum of squares may be past it).  An
+ * infinity or a NaN stays in its row: it shows in that row's h and y, and the
+ * row's codes and scales are unspecified, as the quantizers' are.
  * ------------------------------------------------------------------------ */
 fp8bs_status fp8_block_norm(int64_t rows, int64_t cols, const uint16_t* x, int64_t ld_x,
                             const void* residual, int64_t ld_r, fp8bs_out stream_type,
@@ -645,7 +647,8 @@ fp8bs_status fp8_block_norm(int64_t rows, int64_t cols, const uint16_t* x, int64
  *         Calls that overlap in time need separate workspaces.
  * The sums have a fixed order: the results are the same bits every time.
  * Requirements: as fp8_block_norm; dy or dh; at least one output; each of
- * dgate, dw_post, dw_pre only with its gate or weight.
+ * dgate, dw_post, dw_pre only with its gate or weight.  The sums over a row of
+ * dy w_pre h and of dn w_post xh, too, are expected to be in fp32's range.
  * ------------------------------------------------------------------------ */
 fp8bs_status fp8_block_norm_backward(int64_t rows, int64_t cols, const void* dy, int64_t ld_dy, fp8bs_out dy_type,
                                      const void* dh, int64_t ld_dh, const void* h, int64_t ld_h,
