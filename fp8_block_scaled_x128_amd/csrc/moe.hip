@@ -6,9 +6,14 @@
 //
 // HBM-bound: k bf16 rows read per token, one row written.  One thread owns
 // one (token, 8-column chunk) pair: the k rows of a token are each read as
-// one contiguous run across the workgroup (16-byte loads), all k loads are
-// issued before the FMAs, and the sum is an fp32 FMA chain in slot order
-// (deterministic: no atomics, no order that depends on scheduling).
+// one contiguous run across the workgroup (16-byte loads), up to eight rows are
+// loaded before the FMAs, and the sum is an fp32 FMA chain in slot order
+// (deterministic: no atomics, no order that depends on scheduling).  A slot's
+// position is waited for before its row is loaded, and loads return in order,
+// so one thread's slots are up to eight round trips; other waves fill them at
+// 16384 tokens, nothing does in decode.  Measured, 2048 columns, top-8: 16384
+// tokens 605 MB in 107 us (5.6 TB/s, the rate of a large copy), 512 tokens 7.1
+// us, 32 tokens 3.6, one 2.8; on the router's maps (SKIP) 107.6, 7.8, 4.1, 3.0.
 #include "device_common.h"
 #include "internal.h"
 #include "reduce.h"

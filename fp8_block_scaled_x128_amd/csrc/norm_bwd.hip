@@ -9,12 +9,12 @@
 //
 // HBM-bound.  A workgroup walks units of rows that share a gate row; its column
 // sums of dw_pre and dw_post stay in registers over all its rows and leave one
-// partial row each, which k_col_reduce adds in workgroup order (no atomics: the
-// same bits every time).
+// partial row each, which k_col_reduce adds in a fixed order (every 128th row,
+// then a tree; no atomics: the same bits every time).
 //
-// Measured: 4096x2560 with an fp32 dy, 147 MB, 30.8 us (4.8 TB/s) and 4.7 us
+// Measured: 4096x2560 with an fp32 dy, 147 MB, 31 us (4.7 TB/s) and 4.5 us
 // for the column sums; 16384x2048 over an fp32 stream with the gradient of a
-// gate per sequence, 604 MB, 127.7 us (4.7 TB/s) and 5.3 us; 131072x128 40 us
+// gate per sequence, 604 MB, 127.5 us (4.7 TB/s) and 5.3 us; 131072x128 40 us
 // in all.  Without the next row in flight and with conversions between the
 // loads the first two ran 65 and 143 us.
 #include "norm_common.h"
@@ -174,11 +174,13 @@ struct RowIn {
 // behind the next row's loads would wait for them: up to two chunks per lane
 // the weights stay in registers (KEEP), above that each row's are loaded ahead
 // of the next row's data.
-// Column sums are in registers too up to two chunks per lane; above that the
-// registers would spill (2048x10240: 99 us, 71 now), and each lane keeps its
-// columns' sums in LDS, 8 bytes a column and weight (halves of a chunk 16 bytes
-// apart from lane to lane: no bank conflicts).  Four chunks per lane (more than
-// 12288 columns) still spill: 2048x16384 runs at 2.6 TB/s.
+// Column sums are in registers too up to two chunks per lane; above that (2048x
+// 10240 with register sums: 99 us, 71 with both launches now) each lane keeps
+// its columns' sums in LDS, 8 bytes a column and weight (halves of a chunk 16
+// bytes apart from lane to lane: no bank conflicts).  Rows of more than 8192
+// columns spill all the same, since a row's packed weights live from before its
+// loads to its end: with three chunks per lane 5 (all bf16, no gate) to 115
+// registers, with four 77 to 273 (2032x16384: 3.0 TB/s, 2048x10240 3.9).
 template <int NV, bool RES32, bool DY32, int LPR, int GATE>
 __global__ void __launch_bounds__(64 * (LPR == kMulti ? kMaxRowWaves : row_waves(GATE == kGateSum)),
                                   min_waves(NV, LPR, RES32, DY32, GATE)) k_block_norm_bwd(NormBwdArgs p, NormBwdPlan pl) {

@@ -12,9 +12,14 @@
 //
 // 10.6 MB move for 16384 tokens of 128 experts, 2 us at the rate of a copy; what
 // bounds the routing is the selection's rounds (820 vector instructions a
-// wave, 5.5 us of issue) and the latency of two dependent launches.  Measured,
-// top-8: 16384 tokens 9.4 us (selection) and 7.8 (placement); 32 tokens 5.8 in
-// one launch; 262144 tokens 131 in three.  The gradient at 16384 tokens 7.1.
+// wave, 5.5 us of issue) and the latency of two dependent launches, in the
+// second of which each workgroup goes through 113 scalar branches (the steps of
+// lanes_sum_mod on the number of experts) before its first barrier.  With more
+// experts a round scans as many more values per lane, and the histograms that
+// every placing workgroup adds grow with experts times tokens squared.
+// Measured, top-8: 16384 tokens 9.4 us (selection) and 7.9 (placement), of 512
+// experts 21.5 and 14; 32768 of 512 38.7 and 21.4; 32 tokens 5.8 in one launch;
+// 262144 tokens 133 in three (72.6, 4.7, 55.4).  The gradient at 16384 tokens 7.1.
 // A third launch that scanned the histograms made it 30.7 us, logits loaded one
 // after the other 26, placement sums by LDS shuffles 21.
 #include "device_common.h"
