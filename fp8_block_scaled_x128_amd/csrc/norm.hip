@@ -11,9 +11,9 @@
 // registers.
 //
 // Measured (a 1 GiB device copy moves 5.2 TB/s on the same card): 4096x2560
-// bf16 with every output, 95 MB, 20.5 us (4.6 TB/s); 16384x2048 over an fp32
+// bf16 with every output, 95 MB, 21 us (4.5 TB/s); 16384x2048 over an fp32
 // stream with a gate per sequence, 437 MB, 91 us (4.8); 131072x128 29.9 us
-// (5.1); one row of 2560 3.5 us, all latency: three dependent trips to memory
+// (5.1); one row of 2560 3.6 us, all latency: three dependent trips to memory
 // (w_pre, w_post, then the row: a bf16 weight is converted, so waited for,
 // before the next load) and two reductions.  Wide rows: 2048x10240 44.8 us
 // (4.2 TB/s), 2032x16384 72 (4.2).  A row per workgroup without the next row in
