@@ -950,6 +950,168 @@ fp8bs_status mxfp8_grouped_gemm_swiglu_quant(int64_t total_rows, int64_t I, int6
                     "mxfp8_grouped_gemm_swiglu_quant");
 }
 
+// Codes of int8_quant and int8_silu_mul_quant: `len` of them per output row.
+static fp8bs_status i8_codes_args(int64_t len, const int8_t* q, int64_t ld_q, const float* s) {
+    if (!s || (len > 0 && !q)) return fail(FP8BS_ERR_NULL, "q and s are required");
+    if (ld_q < (len + 15) / 16 * 16) return fail(FP8BS_ERR_STRIDE, "ld_q must be >= the row of codes padded to 16");
+    if (len > 0 && (ld_q % 16 || !aligned(q, 16))) return fail(FP8BS_ERR_ALIGN, "q must be 16-byte aligned with ld_q %% 16 == 0");
+    if (!aligned(s, 4)) return fail(FP8BS_ERR_ALIGN, "s must be 4-byte aligned");
+    return FP8BS_OK;
+}
+
+fp8bs_status int8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, fp8bs_axis axis, int8_t* q,
+                        int64_t ld_q, float* s, hipStream_t stream) {
+    if (axis != FP8BS_AXIS_ROW && axis != FP8BS_AXIS_COL) return fail(FP8BS_ERR_UNSUPPORTED, "axis %d", (int)axis);
+    if (rows < 0 || cols < 0) return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
+    if (cols % 8) return fail(FP8BS_ERR_SHAPE, "cols %% 8 != 0 (cols=%lld)", (long long)cols);
+    if (rows > INT32_MAX / 2 || cols > INT32_MAX / 2 || (axis == FP8BS_AXIS_COL && rows > 65535ll * 128))
+        return fail(FP8BS_ERR_SHAPE, "tensor too large");
+    const bool by_row = axis == FP8BS_AXIS_ROW;
+    if ((by_row ? rows : cols) == 0) return ok();
+    if (rows > 0 && cols > 0) {
+        if (!x) return fail(FP8BS_ERR_NULL, "x is required");
+        if (ld_x < cols) return fail(FP8BS_ERR_STRIDE, "ld_x must be >= cols");
+        if (ld_x % 8 || !aligned(x, 16)) return fail(FP8BS_ERR_ALIGN, "x must be 16-byte aligned with ld_x %% 8 == 0");
+    }
+    fp8bs_status v = i8_codes_args(by_row ? cols : rows, q, ld_q, s);
+    if (v != FP8BS_OK) return v;
+    fp8bs_status d = check_device();
+    if (d != FP8BS_OK) return d;
+    uint8_t* qu = reinterpret_cast<uint8_t*>(q);
+    return launched(by_row ? launch_i8_quant_rows(x, rows, cols, ld_x, qu, ld_q, s, stream)
+                           : launch_i8_quant_cols(x, rows, cols, ld_x, qu, ld_q, s, stream),
+                    "int8_quant");
+}
+
+fp8bs_status int8_silu_mul_quant(const uint16_t* gate_up, int64_t rows, int64_t I, int64_t ld_in,
+                                 const int32_t* live_rows, int8_t* q, int64_t ld_q, float* s, uint16_t* h_out,
+                                 int64_t ld_h, hipStream_t stream) {
+    if (rows < 0 || I < 0) return fail(FP8BS_ERR_SHAPE, "rows=%lld I=%lld", (long long)rows, (long long)I);
+    if (I % 8) return fail(FP8BS_ERR_SHAPE, "I %% 8 != 0 (I=%lld)", (long long)I);
+    if (rows > INT32_MAX / 2 || I > INT32_MAX / 4) return fail(FP8BS_ERR_SHAPE, "tensor too large");
+    if (rows == 0) return ok();
+    if (I > 0) {
+        if (!gate_up) return fail(FP8BS_ERR_NULL, "gate_up is required");
+        if (ld_in < 2 * I || (h_out && ld_h < I)) return fail(FP8BS_ERR_STRIDE, "ld_in must be >= 2 I and ld_h >= I");
+        if (ld_in % 8 || !aligned(gate_up, 16) || (h_out && (ld_h % 8 || !aligned(h_out, 16))))
+            return fail(FP8BS_ERR_ALIGN, "gate_up and h_out must be 16-byte aligned with leading dimensions %% 8 == 0");
+    }
+    if (!aligned(live_rows, 4)) return fail(FP8BS_ERR_ALIGN, "live_rows must be 4-byte aligned");
+    fp8bs_status v = i8_codes_args(I, q, ld_q, s);
+    if (v != FP8BS_OK) return v;
+    fp8bs_status d = check_device();
+    if (d != FP8BS_OK) return d;
+    return launched(launch_i8_silu_mul_quant(gate_up, rows, I, ld_in, live_rows, reinterpret_cast<uint8_t*>(q), ld_q, s,
+                                             h_out, ld_h, stream),
+                    "int8_silu_mul_quant");
+}
+
+// Sizes, weights and output of an integer product (M rows of A in all).
+static fp8bs_status i8_product_args(int64_t M, int64_t N, int64_t K, const int8_t* b, int64_t ldb, const float* sb,
+                                    const void* c, int64_t ldc, fp8bs_out out) {
+    if (M < 0 || N < 0 || K < 0) return fail(FP8BS_ERR_SHAPE, "negative size");
+    if (K % 16) return fail(FP8BS_ERR_SHAPE, "K %% 16 != 0 (K=%lld)", (long long)K);
+    if (K > 131056) return fail(FP8BS_ERR_SHAPE, "K=%lld > 131056: the sum could leave 32 bits", (long long)K);
+    if (N % 8) return fail(FP8BS_ERR_SHAPE, "N %% 8 != 0 (N=%lld)", (long long)N);
+    if (M > INT32_MAX / 2 || N > INT32_MAX / 2) return fail(FP8BS_ERR_SHAPE, "size too large");
+    if (out != FP8BS_OUT_BF16 && out != FP8BS_OUT_FP32) return fail(FP8BS_ERR_UNSUPPORTED, "out %d", (int)out);
+    if (M == 0 || N == 0) return FP8BS_OK;
+    if (!c || !sb || (K > 0 && !b)) return fail(FP8BS_ERR_NULL, "b, sb and c are required");
+    if (ldb < K || ldc < N) return fail(FP8BS_ERR_STRIDE, "ldb must be >= K and ldc >= N");
+    if (K > 0 && (ldb % 16 || !aligned(b, 16))) return fail(FP8BS_ERR_ALIGN, "b must be 16-byte aligned with ldb %% 16 == 0");
+    if (ldc % 8 || !aligned(c, 16)) return fail(FP8BS_ERR_ALIGN, "c must be 16-byte aligned with ldc %% 8 == 0");
+    if (!aligned(sb, 4)) return fail(FP8BS_ERR_ALIGN, "scales must be 4-byte aligned");
+    if ((uint64_t)N * (uint64_t)ldb >= (1ull << 32)) return fail(FP8BS_ERR_SHAPE, "an operand exceeds 4 GiB");
+    // tiles of at least 64 x 64 are counted in int32
+    if (((M + 63) / 64) * ((N + 63) / 64) >= (1ll << 31) - 8) return fail(FP8BS_ERR_SHAPE, "too many tiles");
+    return FP8BS_OK;
+}
+
+// Codes of A (`arows` of them) and their scales.
+static fp8bs_status i8_operand_args(int64_t arows, int64_t K, const int8_t* a, int64_t lda, const float* sa) {
+    if (!sa || (K > 0 && !a)) return fail(FP8BS_ERR_NULL, "a and sa are required");
+    if (lda < K) return fail(FP8BS_ERR_STRIDE, "lda must be >= K");
+    if (K > 0 && (lda % 16 || !aligned(a, 16))) return fail(FP8BS_ERR_ALIGN, "a must be 16-byte aligned with lda %% 16 == 0");
+    if (!aligned(sa, 4)) return fail(FP8BS_ERR_ALIGN, "scales must be 4-byte aligned");
+    if ((uint64_t)arows * (uint64_t)lda >= (1ull << 32)) return fail(FP8BS_ERR_SHAPE, "an operand exceeds 4 GiB");
+    return FP8BS_OK;
+}
+
+fp8bs_status int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* sa, const int8_t* b,
+                       int64_t ldb, const float* sb, void* c, int64_t ldc, fp8bs_out out, hipStream_t stream) {
+    fp8bs_status v = i8_product_args(M, N, K, b, ldb, sb, c, ldc, out);
+    if (v != FP8BS_OK) return v;
+    if (M == 0 || N == 0) return ok();
+    if ((v = i8_operand_args(M, K, a, lda, sa)) != FP8BS_OK) return v;
+    if ((v = check_device()) != FP8BS_OK) return v;
+    const I8GemmArgs g{M, N, K, reinterpret_cast<const uint8_t*>(a), lda, sa, reinterpret_cast<const uint8_t*>(b), ldb,
+                       0, sb, 0, c, ldc, out == FP8BS_OUT_FP32, 0, nullptr, nullptr};
+    return launched(launch_i8_gemm(g, stream), "int8_gemm");
+}
+
+static size_t i8_linear_scales(int64_t rows) { return (size_t)(rows + 3) / 4 * 16; }
+
+fp8bs_status int8_linear_ws_size(int64_t rows, int64_t cols, size_t* bytes) {
+    if (!bytes) return fail(FP8BS_ERR_NULL, "bytes is required");
+    if (rows < 0 || cols < 0 || rows > INT32_MAX / 2 || cols > INT32_MAX / 2)
+        return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
+    *bytes = i8_linear_scales(rows) + (size_t)rows * (size_t)((cols + 15) / 16 * 16);
+    return ok();
+}
+
+fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* x, int64_t ld_x, const int8_t* w,
+                         int64_t ld_w, const float* sw, void* y, int64_t ld_y, fp8bs_out out, void* ws, size_t ws_bytes,
+                         hipStream_t stream) {
+    if (rows < 0 || cols < 0 || rows > INT32_MAX / 2 || cols > INT32_MAX / 2)
+        return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
+    if (cols % 8) return fail(FP8BS_ERR_SHAPE, "cols %% 8 != 0 (cols=%lld)", (long long)cols);
+    const int64_t K = (cols + 15) / 16 * 16;
+    fp8bs_status v = i8_product_args(rows, N, K, w, ld_w, sw, y, ld_y, out);
+    if (v != FP8BS_OK) return v;
+    if (rows == 0 || N == 0) return ok();
+    if (cols > 0) {
+        if (!x) return fail(FP8BS_ERR_NULL, "x is required");
+        if (ld_x < cols) return fail(FP8BS_ERR_STRIDE, "ld_x must be >= cols");
+        if (ld_x % 8 || !aligned(x, 16)) return fail(FP8BS_ERR_ALIGN, "x must be 16-byte aligned with ld_x %% 8 == 0");
+    }
+    size_t need = 0;
+    if ((v = int8_linear_ws_size(rows, cols, &need)) != FP8BS_OK) return v;
+    if (!ws) return fail(FP8BS_ERR_NULL, "a workspace of %zu bytes is required", need);
+    if (ws_bytes < need) return fail(FP8BS_ERR_SHAPE, "ws_bytes %zu < %zu", ws_bytes, need);
+    if (!aligned(ws, 16)) return fail(FP8BS_ERR_ALIGN, "ws must be 16-byte aligned");
+    float* sx = static_cast<float*>(ws);
+    uint8_t* qx = static_cast<uint8_t*>(ws) + i8_linear_scales(rows);
+    if ((v = i8_operand_args(rows, K, reinterpret_cast<const int8_t*>(qx), K, sx)) != FP8BS_OK) return v;
+    if ((v = check_device()) != FP8BS_OK) return v;
+    const hipError_t e = launch_i8_quant_rows(x, rows, cols, ld_x, qx, K, sx, stream);
+    if (e != hipSuccess) return launched(e, "int8_linear");
+    const I8GemmArgs g{rows, N, K, qx, K, sx, reinterpret_cast<const uint8_t*>(w), ld_w, 0, sw, 0, y, ld_y,
+                       out == FP8BS_OUT_FP32, 0, nullptr, nullptr};
+    return launched(launch_i8_gemm(g, stream), "int8_linear");
+}
+
+fp8bs_status int8_grouped_gemm(int64_t total_rows, int64_t N, int64_t K, int32_t G, const int32_t* offsets,
+                               const int32_t* a_rows, int64_t a_count, const int8_t* a, int64_t lda, const float* sa,
+                               const int8_t* b, int64_t ldb, int64_t b_stride_g, const float* sb, int64_t sb_stride_g,
+                               void* c, int64_t ldc, fp8bs_out out, hipStream_t stream) {
+    if (G < 1 || G > 65535) return fail(FP8BS_ERR_SHAPE, "G=%d outside [1, 65535]", (int)G);
+    fp8bs_status v = i8_product_args(total_rows, N, K, b, ldb, sb, c, ldc, out);
+    if (v != FP8BS_OK) return v;
+    if (total_rows == 0 || N == 0) return ok();
+    if (!offsets) return fail(FP8BS_ERR_NULL, "offsets is required");
+    if (!aligned(offsets, 4) || !aligned(a_rows, 4)) return fail(FP8BS_ERR_ALIGN, "offsets and a_rows must be 4-byte aligned");
+    if (b_stride_g < 0 || sb_stride_g < 0) return fail(FP8BS_ERR_STRIDE, "negative group stride");
+    if (b_stride_g % 16) return fail(FP8BS_ERR_ALIGN, "b_stride_g %% 16 != 0");
+    if (a_rows && (a_count < 1 || a_count > INT32_MAX)) return fail(FP8BS_ERR_SHAPE, "a_count must be >= 1 with a_rows");
+    if (((total_rows + 63) / 64 + G) * ((N + 63) / 64) >= (1ll << 31) - 8) return fail(FP8BS_ERR_SHAPE, "too many tiles");
+    if ((v = i8_operand_args(a_rows ? a_count : total_rows, K, a, lda, sa)) != FP8BS_OK) return v;
+    if ((v = check_device()) != FP8BS_OK) return v;
+    const I8GemmArgs g{total_rows, N, K, reinterpret_cast<const uint8_t*>(a), lda, sa,
+                       reinterpret_cast<const uint8_t*>(b), ldb, b_stride_g, sb, sb_stride_g, c, ldc,
+                       out == FP8BS_OUT_FP32, G, offsets, a_rows};
+    return launched(launch_i8_gemm(g, stream), "int8_grouped_gemm");
+}
+
 fp8bs_status fp8bs_e4m3_encode(const float* in, uint8_t* out, int64_t n, hipStream_t stream) {
     if (n < 0) return fail(FP8BS_ERR_SHAPE, "n < 0");
     if (n == 0) return ok();

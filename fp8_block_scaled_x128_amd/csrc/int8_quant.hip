@@ -1,0 +1,284 @@
+// Quantization to 8-bit integers with one scale per row (token) or per column
+// (channel), and SiLU*mul followed by the row form: the operands of int8_gemm.
+// Rowwise and columnwise are the granularities of scaled 8-bit products ("Towards
+// Full Pipeline FP8 Reinforcement Learning for LLMs" compares rowwise scaling with
+// the block-wise one for FP8 codes; here the codes are integers).
+//
+// Bound by HBM: 2 bytes read and 1 written per value, once for rows; columns
+// need their maximum over all rows before the first code, so a long tensor is read
+// twice (the second time mostly from the last-level cache).
+#include "int8_common.h"
+#include "internal.h"
+#include "reduce.h"
+
+namespace fp8bs {
+namespace {
+
+struct RowArgs {
+    const uint16_t* x; int64_t rows; int32_t cols; int64_t ld_x;
+    uint8_t* q; int64_t ld_q; float* s;
+    const int32_t* live;                    // nullable: rows from *live on are left alone
+    uint16_t* h; int64_t ld_h;              // SILU: nullable
+};
+
+// Eight values of a row as packed bf16: x itself, or h = bf16(silu(gate) * up)
+// with the up projection's columns behind the gate's.
+template <bool SILU>
+__device__ __forceinline__ uint4 row_chunk(const RowArgs& p, const uint16_t* x, int at) {
+    const uint4 a = load_nt16(x + at);
+    if (!SILU) return a;
+    const uint4 u = load_nt16(x + p.cols + at);
+    uint32_t hb[8];
+    silu_mul8_bf16(a, u, hb);
+    return make_uint4(hb[0] | hb[1] << 16, hb[2] | hb[3] << 16, hb[4] | hb[5] << 16, hb[6] | hb[7] << 16);
+}
+
+__device__ __forceinline__ void store_codes(const RowArgs& p, uint8_t* q, int at, const uint4 w, const I8Scale& sc) {
+    float v[8];
+    unpack8(w, v);
+    *reinterpret_cast<uint2*>(q + at) = i8_codes8<0>(v, &sc);
+}
+
+// L lanes (a wave or the workgroup) hold a row, C chunks of eight columns each,
+// from the one read to the codes.  A wave per row serves many rows of up to 4096
+// columns; few rows, and longer ones, take a workgroup each.
+template <int L, int C, bool SILU>
+__global__ void __launch_bounds__(256) k_i8_rows(RowArgs p) {
+    __shared__ uint32_t part[4];
+    const int l = threadIdx.x % L;
+    const int64_t row = (int64_t)blockIdx.x * (256 / L) + threadIdx.x / L;
+    const int64_t end = p.live ? min(p.rows, (int64_t)*p.live) : p.rows;
+    if (row >= end) return;                 // whole waves (L 64) or workgroups (L 256)
+    const uint16_t* x = p.x + row * p.ld_x;
+    uint4 w[C];
+    u16x2 m = {0, 0};
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int at = (l + i * L) * 8;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (at < p.cols) w[i] = row_chunk<SILU>(p, x, at);
+        m = absmax_bits(m, w[i]);
+    }
+    uint32_t top = lanes_umax<64>(max((uint32_t)m.x, (uint32_t)m.y));
+    if (L == 256) {
+        if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = top;
+        __syncthreads();
+        top = max(max(part[0], part[1]), max(part[2], part[3]));
+    }
+    const float s = i8_scale_of(top);
+    const I8Scale sc = i8_scale(s);
+    if (l == 0) p.s[row] = s;
+    uint8_t* q = p.q + row * p.ld_q;
+    const int padded = (p.cols + 15) & ~15;
+#pragma unroll
+    for (int i = 0; i < C; ++i) {
+        const int at = (l + i * L) * 8;
+        if (at < padded) store_codes(p, q, at, w[i], sc);       // behind cols: zeros
+        if (SILU && p.h && at < p.cols) store_nt16(p.h + row * p.ld_h + at, w[i]);
+    }
+}
+
+// Rows past 16384 columns: the row is read twice.
+template <bool SILU>
+__global__ void __launch_bounds__(256) k_i8_rows_long(RowArgs p) {
+    __shared__ uint32_t part[4];
+    const int64_t row = blockIdx.x;
+    if (p.live && row >= *p.live) return;
+    const uint16_t* x = p.x + row * p.ld_x;
+    u16x2 m = {0, 0};
+    for (int64_t at = threadIdx.x * 8; at < p.cols; at += 2048) m = absmax_bits(m, row_chunk<SILU>(p, x, (int)at));
+    const uint32_t mine = lanes_umax<64>(max((uint32_t)m.x, (uint32_t)m.y));
+    if ((threadIdx.x & 63) == 0) part[threadIdx.x >> 6] = mine;
+    __syncthreads();
+    const float s = i8_scale_of(max(max(part[0], part[1]), max(part[2], part[3])));
+    const I8Scale sc = i8_scale(s);
+    if (threadIdx.x == 0) p.s[row] = s;
+    const int64_t padded = ((int64_t)p.cols + 15) & ~15ll;
+    for (int64_t at = threadIdx.x * 8; at < padded; at += 2048) {
+        uint4 w = make_uint4(0, 0, 0, 0);
+        if (at < p.cols) w = row_chunk<SILU>(p, x, (int)at);
+        store_codes(p, p.q + row * p.ld_q, (int)at, w, sc);
+        if (SILU && p.h && at < p.cols) store_nt16(p.h + row * p.ld_h + at, w);
+    }
+}
+
+template <bool SILU>
+hipError_t launch_rows(const RowArgs& p, hipStream_t st) {
+    const int chunks = (p.cols + 7) / 8;
+    // a workgroup per row while a wave per row would leave compute units idle
+    const bool wide = chunks > 512 || p.rows < 1024;
+    const dim3 grid((unsigned)(wide ? p.rows : (p.rows + 3) / 4));
+#define FP8BS_ROWS(L, C) hipLaunchKernelGGL((k_i8_rows<L, C, SILU>), grid, dim3(256), 0, st, p)
+    if (wide) {
+        if (chunks <= 256) FP8BS_ROWS(256, 1);
+        else if (chunks <= 512) FP8BS_ROWS(256, 2);
+        else if (chunks <= 1024) FP8BS_ROWS(256, 4);
+        else if (chunks <= 1280) FP8BS_ROWS(256, 5);
+        else if (chunks <= 2048) FP8BS_ROWS(256, 8);
+        else hipLaunchKernelGGL(k_i8_rows_long<SILU>, grid, dim3(256), 0, st, p);
+    } else {
+        if (chunks <= 64) FP8BS_ROWS(64, 1);
+        else if (chunks <= 128) FP8BS_ROWS(64, 2);
+        else if (chunks <= 256) FP8BS_ROWS(64, 4);
+        else if (chunks <= 320) FP8BS_ROWS(64, 5);
+        else FP8BS_ROWS(64, 8);
+    }
+#undef FP8BS_ROWS
+    return hipGetLastError();
+}
+
+// ------------------------------------------------------------------ columns
+// A tile is 128 rows x 64 columns: a thread takes eight columns of four
+// consecutive rows, so that a column's four codes are one word of the LDS tile
+// (column stride 33 words: the 64 writes of a wave hit 64 banks), which leaves
+// for memory as 128 consecutive bytes per column.
+constexpr int kTileRows = 128, kTileCols = 64, kColWords = kTileRows / 4 + 1;
+
+struct ColArgs {
+    const uint16_t* x; int64_t rows; int32_t cols; int64_t ld_x;
+    uint8_t* q; int64_t ld_q; float* s;
+};
+
+__device__ __forceinline__ uint4 col_chunk(const ColArgs& p, int64_t row, int col) {
+    if (row < p.rows && col < p.cols) return *reinterpret_cast<const uint4*>(p.x + row * p.ld_x + col);
+    return make_uint4(0, 0, 0, 0);
+}
+
+__device__ __forceinline__ void encode_tile(const ColArgs& p, int64_t row0, int col0, const I8Scale (&sc)[8],
+                                            uint32_t* tile) {
+    const int c = threadIdx.x & 7, rq = threadIdx.x >> 3;
+    uint2 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+        float v[8];
+        unpack8(col_chunk(p, row0 + 4 * rq + j, col0 + 8 * c), v);
+        w[j] = i8_codes8<1>(v, sc);
+    }
+    __syncthreads();                        // the tile's last readers are done
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const uint32_t sel = (uint32_t)(i & 3) | (uint32_t)(4 + (i & 3)) << 8 | 0x0c0c0000u;
+        const uint32_t a = i < 4 ? w[0].x : w[0].y, b = i < 4 ? w[1].x : w[1].y;
+        const uint32_t d = i < 4 ? w[2].x : w[2].y, e = i < 4 ? w[3].x : w[3].y;
+        tile[(8 * c + i) * kColWords + rq] =
+            __builtin_amdgcn_perm(b, a, sel) | __builtin_amdgcn_perm(e, d, sel) << 16;
+    }
+    __syncthreads();
+    const int64_t padded = (p.rows + 15) & ~15ll;
+#pragma unroll
+    for (int u = 0; u < 2; ++u) {
+        const int piece = threadIdx.x + u * 256, col = piece >> 3, at = (piece & 7) * 16;
+        const uint32_t* t = tile + col * kColWords + (at >> 2);
+        if (col0 + col < p.cols && row0 + at < padded)
+            *reinterpret_cast<uint4*>(p.q + (int64_t)(col0 + col) * p.ld_q + row0 + at) = make_uint4(t[0], t[1], t[2], t[3]);
+    }
+}
+
+// Maxima of a thread's eight columns over its rows row0 + (t / 8), + 32, ...
+__device__ __forceinline__ void col_maxima(const ColArgs& p, int64_t row0, int64_t row1, int col0, uint32_t (&m)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) m[i] = 0;
+    const int col = col0 + 8 * (threadIdx.x & 7);
+#pragma unroll 4
+    for (int64_t r = row0 + (threadIdx.x >> 3); r < row1; r += 32) {
+        const uint4 w = col_chunk(p, r, col);
+        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            m[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m[i]),
+                                                                           __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu)));
+    }
+}
+// ... joined over the workgroup's 32 row lanes: the pattern of column t (t < 64).
+__device__ __forceinline__ uint32_t join_maxima(const uint32_t (&m)[4], uint32_t* lds) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) lds[(threadIdx.x >> 3) * kColWords + 4 * (threadIdx.x & 7) + i] = m[i];
+    __syncthreads();
+    uint32_t top = 0;
+    if (threadIdx.x < kTileCols) {
+        for (int r = 0; r < 32; ++r) {
+            const uint32_t w = lds[r * kColWords + (threadIdx.x >> 1)];
+            top = max(top, (threadIdx.x & 1) ? w >> 16 : w & 0xffffu);
+        }
+    }
+    return top;
+}
+
+// Few rows: a workgroup takes 64 columns whole, maximum first, codes after.
+__global__ void __launch_bounds__(256) k_i8_cols(ColArgs p) {
+    __shared__ uint32_t tile[kTileCols * kColWords];
+    __shared__ float scale[kTileCols];
+    const int col0 = blockIdx.x * kTileCols;
+    uint32_t m[4];
+    col_maxima(p, 0, p.rows, col0, m);
+    const uint32_t top = join_maxima(m, tile);
+    if (threadIdx.x < kTileCols) {
+        const float s = i8_scale_of(top);
+        scale[threadIdx.x] = s;
+        if (col0 + (int)threadIdx.x < p.cols) p.s[col0 + threadIdx.x] = s;
+    }
+    __syncthreads();
+    I8Scale sc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) sc[i] = i8_scale(scale[8 * (threadIdx.x & 7) + i]);
+    for (int64_t r = 0; r < p.rows; r += kTileRows) encode_tile(p, r, col0, sc, tile);
+}
+
+// Many rows, in three launches: zeros into s; the maxima of runs of kMaxRows
+// rows, joined by integer atomics on the scales' patterns (rounding is monotone,
+// so the largest run's scale is the scale of the maximum, and the order of the
+// joins does not matter; NaN's pattern is above infinity's); the codes.
+constexpr int kMaxRows = 256;
+__global__ void __launch_bounds__(256) k_i8_zero(float* s, int64_t n) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i < n) s[i] = 0.0f;
+}
+__global__ void __launch_bounds__(256) k_i8_col_max(ColArgs p) {
+    __shared__ uint32_t lds[32 * kColWords];
+    const int col0 = blockIdx.x * kTileCols;
+    const int64_t r0 = (int64_t)blockIdx.y * kMaxRows;
+    uint32_t m[4];
+    col_maxima(p, r0, min(r0 + kMaxRows, p.rows), col0, m);
+    const uint32_t top = join_maxima(m, lds);
+    if (threadIdx.x < kTileCols && col0 + (int)threadIdx.x < p.cols)
+        atomicMax(reinterpret_cast<uint32_t*>(p.s) + col0 + threadIdx.x, __float_as_uint(i8_scale_of(top)));
+}
+__global__ void __launch_bounds__(256) k_i8_col_codes(ColArgs p) {
+    __shared__ uint32_t tile[kTileCols * kColWords];
+    const int col0 = blockIdx.x * kTileCols;
+    I8Scale sc[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const int col = col0 + 8 * (threadIdx.x & 7) + i;
+        sc[i] = i8_scale(col < p.cols ? p.s[col] : 0.0f);
+    }
+    encode_tile(p, (int64_t)blockIdx.y * kTileRows, col0, sc, tile);
+}
+
+}  // namespace
+
+hipError_t launch_i8_quant_rows(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, uint8_t* q, int64_t ld_q,
+                                float* s, hipStream_t st) {
+    return launch_rows<false>(RowArgs{x, rows, (int32_t)cols, ld_x, q, ld_q, s, nullptr, nullptr, 0}, st);
+}
+
+hipError_t launch_i8_silu_mul_quant(const uint16_t* gu, int64_t rows, int64_t I, int64_t ld_in, const int32_t* live,
+                                    uint8_t* q, int64_t ld_q, float* s, uint16_t* h, int64_t ld_h, hipStream_t st) {
+    return launch_rows<true>(RowArgs{gu, rows, (int32_t)I, ld_in, q, ld_q, s, live, h, ld_h}, st);
+}
+
+hipError_t launch_i8_quant_cols(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, uint8_t* q, int64_t ld_q,
+                                float* s, hipStream_t st) {
+    const ColArgs p{x, rows, (int32_t)cols, ld_x, q, ld_q, s};
+    const unsigned strips = (unsigned)((cols + kTileCols - 1) / kTileCols);
+    if (rows <= 512) {
+        hipLaunchKernelGGL(k_i8_cols, dim3(strips), dim3(256), 0, st, p);
+        return hipGetLastError();
+    }
+    hipLaunchKernelGGL(k_i8_zero, dim3((unsigned)((cols + 255) / 256)), dim3(256), 0, st, s, cols);
+    hipLaunchKernelGGL(k_i8_col_max, dim3(strips, (unsigned)((rows + kMaxRows - 1) / kMaxRows)), dim3(256), 0, st, p);
+    hipLaunchKernelGGL(k_i8_col_codes, dim3(strips, (unsigned)((rows + kTileRows - 1) / kTileRows)), dim3(256), 0, st, p);
+    return hipGetLastError();
+}
+
+}  // namespace fp8bs

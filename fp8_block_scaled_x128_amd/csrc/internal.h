@@ -46,6 +46,26 @@ hipError_t launch_quant_linear_pow2(const uint16_t* x, int64_t rows, int64_t col
                                     hipStream_t st);
 hipError_t launch_e4m3_encode(const float* in, uint8_t* out, int64_t n, hipStream_t st);
 
+// int8_quant.hip: codes in 8-bit integers with a scale per row, or per column
+// (codes transposed), zero-padded to a multiple of 16 along the contraction.
+hipError_t launch_i8_quant_rows(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, uint8_t* q, int64_t ld_q,
+                                float* s, hipStream_t st);
+hipError_t launch_i8_quant_cols(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, uint8_t* q, int64_t ld_q,
+                                float* s, hipStream_t st);
+// SiLU*mul, then the row form; rows from *live on (nullable) are left alone.
+hipError_t launch_i8_silu_mul_quant(const uint16_t* gu, int64_t rows, int64_t I, int64_t ld_in, const int32_t* live,
+                                    uint8_t* q, int64_t ld_q, float* s, uint16_t* h, int64_t ld_h, hipStream_t st);
+
+// int8_gemm.hip
+struct I8GemmArgs {
+    int64_t M, N, K;                 // M = total rows (grouped: rows of all groups)
+    const uint8_t* a; int64_t lda; const float* sa;
+    const uint8_t* b; int64_t ldb; int64_t b_sg; const float* sb; int64_t sb_sg;
+    void* c; int64_t ldc; int out_f32;
+    int32_t G; const int32_t* offsets; const int32_t* a_rows;   // G 0: dense
+};
+hipError_t launch_i8_gemm(const I8GemmArgs& g, hipStream_t st);
+
 // moe.hip
 hipError_t launch_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y, const int32_t* pos,
                               const float* w, int64_t T, int32_t k, void* out, int64_t ld_out, int out_f32,

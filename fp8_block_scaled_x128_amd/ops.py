@@ -32,7 +32,9 @@ EXPORTS = ["fp8_quant_rowblock", "fp8_quant_block2d", "fp8_quant_linear", "fp8_q
            "fp8_moe_route", "fp8_moe_route_ws_size", "fp8_moe_route_backward",
            "fp8_block_norm", "fp8_block_norm_backward", "fp8_block_norm_backward_ws_size", "mxfp8_quant", "mxfp8_quant_t",
            "fp8_quant_dual_axis", "fp8_transpose_codes", "fp8_quant_linear_pow2",
-           "fp8_quant_pow2", "fp8_blockscaled_gemm_pow2", "mxfp8_gemm", "fp8bs_e4m3_encode",
+           "fp8_quant_pow2", "fp8_blockscaled_gemm_pow2", "mxfp8_gemm", "int8_quant",
+           "int8_silu_mul_quant", "int8_gemm", "int8_linear", "int8_linear_ws_size", "int8_grouped_gemm",
+           "fp8bs_e4m3_encode",
            "fp8bs_status_string", "fp8bs_last_error_detail"]
 
 
@@ -100,6 +102,12 @@ def load():
             "fp8_quant_pow2": [P, I64, I64, I64, I32, P, I64, P, I64, P],
             "fp8_blockscaled_gemm_pow2": [I64, I64, I64, P, I64, P, I64, P, I64, P, I64, P, I64, INT, P],
             "mxfp8_gemm": [I64, I64, I64, I32, P, P, I64, P, I64, P, I64, P, I64, I64, P, I64, I64, P, I64, INT, P],
+            "int8_quant": [P, I64, I64, I64, INT, P, I64, P, P],
+            "int8_silu_mul_quant": [P, I64, I64, I64, P, P, I64, P, P, I64, P],
+            "int8_gemm": [I64, I64, I64, P, I64, P, P, I64, P, P, I64, INT, P],
+            "int8_linear": [I64, I64, I64, P, I64, P, I64, P, P, I64, INT, P, ctypes.c_size_t, P],
+            "int8_linear_ws_size": [I64, I64, P],
+            "int8_grouped_gemm": [I64, I64, I64, I32, P, P, I64, P, I64, P, P, I64, I64, P, I64, P, I64, INT, P],
             "fp8bs_e4m3_encode": [P, P, I64, P],
         }
         for name, args in sig.items():
@@ -374,6 +382,43 @@ def mxfp8_gemm(rows, N, K, G, offsets, a_rows, a_count, a, lda, sa, lds_a, b, ld
     st = load().mxfp8_gemm(rows, N, K, G, _p(offsets), _p(a_rows), a_count, _p(a), lda, _p(sa), lds_a, _p(b), ldb,
                            b_stride_g, _p(sb), lds_b, sb_stride_g, _p(c), ldc, out, _stream(stream))
     return _check("mxfp8_gemm", st, raise_on_error)
+
+
+def int8_quant(x, rows, cols, ld_x, axis, q, ld_q, s, stream=None, raise_on_error=True):
+    st = load().int8_quant(_p(x), rows, cols, ld_x, axis, _p(q), ld_q, _p(s), _stream(stream))
+    return _check("int8_quant", st, raise_on_error)
+
+
+def int8_silu_mul_quant(gate_up, rows, I, ld_in, live_rows, q, ld_q, s, h_out, ld_h, stream=None,
+                        raise_on_error=True):
+    st = load().int8_silu_mul_quant(_p(gate_up), rows, I, ld_in, _p(live_rows), _p(q), ld_q, _p(s), _p(h_out), ld_h,
+                                    _stream(stream))
+    return _check("int8_silu_mul_quant", st, raise_on_error)
+
+
+def int8_gemm(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, out, stream=None, raise_on_error=True):
+    st = load().int8_gemm(M, N, K, _p(a), lda, _p(sa), _p(b), ldb, _p(sb), _p(c), ldc, out, _stream(stream))
+    return _check("int8_gemm", st, raise_on_error)
+
+
+def int8_linear(rows, N, cols, x, ld_x, w, ld_w, sw, y, ld_y, out, ws, ws_bytes, stream=None, raise_on_error=True):
+    st = load().int8_linear(rows, N, cols, _p(x), ld_x, _p(w), ld_w, _p(sw), _p(y), ld_y, out, _p(ws), ws_bytes,
+                            _stream(stream))
+    return _check("int8_linear", st, raise_on_error)
+
+
+def int8_linear_ws_size(rows, cols):
+    """Workspace bytes of int8_linear (host only)."""
+    out = ctypes.c_size_t(0)
+    _check("int8_linear_ws_size", load().int8_linear_ws_size(rows, cols, ctypes.byref(out)))
+    return out.value
+
+
+def int8_grouped_gemm(total_rows, N, K, G, offsets, a_rows, a_count, a, lda, sa, b, ldb, b_stride_g, sb, sb_stride_g,
+                      c, ldc, out, stream=None, raise_on_error=True):
+    st = load().int8_grouped_gemm(total_rows, N, K, G, _p(offsets), _p(a_rows), a_count, _p(a), lda, _p(sa), _p(b),
+                                  ldb, b_stride_g, _p(sb), sb_stride_g, _p(c), ldc, out, _stream(stream))
+    return _check("int8_grouped_gemm", st, raise_on_error)
 
 
 def fp8bs_e4m3_encode(inp, out, n, stream=None, raise_on_error=True):
@@ -874,6 +919,177 @@ def moe_combine_backward(dout, y, token_rows, weights, *, out=None):
                                          _arr("out[1]", dw, (T, k), dev, _F32), _stream())
     if st:
         _check("fp8_moe_combine_backward", st)
+    return out
+
+
+# ------------------------------------------ linear layers in 8-bit integers
+# Codes are int8 tensors whose rows are zero-padded to a multiple of 16 columns
+# (the products' granularity along K) and scales fp32, one per row.
+_I8 = torch.int8
+
+
+def _pad16(n):
+    return (n + 15) // 16 * 16
+
+
+def i8_quant(x, axis: int = AXIS_ROW, out=None):
+    """Codes and scales of a bf16 [rows, cols] tensor (see int8_quant): (q [rows,
+    cols padded to 16], s [rows]), or with AXIS_COL the transposed codes with a
+    scale per column, (q [cols, rows padded to 16], s [cols])."""
+    rows, cols = x.shape
+    dev = _device()
+    xp, ld_x = _mat("x", x, rows, cols, dev, _BF)
+    n, k = (rows, cols) if axis == AXIS_ROW else (cols, rows)
+    if out is None:
+        out = (torch.empty((n, _pad16(k)), dtype=_I8, device=x.device), torch.empty(n, dtype=_F32, device=x.device))
+    qp, ld_q = _mat("out[0]", out[0], n, _pad16(k), dev, _I8)
+    st = load().int8_quant(xp, rows, cols, ld_x, axis, qp, ld_q, _arr("out[1]", out[1], (n,), dev, _F32), _stream())
+    if st:
+        _check("int8_quant", st)
+    return out
+
+
+def i8_gemm(a, sa, b, sb, out_dtype=torch.bfloat16, out=None):
+    """C [M, N] = diag(sa) (A B^T) diag(sb) for int8 codes a [M, K], b [N, K] and
+    fp32 scales sa [M], sb [N] (see int8_gemm)."""
+    (M, K), N, dev = a.shape, b.shape[0], _device()
+    ap, lda = _mat("a", a, M, K, dev, _I8)
+    bp, ldb = _mat("b", b, N, K, dev, _I8)
+    if out is None:
+        out = torch.empty((M, N), dtype=out_dtype, device=a.device)
+    cp, ldc = _mat("out", out, M, N, dev, out_dtype)
+    st = load().int8_gemm(M, N, K, ap, lda, _arr("sa", sa, (M,), dev, _F32), bp, ldb, _arr("sb", sb, (N,), dev, _F32),
+                          cp, ldc, _otype(out_dtype), _stream())
+    if st:
+        _check("int8_gemm", st)
+    return out
+
+
+class I8Linear(NamedTuple):
+    """Output of i8_linear and its workspace."""
+    y: torch.Tensor
+    ws: torch.Tensor
+
+
+def i8_linear(x, qw, sw, out_dtype=torch.bfloat16, out: Optional[I8Linear] = None) -> I8Linear:
+    """Y = X W^T for X bf16 [rows, cols], quantized per token on the way, and a
+    weight's codes qw [out features, cols padded to 16] and scales sw (i8_quant of
+    the weight).  `out` is an earlier result for the same sizes whose tensors are
+    written again (two calls in flight need two)."""
+    (rows, cols), N, dev = x.shape, qw.shape[0], _device()
+    xp, ld_x = _mat("x", x, rows, cols, dev, _BF)
+    wp, ld_w = _mat("qw", qw, N, _pad16(cols), dev, _I8)
+    if out is None:
+        out = I8Linear(torch.empty((rows, N), dtype=out_dtype, device=x.device),
+                       _u8((int8_linear_ws_size(rows, cols),), x.device))
+    yp, ld_y = _mat("out.y", out.y, rows, N, dev, out_dtype)
+    wsp, wsn = _workspace(out.ws, dev)
+    st = load().int8_linear(rows, N, cols, xp, ld_x, wp, ld_w, _arr("sw", sw, (N,), dev, _F32), yp, ld_y,
+                            _otype(out_dtype), wsp, wsn, _stream())
+    if st:
+        _check("int8_linear", st)
+    return out
+
+
+def i8_linear_forward(x, w, out_dtype=torch.bfloat16):
+    """(y, saved) of a linear layer whose bf16 weight w [out, in] is quantized per
+    output channel for this call; saved = (w, x) is what i8_linear_backward reads."""
+    qw, sw = i8_quant(w)
+    return i8_linear(x, qw, sw, out_dtype).y, (w, x)
+
+
+class I8LinearGrads(NamedTuple):
+    """Outputs of i8_linear_backward; codes and scales are its workspaces: (q, s)
+    of dY per token, dY per output channel, W and X per input channel."""
+    dx: torch.Tensor
+    dw: torch.Tensor
+    codes: tuple
+
+
+def i8_linear_backward(dy, saved, out: Optional[I8LinearGrads] = None) -> I8LinearGrads:
+    """dX = dY W and dW = dY^T X, both fp32, of Y = X W^T in 8-bit integers, each
+    operand with a scale per row of the product it enters: dY per token and W per
+    input channel for dX, dY per output channel and X per input channel, both over
+    the tokens, for dW (rounding to codes is passed straight through)."""
+    w, x = saved
+    (T, O), I = dy.shape, x.shape[1]
+    if x.shape[0] != T or w.shape != (O, I):
+        raise ValueError("dy %s, w %s and x %s do not belong to one layer" % (tuple(dy.shape), tuple(w.shape),
+                                                                              tuple(x.shape)))
+    if out is None:
+        e = lambda r, c: torch.empty((r, c), dtype=_F32, device=dy.device)
+        out = I8LinearGrads(e(T, I), e(O, I), (None,) * 4)
+    dyr, dyc, wc, xc = out.codes
+    dyr, dyc = i8_quant(dy, AXIS_ROW, dyr), i8_quant(dy, AXIS_COL, dyc)
+    wc, xc = i8_quant(w, AXIS_COL, wc), i8_quant(x, AXIS_COL, xc)
+    i8_gemm(*dyr, *wc, _F32, out.dx)
+    i8_gemm(*dyc, *xc, _F32, out.dw)
+    return I8LinearGrads(out.dx, out.dw, (dyr, dyc, wc, xc))
+
+
+def i8_grouped_gemm(a, sa, b, sb, offsets, row_token=None, out_dtype=torch.bfloat16, out=None):
+    """C [rows, N] of the experts' products (see int8_grouped_gemm): codes a [T, K]
+    with scales sa [T], experts' codes b [G, N, K] with sb [G, N], int32 offsets
+    [G + 1]; row r reads a's row row_token[r] (int32 [rows]; without it, row r).
+    Rows from offsets[G] on are not written."""
+    (T, K), (G, N, Kb), dev = a.shape, b.shape, _device()
+    if Kb != K or b.dtype is not _I8 or b.get_device() != dev or (K > 1 and b.stride(2) != 1):
+        raise ValueError("b: int8 [G, N, %d] with unit column stride on cuda:%d expected, got %s %s, strides %s, on %s"
+                         % (K, dev, b.dtype, tuple(b.shape), b.stride(), b.device))
+    ap, lda = _mat("a", a, T, K, dev, _I8)
+    rows = T if row_token is None else row_token.numel()
+    if out is None:
+        out = torch.empty((rows, N), dtype=out_dtype, device=a.device)
+    cp, ldc = _mat("out", out, rows, N, dev, out_dtype)
+    st = load().int8_grouped_gemm(rows, N, K, G, _arr("offsets", offsets, (G + 1,), dev, _I32),
+                                  _arr("row_token", row_token, (rows,), dev, _I32), T, ap, lda,
+                                  _arr("sa", sa, (T,), dev, _F32), b.data_ptr(), b.stride(1) if N > 1 else K,
+                                  b.stride(0) if G > 1 else 0, _arr("sb", sb, (G, N), dev, _F32), N, cp, ldc,
+                                  _otype(out_dtype), _stream())
+    if st:
+        _check("int8_grouped_gemm", st)
+    return out
+
+
+def i8_silu_mul_quant(gate_up, live_rows=None, out=None):
+    """Codes and scales of h = bf16(silu(gate) * up) per row, gate_up bf16 [rows,
+    2 I] (see int8_silu_mul_quant): (q [rows, I padded to 16], s [rows]).
+    live_rows: one int32 on the device; rows from it on are left alone."""
+    rows, I, dev = gate_up.shape[0], gate_up.shape[1] // 2, _device()
+    gp, ld = _mat("gate_up", gate_up, rows, 2 * I, dev, _BF)
+    if out is None:
+        out = (torch.empty((rows, _pad16(I)), dtype=_I8, device=gate_up.device),
+               torch.empty(rows, dtype=_F32, device=gate_up.device))
+    qp, ld_q = _mat("out[0]", out[0], rows, _pad16(I), dev, _I8)
+    lp = None if live_rows is None else _arr("live_rows", live_rows, live_rows.shape, dev, _I32)
+    if lp is not None and live_rows.numel() != 1:
+        raise ValueError("live_rows: one number expected")
+    st = load().int8_silu_mul_quant(gp, rows, I, ld, lp, qp, ld_q, _arr("out[1]", out[1], (rows,), dev, _F32), None, 0,
+                                    _stream())
+    if st:
+        _check("int8_silu_mul_quant", st)
+    return out
+
+
+def i8_moe_forward(x, qgu, sgu, qdt, sdt, offsets, row_token, token_rows, weights, out_dtype=torch.bfloat16):
+    """One MoE layer forward in 8-bit integers: X [T, H] per token, the experts'
+    gate and up products (gathered by row_token), SiLU*mul and the codes of h, the
+    down product, the routing-weighted combine over the slots that have a row.
+    qgu [G, 2 I, H] codes (gate rows [0, I), up rows [I, 2 I)) with sgu [G, 2 I],
+    qdt [G, H, I] with sdt [G, H]; H % 16 == I % 16 == 0.  offsets, row_token,
+    token_rows and weights as moe_route and moe_route_grouped give them."""
+    T, H = x.shape
+    k, rows = token_rows.shape[1], row_token.numel()
+    if H % 16 or qgu.shape[2] != H or qgu.shape[1] % 32 or qdt.shape != (qgu.shape[0], H, qgu.shape[1] // 2):
+        raise ValueError("activations of %d columns, experts of %s and %s" % (H, tuple(qgu.shape), tuple(qdt.shape)))
+    dev = _device()
+    pos, w = _arr("token_rows", token_rows, (T, k), dev, _I32), _arr("weights", weights, (T, k), dev, _F32)
+    qx, sx = i8_quant(x)
+    gu = i8_grouped_gemm(qx, sx, qgu, sgu, offsets, row_token)
+    qh, sh = i8_silu_mul_quant(gu, offsets[-1])
+    y = i8_grouped_gemm(qh, sh, qdt, sdt, offsets)
+    out = torch.empty((T, H), dtype=out_dtype, device=x.device)
+    fp8_moe_combine_routed(y, rows, H, H, pos, w, T, k, out, H, _otype(out_dtype))
     return out
 
 

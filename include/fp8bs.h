@@ -814,6 +814,103 @@ fp8bs_status mxfp8_gemm(int64_t rows, int64_t N, int64_t K, int32_t G,
                         void* c, int64_t ldc, fp8bs_out out, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
+ * int8_quant -- codes in 8-bit integers with one scale per row (per token) or
+ * per column (per channel), the operands of int8_gemm: next to the FP8 codes,
+ * the integer form of rowwise scaling ("Towards Full Pipeline FP8 Reinforcement
+ * Learning for LLMs" compares rowwise with blockwise scalings).  Per row or
+ * column
+ *     S = fp32(max|x| / 127),  q = the integer nearest to x / S, ties to even
+ * (S = 0 and codes 0 where all values are 0; |q| <= 127).  The quotient is
+ * decided exactly: codes equal those of a 64-bit evaluation for every finite x.
+ * A row or column that holds an infinity or a NaN has that scale (infinite or
+ * NaN) and codes 0, so that every product with it is NaN.
+ *
+ * x    : bf16 [rows][ld_x].
+ * axis : FP8BS_AXIS_ROW: q is [rows][ld_q], s [rows].  FP8BS_AXIS_COL: one scale
+ *        per column; q is written transposed, [cols][ld_q] with the rows
+ *        contiguous, s [cols] (this equals FP8BS_AXIS_ROW on the transpose).
+ * The codes of each output row are padded with zeros to a multiple of 16, the
+ * products' granularity along K; bytes behind that are left as they were.
+ * s holds maxima while the call's kernels run (AXIS_COL).  Without rows, a
+ * column's scale is 0.
+ * Requirements: rows, cols >= 0; cols % 8 == 0, ld_x >= cols, ld_x % 8 == 0, x
+ * 16-byte aligned; ld_q >= the padded length, ld_q % 16 == 0, q 16-byte aligned;
+ * s 4-byte aligned; AXIS_COL: rows <= 65535 * 128.
+ * ------------------------------------------------------------------------ */
+fp8bs_status int8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, fp8bs_axis axis,
+                        int8_t* q, int64_t ld_q, float* s, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * int8_silu_mul_quant -- the step between the two products of an expert:
+ * h = bf16(silu(gate) * up) (as in fp8_silu_mul_quant, bit-exact against a 64-bit
+ * evaluation), then int8_quant's row form of h.
+ *
+ * gate_up   : bf16 [rows][ld_in]; columns [0, I) gate, [I, 2 I) up.
+ * live_rows : nullable device int32: rows from *live_rows on are neither read nor
+ *             written (the last entry of a router's offsets: the rows behind the
+ *             last assignment hold nothing).
+ * q, ld_q, s : as in int8_quant.   h_out : nullable bf16 [rows][ld_h].
+ * Requirements: I % 8 == 0; ld_in >= 2 I, ld_in % 8 == 0, gate_up 16-byte
+ * aligned; ld_h >= I, ld_h % 8 == 0, h_out 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+fp8bs_status int8_silu_mul_quant(const uint16_t* gate_up, int64_t rows, int64_t I, int64_t ld_in,
+                                 const int32_t* live_rows, int8_t* q, int64_t ld_q, float* s, uint16_t* h_out,
+                                 int64_t ld_h, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * int8_gemm -- C = A B^T on 8-bit integer codes with a scale per row of either
+ * operand (tokens, channels):
+ *
+ *   C[m, n] = sa[m] * sb[n] * sum_k a[m, k] b[n, k]
+ *
+ * The sum is exact (32-bit integers), converted to fp32 once, multiplied by sa,
+ * then by sb, in fp32, and rounded once for bf16 output: the result does not
+ * depend on tiles or order.  K == 0 gives 0 * sa * sb.
+ *
+ * a : int8 [M][lda], sa fp32 [M];  b : int8 [N][ldb], sb fp32 [N], K contiguous.
+ * c : [M][ldc], bf16 or fp32 per `out`.
+ * Requirements: M, N >= 0; 0 <= K <= 131056; K % 16 == 0 (int8_quant pads codes
+ * with zeros); N % 8 == 0; lda, ldb >= K, % 16 == 0, a and b 16-byte aligned and
+ * below 4 GiB each; ldc >= N, ldc % 8 == 0, c 16-byte aligned.
+ * ------------------------------------------------------------------------ */
+fp8bs_status int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* sa,
+                       const int8_t* b, int64_t ldb, const float* sb, void* c, int64_t ldc, fp8bs_out out,
+                       hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * int8_linear -- Y = X W^T with X bf16 quantized per token on the way (int8_quant,
+ * FP8BS_AXIS_ROW) and W given as codes and scales per output channel; the result
+ * is that of the two calls.
+ *
+ * x : bf16 [rows][ld_x], cols columns.   w : int8 [N][ld_w], sw fp32 [N]; columns
+ * from cols to the next multiple of 16 hold zeros.   y : [rows][ld_y] per `out`.
+ * ws : device workspace of int8_linear_ws_size bytes, 16-byte aligned; contents on
+ *      entry are ignored.  Calls that overlap in time need separate workspaces.
+ * Requirements: as int8_quant and int8_gemm.
+ * ------------------------------------------------------------------------ */
+fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* x, int64_t ld_x, const int8_t* w,
+                         int64_t ld_w, const float* sw, void* y, int64_t ld_y, fp8bs_out out, void* ws,
+                         size_t ws_bytes, hipStream_t stream);
+/* Host only: the workspace int8_linear needs. */
+fp8bs_status int8_linear_ws_size(int64_t rows, int64_t cols, size_t* bytes);
+
+/* ------------------------------------------------------------------------
+ * int8_grouped_gemm -- int8_gemm over G expert groups of rows: row r of group g
+ * is C[r, n] = sa[t] sb_g[n] sum_k a[t, k] b_g[n, k], t = a_rows[r] (t = r without
+ * a_rows).  offsets, a_rows, a_count and what is left unwritten: as in
+ * fp8_grouped_gemm.
+ *
+ * b : expert g's [N][ldb] codes at b + g * b_stride_g, its scales at
+ *     sb + g * sb_stride_g.
+ * Requirements: as int8_gemm; 1 <= G <= 65535; b_stride_g >= 0, % 16 == 0;
+ * sb_stride_g >= 0.
+ * ------------------------------------------------------------------------ */
+fp8bs_status int8_grouped_gemm(int64_t total_rows, int64_t N, int64_t K, int32_t G, const int32_t* offsets,
+                               const int32_t* a_rows, int64_t a_count, const int8_t* a, int64_t lda, const float* sa,
+                               const int8_t* b, int64_t ldb, int64_t b_stride_g, const float* sb,
+                               int64_t sb_stride_g, void* c, int64_t ldc, fp8bs_out out, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
  * fp8bs_e4m3_encode -- encode n fp32 values with the same device routine the
  * quantizers use (round to nearest even, saturating to +-448).  For checking
  * the device codec against a table; not on the layer's hot path.
