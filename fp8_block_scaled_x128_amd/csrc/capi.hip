@@ -595,6 +595,28 @@ static fp8bs_status route_shape(int64_t T, int32_t E, int64_t ld, fp8bs_out type
     return FP8BS_OK;
 }
 
+// The buffers of both routers; fills p.
+static fp8bs_status route_buffers(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k,
+                                  int32_t renorm, const uint8_t* mask, int32_t* experts, float* weights,
+                                  int32_t* counts, int32_t* offsets, int32_t* row_token, int32_t* token_rows,
+                                  float* lse, float* loss, const void* ws, size_t ws_bytes, RouteArgs* p) {
+    if (!counts || !offsets || !loss) return fail(FP8BS_ERR_NULL, "counts, offsets and loss are required");
+    if (T > 0 && (!logits || !experts || !weights || !row_token || !token_rows || !lse))
+        return fail(FP8BS_ERR_NULL, "logits, experts, weights, row_token, token_rows and lse are required");
+    const size_t need = route_ws_bytes(T, E);
+    if (need > 0 && !ws) return fail(FP8BS_ERR_NULL, "a workspace of %zu bytes is required", need);
+    if (ws_bytes < need) return fail(FP8BS_ERR_SHAPE, "ws_bytes %zu < %zu", ws_bytes, need);
+    if (!aligned(logits, type == FP8BS_OUT_FP32 ? 4 : 2) || !aligned(experts, 4) || !aligned(weights, 4) ||
+        !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(token_rows, 4) ||
+        !aligned(lse, 4) || !aligned(loss, 4) || !aligned(ws, 16))
+        return fail(FP8BS_ERR_ALIGN, "a pointer is not aligned to its element (ws: 16 bytes)");
+    fp8bs_status d = check_device();
+    if (d != FP8BS_OK) return d;
+    *p = RouteArgs{logits, T, E, ld, type == FP8BS_OUT_FP32, k, renorm != 0, mask, experts, weights,
+                   counts, offsets, row_token, token_rows, lse, loss};
+    return FP8BS_OK;
+}
+
 fp8bs_status fp8_moe_route_ws_size(int64_t T, int32_t E, size_t* bytes) {
     if (T < 0 || T > (1ll << 22)) return fail(FP8BS_ERR_SHAPE, "T=%lld outside [0, 2^22]", (long long)T);
     if (E < 1 || E > 1024) return fail(FP8BS_ERR_SHAPE, "E=%d outside [1, 1024]", (int)E);
@@ -609,20 +631,10 @@ fp8bs_status fp8_moe_route(const void* logits, int64_t T, int32_t E, int64_t ld,
                            void* ws, size_t ws_bytes, hipStream_t stream) {
     fp8bs_status v = route_shape(T, E, ld, type, k, renorm);
     if (v != FP8BS_OK) return v;
-    if (!counts || !offsets || !loss) return fail(FP8BS_ERR_NULL, "counts, offsets and loss are required");
-    if (T > 0 && (!logits || !experts || !weights || !row_token || !token_rows || !lse))
-        return fail(FP8BS_ERR_NULL, "logits, experts, weights, row_token, token_rows and lse are required");
-    const size_t need = route_ws_bytes(T, E);
-    if (need > 0 && !ws) return fail(FP8BS_ERR_NULL, "a workspace of %zu bytes is required", need);
-    if (ws_bytes < need) return fail(FP8BS_ERR_SHAPE, "ws_bytes %zu < %zu", ws_bytes, need);
-    if (!aligned(logits, type == FP8BS_OUT_FP32 ? 4 : 2) || !aligned(experts, 4) || !aligned(weights, 4) ||
-        !aligned(counts, 4) || !aligned(offsets, 4) || !aligned(row_token, 4) || !aligned(token_rows, 4) ||
-        !aligned(lse, 4) || !aligned(loss, 4) || !aligned(ws, 16))
-        return fail(FP8BS_ERR_ALIGN, "a pointer is not aligned to its element (ws: 16 bytes)");
-    fp8bs_status d = check_device();
-    if (d != FP8BS_OK) return d;
-    RouteArgs p{logits, T, E, ld, type == FP8BS_OUT_FP32, k, renorm != 0, mask, experts, weights,
-                counts, offsets, row_token, token_rows, lse, loss};
+    RouteArgs p{};
+    if ((v = route_buffers(logits, T, E, ld, type, k, renorm, mask, experts, weights, counts, offsets, row_token,
+                           token_rows, lse, loss, ws, ws_bytes, &p)) != FP8BS_OK)
+        return v;
     return launched(launch_moe_route(p, ws, stream), "fp8_moe_route");
 }
 
@@ -647,6 +659,72 @@ fp8bs_status fp8_moe_route_backward(const void* logits, int64_t T, int32_t E, in
     RouteBwdArgs p{logits, T, E, ld, type == FP8BS_OUT_FP32, k, renorm != 0, experts, weights, counts, lse,
                    dweights, dloss, dlogits, ld_d};
     return launched(launch_moe_route_bwd(p, stream), "fp8_moe_route_backward");
+}
+
+// Scores and groups of fp8_moe_route_grouped; finite without <cmath>: x - x is 0.
+static fp8bs_status gate_shape(int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k, int32_t renorm,
+                               fp8bs_score score, float scale) {
+    if (score != FP8BS_SCORE_SOFTMAX && score != FP8BS_SCORE_SIGMOID)
+        return fail(FP8BS_ERR_UNSUPPORTED, "score %d", (int)score);
+    if (!(scale - scale == 0.0f)) return fail(FP8BS_ERR_UNSUPPORTED, "scale must be finite");
+    return route_shape(T, E, ld, type, k, renorm);
+}
+
+fp8bs_status fp8_moe_route_grouped(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k,
+                                   fp8bs_score score, const float* bias, int32_t groups, int32_t keep_groups,
+                                   fp8bs_group_score group_score, int32_t renorm, float scale, const uint8_t* mask,
+                                   int32_t* experts, float* weights, int32_t* counts, int32_t* offsets,
+                                   int32_t* row_token, int32_t* token_rows, float* total, float* loss, void* ws,
+                                   size_t ws_bytes, hipStream_t stream) {
+    fp8bs_status v = gate_shape(T, E, ld, type, k, renorm, score, scale);
+    if (v != FP8BS_OK) return v;
+    if (group_score != FP8BS_GROUP_MAX && group_score != FP8BS_GROUP_TOP2)
+        return fail(FP8BS_ERR_UNSUPPORTED, "group_score %d", (int)group_score);
+    if (groups < 1 || groups > 64 || E % groups)
+        return fail(FP8BS_ERR_SHAPE, "groups=%d: 1 to 64 that divide E=%d", (int)groups, (int)E);
+    if (keep_groups < 1 || keep_groups > groups || k > keep_groups * (E / groups))
+        return fail(FP8BS_ERR_SHAPE, "keep_groups=%d outside [1, groups], or fewer than k=%d experts in them",
+                    (int)keep_groups, (int)k);
+    if (!aligned(bias, 4)) return fail(FP8BS_ERR_ALIGN, "bias must be 4-byte aligned");
+    RouteArgs p{};
+    if ((v = route_buffers(logits, T, E, ld, type, k, renorm, mask, experts, weights, counts, offsets, row_token,
+                           token_rows, total, loss, ws, ws_bytes, &p)) != FP8BS_OK)
+        return v;
+    const GateArgs g{p, score == FP8BS_SCORE_SIGMOID, bias, groups, keep_groups, group_score == FP8BS_GROUP_TOP2, scale};
+    return launched(launch_moe_route_grouped(g, ws, stream), "fp8_moe_route_grouped");
+}
+
+fp8bs_status fp8_moe_route_grouped_backward(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type,
+                                            int32_t k, fp8bs_score score, int32_t renorm, float scale,
+                                            const int32_t* experts, const int32_t* counts, const float* total,
+                                            const float* dweights, const float* dloss, void* dlogits, int64_t ld_d,
+                                            hipStream_t stream) {
+    fp8bs_status v = gate_shape(T, E, ld, type, k, renorm, score, scale);
+    if (v != FP8BS_OK) return v;
+    if (T == 0) return ok();
+    if (!dweights && !dloss) return fail(FP8BS_ERR_NULL, "dweights or dloss is required");
+    if (!logits || !total || !dlogits) return fail(FP8BS_ERR_NULL, "logits, total and dlogits are required");
+    if (dweights && !experts) return fail(FP8BS_ERR_NULL, "experts are required with dweights");
+    if (dloss && !counts) return fail(FP8BS_ERR_NULL, "counts are required with dloss");
+    if (ld_d < E) return fail(FP8BS_ERR_STRIDE, "ld_d < E");
+    const uintptr_t a = type == FP8BS_OUT_FP32 ? 4 : 2;
+    if (!aligned(logits, a) || !aligned(dlogits, a) || !aligned(experts, 4) || !aligned(counts, 4) ||
+        !aligned(total, 4) || !aligned(dweights, 4) || !aligned(dloss, 4))
+        return fail(FP8BS_ERR_ALIGN, "a pointer is not aligned to its element");
+    if ((v = check_device()) != FP8BS_OK) return v;
+    const GateBwdArgs p{logits, T, E, ld, type == FP8BS_OUT_FP32, k, renorm != 0, score == FP8BS_SCORE_SIGMOID, scale,
+                        experts, counts, total, dweights, dloss, dlogits, ld_d};
+    return launched(launch_moe_route_grouped_bwd(p, stream), "fp8_moe_route_grouped_backward");
+}
+
+fp8bs_status fp8_moe_bias_update(float* bias, const int32_t* counts, int32_t E, float rate, hipStream_t stream) {
+    if (E < 1 || E > 1024) return fail(FP8BS_ERR_SHAPE, "E=%d outside [1, 1024]", (int)E);
+    if (!(rate - rate == 0.0f)) return fail(FP8BS_ERR_UNSUPPORTED, "rate must be finite");
+    if (!bias || !counts) return fail(FP8BS_ERR_NULL, "bias and counts are required");
+    if (!aligned(bias, 4) || !aligned(counts, 4)) return fail(FP8BS_ERR_ALIGN, "a pointer is not aligned to its element");
+    const fp8bs_status d = check_device();
+    if (d != FP8BS_OK) return d;
+    return launched(launch_moe_bias_update(bias, counts, E, rate, stream), "fp8_moe_bias_update");
 }
 
 // One matrix argument of the norms: nullable; leading dimension and alignment.

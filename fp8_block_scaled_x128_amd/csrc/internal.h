@@ -132,6 +132,10 @@ struct RouteArgs {
 };
 struct RouteWs { int32_t epad; uint8_t* hist; float* psum; float* lse2; int32_t* live; int32_t* run_cnt; float* run_psum; };
 size_t route_ws_bytes(int64_t T, int32_t E);
+RouteWs route_workspace(int64_t T, int32_t E, void* ws);
+// Counts, offsets, row maps and losses from what the selecting launch left in ws
+// (more than 64 tokens).
+hipError_t launch_route_rows(const RouteArgs& p, const RouteWs& ws, hipStream_t st);
 hipError_t launch_moe_route(const RouteArgs& p, void* ws, hipStream_t st);
 
 struct RouteBwdArgs {
@@ -142,6 +146,22 @@ struct RouteBwdArgs {
     void* dlogits; int64_t ld_d;
 };
 hipError_t launch_moe_route_bwd(const RouteBwdArgs& p, hipStream_t st);
+
+// route_grouped.hip: scores, a selection bias and groups of experts.
+struct GateArgs {
+    RouteArgs r;                     // r.lse: the scores' total
+    bool sigmoid; const float* bias; int32_t groups, keep; bool top2; float scale;
+};
+hipError_t launch_moe_route_grouped(const GateArgs& p, void* ws, hipStream_t st);
+struct GateBwdArgs {
+    const void* logits; int64_t T; int32_t E; int64_t ld; bool logits32;      // dlogits has the same type
+    int32_t k; bool renorm, sigmoid; float scale;
+    const int32_t* experts; const int32_t* counts; const float* total;
+    const float* dweights; const float* dloss;
+    void* dlogits; int64_t ld_d;
+};
+hipError_t launch_moe_route_grouped_bwd(const GateBwdArgs& p, hipStream_t st);
+hipError_t launch_moe_bias_update(float* bias, const int32_t* counts, int32_t E, float rate, hipStream_t st);
 
 // gemm.hip
 struct GemmArgs {

@@ -24,12 +24,15 @@ STATUS = {0: "FP8BS_OK", 1: "FP8BS_ERR_NULL", 2: "FP8BS_ERR_SHAPE", 3: "FP8BS_ER
 AXIS_ROW, AXIS_COL = 0, 1
 OUT_BF16, OUT_FP32 = 0, 1
 BSCALE_BLOCK128, BSCALE_ROW128 = 0, 1
+SCORE_SOFTMAX, SCORE_SIGMOID = 0, 1
+GROUP_MAX, GROUP_TOP2 = 0, 1
 
 EXPORTS = ["fp8_quant_rowblock", "fp8_quant_block2d", "fp8_quant_linear", "fp8_quant_rowwise", "fp8_quant_tensorwise", "fp8_blockscaled_gemm", "fp8_blockscaled_gemm_plan",
            "fp8_blockscaled_gemm_splitk", "fp8_blockscaled_gemm_splitk_noalloc", "fp8_blockscaled_gemm_splitk_plan",
            "fp8_grouped_gemm", "fp8_grouped_gemm_ws_size", "fp8_grouped_gemm_swiglu_quant", "mxfp8_grouped_gemm_swiglu_quant",
            "fp8_silu_mul_quant", "fp8_moe_combine", "fp8_moe_combine_routed", "fp8_moe_combine_backward",
            "fp8_moe_route", "fp8_moe_route_ws_size", "fp8_moe_route_backward",
+           "fp8_moe_route_grouped", "fp8_moe_route_grouped_backward", "fp8_moe_bias_update",
            "fp8_block_norm", "fp8_block_norm_backward", "fp8_block_norm_backward_ws_size", "mxfp8_quant", "mxfp8_quant_t",
            "fp8_quant_dual_axis", "fp8_transpose_codes", "fp8_quant_linear_pow2",
            "fp8_quant_pow2", "fp8_blockscaled_gemm_pow2", "mxfp8_gemm", "int8_quant",
@@ -89,6 +92,10 @@ def load():
             "fp8_moe_route": [P, I64, I32, I64, INT, I32, I32, P, P, P, P, P, P, P, P, P, P, ctypes.c_size_t, P],
             "fp8_moe_route_ws_size": [I64, I32, P],
             "fp8_moe_route_backward": [P, I64, I32, I64, INT, I32, I32, P, P, P, P, P, P, P, I64, P],
+            "fp8_moe_route_grouped": [P, I64, I32, I64, INT, I32, INT, P, I32, I32, INT, I32, F32, P, P, P, P, P, P, P, P, P,
+                                      P, ctypes.c_size_t, P],
+            "fp8_moe_route_grouped_backward": [P, I64, I32, I64, INT, I32, INT, I32, F32, P, P, P, P, P, P, I64, P],
+            "fp8_moe_bias_update": [P, P, I32, F32, P],
             "fp8_block_norm": [I64, I64, P, I64, P, I64, INT, P, I64, I64, F32, P, P, INT, F32, P, I64, P, I64, P,
                                I64, P, I64, I64, P],
             "fp8_block_norm_backward": [I64, I64, P, I64, INT, P, I64, P, I64, INT, P, I64, P, I64, I64, F32, P, P,
@@ -303,6 +310,29 @@ def fp8_moe_route_backward(logits, T, E, ld, type_, k, renorm, experts, weights,
     st = load().fp8_moe_route_backward(_p(logits), T, E, ld, type_, k, renorm, _p(experts), _p(weights), _p(counts),
                                        _p(lse), _p(dweights), _p(dloss), _p(dlogits), ld_d, _stream(stream))
     return _check("fp8_moe_route_backward", st, raise_on_error)
+
+
+def fp8_moe_route_grouped(logits, T, E, ld, type_, k, score, bias, groups, keep_groups, group_score, renorm, scale, mask,
+                          experts, weights, counts, offsets, row_token, token_rows, total, loss, ws, ws_bytes,
+                          stream=None, raise_on_error=True):
+    st = load().fp8_moe_route_grouped(_p(logits), T, E, ld, type_, k, score, _p(bias), groups, keep_groups, group_score,
+                                      renorm, scale, _p(mask), _p(experts), _p(weights), _p(counts), _p(offsets),
+                                      _p(row_token), _p(token_rows), _p(total), _p(loss), _p(ws), ws_bytes,
+                                      _stream(stream))
+    return _check("fp8_moe_route_grouped", st, raise_on_error)
+
+
+def fp8_moe_route_grouped_backward(logits, T, E, ld, type_, k, score, renorm, scale, experts, counts, total, dweights,
+                                   dloss, dlogits, ld_d, stream=None, raise_on_error=True):
+    st = load().fp8_moe_route_grouped_backward(_p(logits), T, E, ld, type_, k, score, renorm, scale, _p(experts),
+                                               _p(counts), _p(total), _p(dweights), _p(dloss), _p(dlogits), ld_d,
+                                               _stream(stream))
+    return _check("fp8_moe_route_grouped_backward", st, raise_on_error)
+
+
+def fp8_moe_bias_update(bias, counts, E, rate, stream=None, raise_on_error=True):
+    st = load().fp8_moe_bias_update(_p(bias), _p(counts), E, rate, _stream(stream))
+    return _check("fp8_moe_bias_update", st, raise_on_error)
 
 
 def fp8_block_norm(rows, cols, x, ld_x, residual, ld_r, stream_type, gate, ld_gate, rows_per_gate, scale, w_post,
@@ -629,9 +659,10 @@ def moe_forward(x, qgu, sgu, qdt, sdt, offsets, row_token, token_rows, weights, 
 
 
 def moe_forward_routed(codes, logits, top_k, qgu, sgu, qdt, sdt, *, renorm=True, mask=None,
-                       out_dtype=torch.bfloat16):
-    """One block-wise FP8 MoE layer from router logits [T, G]: moe_route, the
-    experts on the activation's codes, the combine.  codes = (q [T, H] with
+                       out_dtype=torch.bfloat16, router: Optional[dict] = None):
+    """One block-wise FP8 MoE layer from router logits [T, G]: moe_route (or, with
+    `router`, moe_route_grouped with those options), the experts on the
+    activation's codes, the combine.  codes = (q [T, H] with
     unit column stride, s [T, H/128]) as quant_rowblock or block_norm give
     them; weights as in moe_forward.  Masked tokens reach no expert and get zeros.  Returns (out
     [T, H], routing, y): y is the experts' output, which
@@ -647,7 +678,10 @@ def moe_forward_routed(codes, logits, top_k, qgu, sgu, qdt, sdt, *, renorm=True,
     if sx.dtype is not _F32 or sx.shape != (T, (H + 127) // 128) or sx.get_device() != _device():
         raise ValueError("scales of the codes: float32 [%d, %d] on cuda:%d expected, got %s %s on %s"
                          % (T, (H + 127) // 128, _device(), sx.dtype, tuple(sx.shape), sx.device))
-    r = moe_route(logits, top_k, renorm=renorm, mask=mask)
+    if router is None:
+        r = moe_route(logits, top_k, renorm=renorm, mask=mask)
+    else:
+        r = moe_route_grouped(logits, top_k, renorm=renorm, mask=mask, **router)
     y = _moe_experts(qx, sx, T, qgu, sgu, qdt, sdt, r.offsets, r.row_token)
     out = torch.empty((T, H), dtype=out_dtype, device=qx.device)
     fp8_moe_combine_routed(y, T * top_k, H, H, r.token_rows, r.weights, T, top_k, out, H, _otype(out_dtype))
@@ -851,6 +885,22 @@ class Routing(NamedTuple):
     ws: Optional[torch.Tensor]
 
 
+def _routing(logits, T, E, tk, dev, out):
+    """(Routing, pointers of its tensors in the entry points' order, workspace and
+    its size behind them)."""
+    if out is None:
+        need = fp8_moe_route_ws_size(T, E)
+        e = lambda *shape, dt=_I32: torch.empty(shape, dtype=dt, device=logits.device)
+        out = Routing(e(*tk), e(*tk, dt=_F32), e(E + 1), e(E + 1), e(T * tk[1]), e(*tk), e(T, dt=_F32), e(2, dt=_F32),
+                      e(need, dt=torch.uint8) if need else None)
+    experts, weights, counts, offsets, row_token, token_rows, lse, loss, ws = out
+    return out, (_arr("out.experts", experts, tk, dev, _I32), _arr("out.weights", weights, tk, dev, _F32),
+                 _arr("out.counts", counts, (E + 1,), dev, _I32), _arr("out.offsets", offsets, (E + 1,), dev, _I32),
+                 _arr("out.row_token", row_token, (T * tk[1],), dev, _I32),
+                 _arr("out.token_rows", token_rows, tk, dev, _I32), _arr("out.lse", lse, (T,), dev, _F32),
+                 _arr("out.loss", loss, (2,), dev, _F32), *_workspace(ws, dev))
+
+
 def moe_route(logits, top_k, *, renorm=True, mask=None, out: Optional[Routing] = None) -> Routing:
     """Top-k routing of router logits [T, E] (bf16 or fp32): experts, weights,
     counts, the expert-sorted row maps of moe_forward and the grouped GEMMs,
@@ -861,23 +911,79 @@ def moe_route(logits, top_k, *, renorm=True, mask=None, out: Optional[Routing] =
     dev, tk = _device(), (T, top_k)
     zp, ld = _mat("logits", logits, T, E, dev, _BF, _F32)
     mp = None if mask is None else _arr("mask", mask, (T,), dev, mask.dtype if mask.dtype is torch.bool else torch.uint8)
-    if out is None:
-        need = fp8_moe_route_ws_size(T, E)
-        e = lambda *shape, dt=_I32: torch.empty(shape, dtype=dt, device=logits.device)
-        out = Routing(e(*tk), e(*tk, dt=_F32), e(E + 1), e(E + 1), e(T * top_k), e(*tk), e(T, dt=_F32), e(2, dt=_F32),
-                      e(need, dt=torch.uint8) if need else None)
-    experts, weights, counts, offsets, row_token, token_rows, lse, loss, ws = out
-    wsp, wsn = _workspace(ws, dev)
-    st = load().fp8_moe_route(zp, T, E, ld, _OTYPES[logits.dtype], top_k, 1 if renorm else 0, mp,
-                              _arr("out.experts", experts, tk, dev, _I32), _arr("out.weights", weights, tk, dev, _F32),
-                              _arr("out.counts", counts, (E + 1,), dev, _I32),
-                              _arr("out.offsets", offsets, (E + 1,), dev, _I32),
-                              _arr("out.row_token", row_token, (T * top_k,), dev, _I32),
-                              _arr("out.token_rows", token_rows, tk, dev, _I32), _arr("out.lse", lse, (T,), dev, _F32),
-                              _arr("out.loss", loss, (2,), dev, _F32), wsp, wsn, _stream())
+    out, ptrs = _routing(logits, T, E, tk, dev, out)
+    st = load().fp8_moe_route(zp, T, E, ld, _OTYPES[logits.dtype], top_k, 1 if renorm else 0, mp, *ptrs, _stream())
     if st:
         _check("fp8_moe_route", st)
     return out
+
+
+_SCORES = {"softmax": SCORE_SOFTMAX, "sigmoid": SCORE_SIGMOID}
+_GROUP_SCORES = {"max": GROUP_MAX, "top2": GROUP_TOP2}
+
+
+def _choice(name, value, choices):
+    c = choices.get(value)
+    if c is None:
+        raise ValueError("%s: one of %s expected, got %r" % (name, ", ".join(choices), value))
+    return c
+
+
+def moe_route_grouped(logits, top_k, *, score="sigmoid", bias=None, groups=1, keep_groups=None, group_score="top2",
+                      renorm=True, scale=1.0, mask=None, out: Optional[Routing] = None) -> Routing:
+    """Routing of logits [T, E] (bf16 or fp32) by softmax or sigmoid scores: the
+    top_k experts by score + bias (fp32 [E]) within the keep_groups best of
+    `groups` runs of experts (all of them by default), by the largest value of a
+    group ("max") or the sum of its two largest ("top2"); weights from the scores
+    alone, times scale (see fp8_moe_route_grouped).  Routing's lse holds the
+    scores' total; mask and `out` as in moe_route."""
+    T, E = logits.shape
+    dev, tk = _device(), (T, top_k)
+    zp, ld = _mat("logits", logits, T, E, dev, _BF, _F32)
+    mp = None if mask is None else _arr("mask", mask, (T,), dev, mask.dtype if mask.dtype is torch.bool else torch.uint8)
+    bp = _arr("bias", bias, (E,), dev, _F32)
+    out, ptrs = _routing(logits, T, E, tk, dev, out)
+    st = load().fp8_moe_route_grouped(zp, T, E, ld, _OTYPES[logits.dtype], top_k, _choice("score", score, _SCORES), bp,
+                                      groups, groups if keep_groups is None else keep_groups,
+                                      _choice("group_score", group_score, _GROUP_SCORES), 1 if renorm else 0, scale, mp,
+                                      *ptrs, _stream())
+    if st:
+        _check("fp8_moe_route_grouped", st)
+    return out
+
+
+def moe_route_grouped_backward(logits, experts, counts, total, *, dweights=None, dloss=None, score="sigmoid",
+                               renorm=True, scale=1.0, out=None):
+    """dlogits [T, E] (the logits' type) of sum(weights * dweights) + dloss . loss,
+    from moe_route_grouped's outputs (total: its lse; see
+    fp8_moe_route_grouped_backward)."""
+    T, E = logits.shape
+    dev, k, dt = _device(), experts.shape[1], logits.dtype
+    zp, ld = _mat("logits", logits, T, E, dev, _BF, _F32)
+    if out is None:
+        out = torch.empty((T, E), dtype=dt, device=logits.device)
+    op, ld_d = _mat("out", out, T, E, dev, dt)
+    st = load().fp8_moe_route_grouped_backward(zp, T, E, ld, _OTYPES[dt], k, _choice("score", score, _SCORES),
+                                               1 if renorm else 0, scale, _arr("experts", experts, (T, k), dev, _I32),
+                                               _arr("counts", counts, (E + 1,), dev, _I32),
+                                               _arr("total", total, (T,), dev, _F32),
+                                               _arr("dweights", dweights, (T, k), dev, _F32),
+                                               _arr("dloss", dloss, (2,), dev, _F32), op, ld_d, _stream())
+    if st:
+        _check("fp8_moe_route_grouped_backward", st)
+    return out
+
+
+def moe_bias_update(bias, counts, rate):
+    """bias[e] += rate * sign(mean(counts) - counts[e]), in place: bias fp32 [E],
+    counts int32 [E] or [E + 1] (moe_route_grouped's, whose last entry counts
+    tokens)."""
+    E, dev = bias.shape[0], _device()
+    n = counts.shape[0]
+    if n not in (E, E + 1):
+        raise ValueError("counts: %d or %d numbers expected, got %d" % (E, E + 1, n))
+    fp8_moe_bias_update(_arr("bias", bias, (E,), dev, _F32), _arr("counts", counts, (n,), dev, _I32), E, rate)
+    return bias
 
 
 def moe_route_backward(logits, experts, weights, counts, lse, *, dweights=None, dloss=None, renorm=True, out=None):

@@ -77,6 +77,16 @@ typedef enum {
     FP8BS_BSCALE_ROW128 = 1    /* B scale per row and 128-wide K slice: index (n, k / 128) */
 } fp8bs_bscale;
 
+typedef enum {
+    FP8BS_SCORE_SOFTMAX = 0,   /* router scores: softmax over the experts   */
+    FP8BS_SCORE_SIGMOID = 1    /* a sigmoid per expert                      */
+} fp8bs_score;
+
+typedef enum {
+    FP8BS_GROUP_MAX = 0,       /* a group of experts counts by its largest value        */
+    FP8BS_GROUP_TOP2 = 1       /* ... by the sum of its two largest                     */
+} fp8bs_group_score;
+
 /* ------------------------------------------------------------------------
  * fp8_quant_rowblock -- per-token (1x128) or token-axis (128x1) quantization.
  *
@@ -571,6 +581,66 @@ fp8bs_status fp8_moe_route_backward(const void* logits, int64_t T, int32_t E, in
                                     int32_t renorm, const int32_t* experts, const float* weights,
                                     const int32_t* counts, const float* lse, const float* dweights,
                                     const float* dloss, void* dlogits, int64_t ld_d, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_moe_route_grouped -- fp8_moe_route with scores, a selection bias and groups
+ * of experts: the router of a MoE layer whose load is balanced by a bias that
+ * takes part in the selection alone.
+ *
+ *   s_e = softmax(z)_e or sigmoid(z_e) per `score`;   v_e = s_e + bias_e
+ *   The experts form `groups` runs of E / groups.  A group's value is its largest
+ *   v or the sum of its two largest (of one, where only one can be taken) per
+ *   group_score; the keep_groups largest stay, ties to the lower group.  Of their
+ *   experts the k largest v are taken, in that order, ties to the lower expert.
+ *   weight_j = scale * s_j / (sum of the token's taken s + 1e-20)   (renorm 1)
+ *            = scale * s_j                                          (renorm 0)
+ *   total    = sum_e s_e (sigmoid), log sum_e exp z_e (softmax); -inf for a token
+ *              that is not routed (masked, or with only -inf logits)
+ *   loss[0]  = E * sum_e f_e P_e as in fp8_moe_route, P_e the mean over routed
+ *              tokens of s_e / (sum_e s_e + 1e-20)
+ *   loss[1]  = mean over routed tokens of total^2 (softmax), 0 (sigmoid)
+ *
+ * v is compared as in 64 bits: values that differ by more than a few roundings of
+ * binary64 are taken in their true order.  An expert whose logit or v is -inf is
+ * not taken; NaN counts as the largest (a group's sum with it as infinity) and
+ * makes its token's weights, total and the losses NaN.  A slot that takes no expert has expert -1, weight 0 and row -1.
+ * Everything else (rows, counts, offsets, masks, workspace) is as in
+ * fp8_moe_route; the workspace is that of fp8_moe_route_ws_size.
+ *
+ * bias : nullable fp32 [E].
+ * Requirements: as fp8_moe_route; 1 <= groups <= 64, E % groups == 0,
+ * 1 <= keep_groups <= groups, k <= keep_groups * (E / groups); scale finite.
+ * ------------------------------------------------------------------------ */
+fp8bs_status fp8_moe_route_grouped(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type, int32_t k,
+                                   fp8bs_score score, const float* bias, int32_t groups, int32_t keep_groups,
+                                   fp8bs_group_score group_score, int32_t renorm, float scale, const uint8_t* mask,
+                                   int32_t* experts, float* weights, int32_t* counts, int32_t* offsets,
+                                   int32_t* row_token, int32_t* token_rows, float* total, float* loss, void* ws,
+                                   size_t ws_bytes, hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_moe_route_grouped_backward -- gradient at the logits of
+ *     sum(weights * dweights) + dloss[0] loss[0] + dloss[1] loss[1]
+ * of fp8_moe_route_grouped (the selection and the counts are constants; the bias
+ * has no gradient).  experts, counts, total: its outputs; score, renorm and scale
+ * as there.  A token whose total is -inf gets zeros, whatever its logits.
+ * dweights, dloss, dlogits and requirements: as in fp8_moe_route_backward;
+ * experts are required with dweights, counts with dloss.
+ * ------------------------------------------------------------------------ */
+fp8bs_status fp8_moe_route_grouped_backward(const void* logits, int64_t T, int32_t E, int64_t ld, fp8bs_out type,
+                                            int32_t k, fp8bs_score score, int32_t renorm, float scale,
+                                            const int32_t* experts, const int32_t* counts, const float* total,
+                                            const float* dweights, const float* dloss, void* dlogits, int64_t ld_d,
+                                            hipStream_t stream);
+
+/* ------------------------------------------------------------------------
+ * fp8_moe_bias_update -- one balancing step of the selection bias:
+ *     bias[e] += rate * sign(mean(counts) - counts[e])
+ * (fp32, the comparison in whole numbers).  counts: int32 [E], of one batch or
+ * added up over several (fp8_moe_route_grouped's; its last entry is not read).
+ * Requirements: 1 <= E <= 1024, rate finite; pointers 4-byte aligned.
+ * ------------------------------------------------------------------------ */
+fp8bs_status fp8_moe_bias_update(float* bias, const int32_t* counts, int32_t E, float rate, hipStream_t stream);
 
 /* ------------------------------------------------------------------------
  * fp8_block_norm -- the norm behind a block, its gate and scale, the residual
