@@ -21,6 +21,7 @@
 // a slice ahead of itself: while one half's matrix instructions run, the other
 // half's fragments are read.
 #include <algorithm>
+#include <utility>
 
 #include "device_common.h"
 #include "internal.h"
@@ -30,6 +31,7 @@ namespace fp8bs {
 namespace {
 
 typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 constexpr int BK = 128;                 // K bytes per slice
@@ -52,19 +54,83 @@ __device__ __forceinline__ void lds_write16(uint32_t addr, i32x4 v) {
     *reinterpret_cast<__attribute__((address_space(3))) i32x4*>((uintptr_t)addr) = v;
 }
 
-// Lane l's 16 bytes at base + off land at LDS address dst + 16 l (dst
+// Lane l's 16 bytes at base + off land at LDS address dst + AT + 16 l (dst
 // wave-uniform).  Inline assembly, since the compiler cannot tell which slice a
 // copy writes and would wait for all copies before each LDS read; the kernel
 // waits itself: vmcnt on the issuing wave, then a barrier.
+template <int AT>
 __device__ __forceinline__ void copy16(const void* base, uint32_t off, uint32_t dst) {
-    const uint32_t m0 = __builtin_amdgcn_readfirstlane(dst);
-    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(m0), "v"(off), "s"(base) : "memory", "m0");
+    asm volatile("s_add_u32 m0, %0, %c3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
+                 :: "s"(dst), "v"(off), "s"(base), "n"(AT) : "memory", "scc");
+}
+// The same where `go` (uniform) is not 0.  The branch is the assembly's own: a slice
+// stays one basic block.
+template <int AT>
+__device__ __forceinline__ void copy16_if(uint32_t go, const void* base, uint32_t off, uint32_t dst) {
+    asm volatile("s_cmp_eq_u32 %4, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_add_u32 m0, %0, %c3\n\ts_nop 0\n\t"
+                 "global_load_lds_dwordx4 %1, %2\n.Lskip%=:"
+                 :: "s"(dst), "v"(off), "s"(base), "n"(AT), "s"(go) : "memory", "scc");
+}
+// All but the last N1 + N2 copies of this wave have landed where `one` and `two` are
+// not 0, the last N1 with `one` alone, all without.
+template <int N1, int N2>
+__device__ __forceinline__ void wait_copies(uint32_t one, uint32_t two) {
+    asm volatile("s_cmp_eq_u32 %0, 0\n\ts_cbranch_scc1 .Lall%=\n\ts_cmp_eq_u32 %1, 0\n\ts_cbranch_scc1 .Lone%=\n\t"
+                 "s_waitcnt vmcnt(%c3)\n\ts_branch .Ldone%=\n.Lone%=:\n\ts_waitcnt vmcnt(%c2)\n\ts_branch .Ldone%=\n"
+                 ".Lall%=:\n\ts_waitcnt vmcnt(0)\n.Ldone%=:"
+                 :: "s"(one), "s"(two), "n"(N1), "n"(N1 + N2) : "memory", "scc");
 }
 
 __device__ __forceinline__ i32x4 mfma(i32x4 a, i32x4 b, i32x4 c) {
     return __builtin_amdgcn_mfma_i32_16x16x64_i8(a, b, c, 0, 0, 0);
 }
+
+// A wave's 256 sums in accumulation registers of our own choice, a0 to a255, which
+// take one half of its registers whole.  The compiler is told that they are used
+// (ACC_IN_USE) and has none of its values there: left to allocate the sums itself it
+// copies them between the two halves of the register file, 388 copies beside 128
+// matrix instructions a slice.  Only the functions below touch them; the waits that
+// the compiler adds around matrix instructions are theirs.
+#define FP8BS_ACC_IN_USE() asm volatile("" ::: \
+        "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", "a10", "a11", "a12", "a13", "a14", "a15", \
+        "a16", "a17", "a18", "a19", "a20", "a21", "a22", "a23", "a24", "a25", "a26", "a27", "a28", "a29", "a30", "a31", \
+        "a32", "a33", "a34", "a35", "a36", "a37", "a38", "a39", "a40", "a41", "a42", "a43", "a44", "a45", "a46", "a47", \
+        "a48", "a49", "a50", "a51", "a52", "a53", "a54", "a55", "a56", "a57", "a58", "a59", "a60", "a61", "a62", "a63", \
+        "a64", "a65", "a66", "a67", "a68", "a69", "a70", "a71", "a72", "a73", "a74", "a75", "a76", "a77", "a78", "a79", \
+        "a80", "a81", "a82", "a83", "a84", "a85", "a86", "a87", "a88", "a89", "a90", "a91", "a92", "a93", "a94", "a95", \
+        "a96", "a97", "a98", "a99", "a100", "a101", "a102", "a103", "a104", "a105", "a106", "a107", "a108", "a109", "a110", "a111", \
+        "a112", "a113", "a114", "a115", "a116", "a117", "a118", "a119", "a120", "a121", "a122", "a123", "a124", "a125", "a126", "a127", \
+        "a128", "a129", "a130", "a131", "a132", "a133", "a134", "a135", "a136", "a137", "a138", "a139", "a140", "a141", "a142", "a143", \
+        "a144", "a145", "a146", "a147", "a148", "a149", "a150", "a151", "a152", "a153", "a154", "a155", "a156", "a157", "a158", "a159", \
+        "a160", "a161", "a162", "a163", "a164", "a165", "a166", "a167", "a168", "a169", "a170", "a171", "a172", "a173", "a174", "a175", \
+        "a176", "a177", "a178", "a179", "a180", "a181", "a182", "a183", "a184", "a185", "a186", "a187", "a188", "a189", "a190", "a191", \
+        "a192", "a193", "a194", "a195", "a196", "a197", "a198", "a199", "a200", "a201", "a202", "a203", "a204", "a205", "a206", "a207", \
+        "a208", "a209", "a210", "a211", "a212", "a213", "a214", "a215", "a216", "a217", "a218", "a219", "a220", "a221", "a222", "a223", \
+        "a224", "a225", "a226", "a227", "a228", "a229", "a230", "a231", "a232", "a233", "a234", "a235", "a236", "a237", "a238", "a239", \
+        "a240", "a241", "a242", "a243", "a244", "a245", "a246", "a247", "a248", "a249", "a250", "a251", "a252", "a253", "a254", "a255")
+template <int I>
+__device__ __forceinline__ void acc_mfma(i32x4 a, i32x4 b) {
+    asm volatile("v_mfma_i32_32x32x32_i8 a[%c0:%c1], %2, %3, a[%c0:%c1]" :: "n"(I), "n"(I + 15), "v"(a), "v"(b));
+}
+template <int I>
+__device__ __forceinline__ void acc_zero() {
+    asm volatile("v_accvgpr_write_b32 a[%c0], 0" :: "n"(I));
+}
+template <int I>
+__device__ __forceinline__ int acc_read() {
+    int v;
+    asm volatile("v_accvgpr_read_b32 %0, a[%c1]" : "=v"(v) : "n"(I));
+    return v;
+}
+// Until the last matrix instruction's sums are there.
+__device__ __forceinline__ void acc_wait() { asm volatile("s_nop 15\n\ts_nop 15" ::: "memory"); }
+
+template <int N, class F, int... I>
+__device__ __forceinline__ void unrolled(F f, std::integer_sequence<int, I...>) {
+    (f(std::integral_constant<int, I>{}), ...);
+}
+template <int N, class F>
+__device__ __forceinline__ void unrolled(F f) { unrolled<N>(f, std::make_integer_sequence<int, N>{}); }
 
 // Four outputs of one row at columns n .. n + 3 (n < N, N % 8 == 0).
 template <bool OUT32>
@@ -87,17 +153,16 @@ __device__ __forceinline__ int group_tiles(const I8Args& p, int g) {
 }
 
 template <int TM, int TN, bool GROUPED, bool GATHER, bool OUT32>
-__global__ void __launch_bounds__(256, (TM * TN > 16 ? 1 : 2)) k_i8_tile(I8Args p) {
-    constexpr int BM = 32 * TM, BN = 32 * TN;
-    constexpr int kABytes = BM * BK, kBuf = (BM + BN) * BK;       // a slice: activations, then weights
-    constexpr int kCopyA = BM / 32, kCopyB = BN / 32;             // copies (8 rows each) per wave
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kBuf];
-    __shared__ int s_found[4];
+__global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p) {
+    constexpr int BM = 64 * TM, BN = 64 * TN;
+    constexpr int kABytes = BM * BK, kBBytes = BN * BK;
+    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kABytes + 3 * kBBytes];
+    int* s_found = reinterpret_cast<int*>(smem);    // before the first copy
 
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wn = wave & 1, wm = wave >> 1;
-    const int q = lane >> 4, r16 = lane & 15;
+    const int hi = lane >> 5, r32 = lane & 31;
 
     // ------------------------------------------------------------ which tile
     Tile t;
@@ -144,114 +209,250 @@ __global__ void __launch_bounds__(256, (TM * TN > 16 ? 1 : 2)) k_i8_tile(I8Args 
         t.n0 = __builtin_amdgcn_readfirstlane(s_found[3]) * BN;
         t.b = p.b + (int64_t)g * p.b_sg;
         t.sb = p.sb + (int64_t)g * p.sb_sg;
+        __syncthreads();                            // s_found's place is copied to
     }
 
+    // The output's scales, loaded ahead of everything: lane l has row l % 32 of each
+    // activation tile and two of the wave's columns.
+    const int mw = t.m0 + wm * 32 * TM + r32, nw = t.n0 + wn * 32 * TN;
+    float sam[TM], sbv[TN / 2];
+#pragma unroll
+    for (int j = 0; j < TM; ++j) {
+        int m = min(mw + 32 * j, t.m1 - 1);
+        if (GATHER) m = p.a_rows[m];
+        sam[j] = p.sa[m];
+    }
+#pragma unroll
+    for (int i = 0; i < TN / 2; ++i) sbv[i] = t.sb[min(nw + 64 * i + lane, p.N - 1)];
+
     // ---------------------------------------------------------------- copies
-    // Copy j of a wave brings tile rows 8 (wave + 4 j) + lane / 8; rows past the
-    // tile repeat its last row, their outputs are not stored.
-    uint32_t offA[kCopyA], offB[kCopyB];
+    // Copy j of a wave brings rows 8 (wave + 4 j) + lane / 8 of a tile; rows past it
+    // repeat its last row, their outputs are not stored.
+    uint32_t offA[2 * TM], offB[2 * TN];
     const int sub = lane >> 3, chunk = (lane & 7) ^ sub;
     const int ntail = p.K % BK / 16;                // chunks of the last slice, 0: all eight
     const int nk = (p.K + BK - 1) / BK;
 #pragma unroll
-    for (int j = 0; j < kCopyA; ++j) {
+    for (int j = 0; j < 2 * TM; ++j) {
         int m = min(t.m0 + 8 * (wave + 4 * j) + sub, t.m1 - 1);
         if (GATHER) m = p.a_rows[m];
         offA[j] = (uint32_t)((int64_t)m * p.lda + chunk * 16);
     }
 #pragma unroll
-    for (int j = 0; j < kCopyB; ++j)
+    for (int j = 0; j < 2 * TN; ++j)
         offB[j] = (uint32_t)((int64_t)min(t.n0 + 8 * (wave + 4 * j) + sub, p.N - 1) * p.ldb + chunk * 16);
+    // activations of slice kb in one of two buffers, weights in one of three
     const uint32_t lds0 = lds_addr(smem);
-    auto copies = [&](int kb) {
-        const uint32_t dst = lds0 + (kb & 1) * kBuf;
-        // the last slice's missing chunks are read from its first one (in bounds)
-        // and cleared in LDS
-        const uint32_t back = kb == nk - 1 && ntail && chunk >= ntail ? (uint32_t)chunk * 16 : 0u;
-#pragma unroll
-        for (int j = 0; j < kCopyA; ++j)
-            copy16(p.a + (int64_t)kb * BK, offA[j] - back, dst + (wave + 4 * j) * 8 * BK);
-#pragma unroll
-        for (int j = 0; j < kCopyB; ++j)
-            copy16(t.b + (int64_t)kb * BK, offB[j] - back, dst + kABytes + (wave + 4 * j) * 8 * BK);
-    };
-    // slice kb has landed for every wave, and every wave has read slice kb - 1
-    auto arrive = [&](int kb) {
-        asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    auto bufA = [&](int kb) { return lds0 + (uint32_t)(kb & 1) * kABytes; };
+    auto bufB = [&](int kb) { return lds0 + 2 * kABytes + (uint32_t)(kb % 3) * kBBytes; };
+    // The last slice's missing chunks are read from its first one (in bounds), by
+    // offsets moved back before its copies, and cleared in LDS.
+    const uint32_t back = ntail && chunk >= ntail ? (uint32_t)chunk * 16 : 0u;
+    const uint32_t mine = (uint32_t)wave * 8 * BK;  // a wave's first copy in a buffer
+    auto copies = [&](int kb, bool acts, bool weights) {
         if (kb == nk - 1 && ntail) {
-            // zeros in the activations are enough: a zero times any code is zero
-            for (int i = threadIdx.x; i < BM * 8; i += 256) {
-                const int r = i >> 3, c = i & 7;
-                if (c >= ntail) lds_write16(lds0 + (kb & 1) * kBuf + r * BK + ((c ^ (r & 7)) << 4), i32x4{0, 0, 0, 0});
-            }
-            asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+#pragma unroll
+            for (int j = 0; j < 2 * TM; ++j) offA[j] -= acts ? back : 0u;
+#pragma unroll
+            for (int j = 0; j < 2 * TN; ++j) offB[j] -= weights ? back : 0u;
         }
+        unrolled<2 * TM>([&](auto j) {
+            constexpr int J = decltype(j)::value;
+            if (acts) copy16<32 * J * BK>(p.a + (int64_t)kb * BK, offA[J], bufA(kb) + mine);
+        });
+        unrolled<2 * TN>([&](auto j) {
+            constexpr int J = decltype(j)::value;
+            if (weights) copy16<32 * J * BK>(t.b + (int64_t)kb * BK, offB[J], bufB(kb) + mine);
+        });
     };
-    // Fragments of half h of slice kb: chunk q + 4 h of each row.
-    auto read_half = [&](int kb, int h, i32x4 (&fa)[TM], i32x4 (&fb)[TN]) {
-        const uint32_t at = lds0 + (kb & 1) * kBuf + r16 * BK + (((q + 4 * h) ^ (r16 & 7)) << 4);
-        uint32_t aa = at + wm * 16 * TM * BK, bb = at + kABytes + wn * 16 * TN * BK;
-        asm volatile("" : "+v"(aa), "+v"(bb));      // one address each, the tiles as offsets
+    // zeros in the last slice's missing activations are enough: zero times any code
+    auto clear = [&](int kb) {
+        for (int i = threadIdx.x; i < BM * 8; i += 256) {
+            const int r = i >> 3, c = i & 7;
+            if (c >= ntail) lds_write16(bufA(kb) + r * BK + ((c ^ (r & 7)) << 4), i32x4{0, 0, 0, 0});
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+    };
+    // This lane's addresses of a wave's first 32 rows: the 16 bytes of matrix
+    // instruction u (32 of the slice's 128) are chunk 2 u + lane / 32; later rows are
+    // constant offsets.
+    struct Frag { uint32_t at[4]; };
+    auto frag = [&](uint32_t rows) {
+        const uint32_t at = rows + r32 * BK;
+        Frag f;
 #pragma unroll
-        for (int i = 0; i < TN; ++i) fb[i] = lds_read16(bb + i * 16 * BK);
-#pragma unroll
-        for (int i = 0; i < TM; ++i) fa[i] = lds_read16(aa + i * 16 * BK);
+        for (int u = 0; u < 4; ++u) {
+            f.at[u] = at + (((2 * u + hi) ^ (r32 & 7)) << 4);
+            asm volatile("" : "+v"(f.at[u]));
+        }
+        return f;
     };
 
-    i32x4 acc[TN][TM];
+    // sums of weight tile i and activation tile j (32 x 32): accumulation registers
+    // from 16 (i TM + j) on, or the compiler's where two workgroups share a compute unit
+    constexpr bool kAcc = TM * TN > 4;
+    i32x16 own[kAcc ? 1 : TN * TM];
+    if constexpr (kAcc) {
+        FP8BS_ACC_IN_USE();
+        unrolled<16 * TN * TM>([](auto i) { acc_zero<decltype(i)::value>(); });
+    } else {
 #pragma unroll
-    for (int i = 0; i < TN; ++i)
+        for (int i = 0; i < TN * TM; ++i) own[i] = i32x16{};
+    }
+    auto add = [&](auto at, i32x4 b, i32x4 a) {
+        constexpr int I = decltype(at)::value;
+        if constexpr (kAcc) acc_mfma<16 * I>(b, a);
+        else own[I] = __builtin_amdgcn_mfma_i32_32x32x32_i8(b, a, own[I], 0, 0, 0);
+    };
+
+    // One slice, in 2 TN steps of half a weight tile each (64 of its bytes): its
+    // activations are in `fa`, the first step's weights in fb[0].  Meanwhile the next
+    // slice's activations go to `na` (steps before kMid), the next step's weights to
+    // the other fb, and the copies of the weights two and the activations three slices
+    // ahead to LDS.  At kMid every wave has read the next activations,
+    // so their buffer is free; before the last step the next slice's weights and the
+    // activations after it have landed.
+    // A wave alone on its SIMD issues an instruction every four cycles or so and a
+    // matrix instruction runs for 32: whatever else there is stands between matrix
+    // instructions, one thing after each (in one place per step it left the matrix
+    // unit idle for a third of the time: 3240 cycles a slice, not 2048).
+    constexpr int kSteps = 2 * TN, kMid = TN, kReads = 4, kSpan = 2 * TM;
+    constexpr int kStepB = (2 * TN + kMid - 1) / kMid, kStepA = (2 * TM + kSteps - kMid - 2) / (kSteps - kMid - 1);
+    static_assert(4 * TM <= kReads * kMid, "the next activations are read before kMid");
+    i32x4 fb[2][2];
+    uint32_t wb = 0, wb1 = 1, wb2 = 2;              // weight buffers of this slice and the next two
+    auto slice = [&](int kb, const i32x4 (&fa)[4][TM], i32x4 (&na)[4][TM]) {
+        const uint32_t two = __builtin_amdgcn_readfirstlane(max(nk - kb - 2, 0)), three = __builtin_amdgcn_readfirstlane(max(nk - kb - 3, 0));
+        if (ntail) {
+            if (kb + 2 == nk) clear(kb + 1);
+            if (kb + 3 == nk) {
 #pragma unroll
-        for (int j = 0; j < TM; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-    auto multiply = [&](const i32x4 (&fa)[TM], const i32x4 (&fb)[TN]) {
+                for (int j = 0; j < 2 * TN; ++j) offB[j] -= back;
+            }
+            if (kb + 4 == nk) {
 #pragma unroll
-        for (int i = 0; i < TN; ++i)
-#pragma unroll
-            for (int j = 0; j < TM; ++j) acc[i][j] = mfma(fb[i], fa[j], acc[i][j]);
+                for (int j = 0; j < 2 * TM; ++j) offA[j] -= back;
+            }
+        }
+        const uint32_t rowsB = lds0 + 2 * kABytes + wn * 32 * TN * BK;
+        const Frag ha = frag(bufA(kb + 1) + wm * 32 * TM * BK), hb = frag(rowsB + wb * kBBytes);
+        const Frag hn = frag(rowsB + wb1 * kBBytes);
+        const uint8_t* baseA = p.a + (int64_t)(kb + 3) * BK;
+        const uint8_t* baseB = t.b + (int64_t)(kb + 2) * BK;
+        const uint32_t dstA = bufA(kb + 1) + mine, dstB = lds0 + 2 * kABytes + wb2 * kBBytes + mine;
+        unrolled<kSteps>([&](auto step) {
+            constexpr int i = decltype(step)::value;
+            if constexpr (i == kMid) asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            // copies of the next weights and of the activations after them are older
+            // than the last 2 (TM + TN) or fewer
+            if constexpr (i == kSteps - 1) {
+                wait_copies<2 * TN, 2 * TM>(two, three);
+                asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+            }
+            i32x4 (&nb)[2] = fb[(i + 1) & 1];
+            unrolled<kSpan>([&](auto vv) {
+                constexpr int v = decltype(vv)::value, u = v / TM;
+                add(std::integral_constant<int, i / 2 * TM + v % TM>{}, fb[i & 1][u], fa[2 * (i % 2) + u][v % TM]);
+                if constexpr (v < 2) {
+                    // (after the last slice: whatever is there, and not used)
+                    if constexpr (i < kSteps - 1) nb[v] = lds_read16(hb.at[2 * ((i + 1) % 2) + v] + (i + 1) / 2 * 32 * BK);
+                    else nb[v] = lds_read16(hn.at[v]);
+                }
+                constexpr int w = v - 2 + 2 * (kSpan == 4);       // spans of four: reads and copies share the places
+                if constexpr (w >= 0 && i < kMid) {
+                    constexpr int n = kSpan == 4 ? 1 : kReads / 2;    // next activations, in two places
+                    if constexpr (w < kReads / n) {
+                        unrolled<n>([&](auto x) {
+                            constexpr int r = i * kReads + w * n + decltype(x)::value;
+                            if constexpr (r < 4 * TM) na[r / TM][r % TM] = lds_read16(ha.at[r / TM] + (r % TM) * 32 * BK);
+                        });
+                    }
+                }
+                constexpr int c = kSpan - 1 - v;    // copies from the span's end on
+                if constexpr (i < kMid && c < kStepB) {
+                    constexpr int j = i * kStepB + c;
+                    if constexpr (j < 2 * TN) copy16_if<32 * j * BK>(two, baseB, offB[j], dstB);
+                }
+                if constexpr (i >= kMid && i < kSteps - 1 && c < kStepA) {
+                    constexpr int j = (i - kMid) * kStepA + c;
+                    if constexpr (j < 2 * TM) copy16_if<32 * j * BK>(three, baseA, offA[j], dstA);
+                }
+                __builtin_amdgcn_sched_barrier(0);
+            });
+        });
+        const uint32_t w = wb;
+        wb = wb1;
+        wb1 = wb2;
+        wb2 = w;
     };
 
     if (nk > 0) {
-        i32x4 fa0[TM], fb0[TN], fa1[TM], fb1[TN];
-        copies(0);
-        arrive(0);
-        if (nk > 1) copies(1);
-        read_half(0, 0, fa0, fb0);
-        for (int kb = 0; kb < nk; ++kb) {
-            read_half(kb, 1, fa1, fb1);
-            multiply(fa0, fb0);
-            if (kb + 1 < nk) {
-                arrive(kb + 1);
-                if (kb + 2 < nk) copies(kb + 2);
-                read_half(kb + 1, 0, fa0, fb0);
-            }
-            multiply(fa1, fb1);
+        i32x4 fa[4][TM], na[4][TM];
+        copies(0, true, true);
+        if (nk > 1) {
+            copies(1, true, true);
+            asm volatile("s_waitcnt vmcnt(%c0)\n\ts_barrier" :: "n"(2 * TN) : "memory");
+        } else {
+            asm volatile("s_waitcnt vmcnt(0)\n\ts_barrier" ::: "memory");
+        }
+        if (ntail && nk == 1) clear(0);
+        const Frag ha = frag(bufA(0) + wm * 32 * TM * BK), hb = frag(bufB(0) + wn * 32 * TN * BK);
+#pragma unroll
+        for (int u = 0; u < 4; ++u) {
+            if (u < 2) fb[0][u] = lds_read16(hb.at[u]);
+#pragma unroll
+            for (int j = 0; j < TM; ++j) fa[u][j] = lds_read16(ha.at[u] + j * 32 * BK);
+        }
+        asm volatile("s_waitcnt lgkmcnt(0)\n\ts_barrier" ::: "memory");
+        if (nk > 2) copies(2, true, false);
+        for (int kb = 0;; kb += 2) {
+            slice(kb, fa, na);
+            if (kb + 1 >= nk) break;
+            slice(kb + 1, na, fa);
+            if (kb + 2 >= nk) break;
         }
     }
 
     // -------------------------------------------------------------- epilogue
-    const int nw = t.n0 + wn * 16 * TN + 4 * q, mw = t.m0 + wm * 16 * TM + r16;
-    float sam[TM];
+    // Sum r of a 32 x 32 tile is column 8 (r / 4) + 4 (lane / 32) + r % 4.  The
+    // columns' scales go through LDS, 32 TN floats of the wave's own (the last barrier
+    // left every buffer free); of two runs of eight bf16 columns the lanes' halves
+    // trade their halves, so that each lane stores sixteen bytes of its row.
+    float* sbl = reinterpret_cast<float*>(smem) + wave * 32 * TN;
 #pragma unroll
-    for (int j = 0; j < TM; ++j) {
-        int m = min(mw + 16 * j, t.m1 - 1);
-        if (GATHER) m = p.a_rows[m];
-        sam[j] = p.sa[m];
-    }
-#pragma unroll
-    for (int i = 0; i < TN; ++i) {
-        const int n = nw + 16 * i;
-        float sbn[4];
-#pragma unroll
-        for (int r = 0; r < 4; ++r) sbn[r] = t.sb[min(n + r, p.N - 1)];
-#pragma unroll
-        for (int j = 0; j < TM; ++j) {
-            const int m = mw + 16 * j;
-            float v[4];
-#pragma unroll
-            for (int r = 0; r < 4; ++r) v[r] = (float)acc[i][j][r] * sam[j] * sbn[r];
-            if (m < t.m1 && n < p.N) store4<OUT32>(p.c, (int64_t)m * p.ldc + n, v);
-        }
-    }
+    for (int i = 0; i < TN / 2; ++i) sbl[64 * i + lane] = sbv[i];
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+    if constexpr (kAcc) acc_wait();
+    unrolled<2 * TN>([&](auto step) {
+        constexpr int i = decltype(step)::value / 2, g = decltype(step)::value % 2 * 2;     // runs g, g + 1 of tile i
+        const float4 s0 = *reinterpret_cast<const float4*>(sbl + 32 * i + 8 * g + 4 * hi);
+        const float4 s1 = *reinterpret_cast<const float4*>(sbl + 32 * i + 8 * g + 8 + 4 * hi);
+        const float sbn[8] = {s0.x, s0.y, s0.z, s0.w, s1.x, s1.y, s1.z, s1.w};
+        unrolled<TM>([&](auto col) {
+            constexpr int j = decltype(col)::value, at = i * TM + j;
+            const int m = mw + 32 * j, n = nw + 32 * i + 8 * g;
+            float v[8];
+            unrolled<8>([&](auto rr) {
+                constexpr int r = decltype(rr)::value;
+                int sum;
+                if constexpr (kAcc) sum = acc_read<16 * at + 4 * g + r>();
+                else sum = own[at][4 * g + r];
+                v[r] = (float)sum * sam[j] * sbn[r];
+            });
+            if constexpr (OUT32) {
+                float* c = static_cast<float*>(p.c) + (int64_t)m * p.ldc + n + 4 * hi;
+                if (m < t.m1 && n < p.N) *reinterpret_cast<float4*>(c) = make_float4(v[0], v[1], v[2], v[3]);
+                if (m < t.m1 && n + 8 < p.N) *reinterpret_cast<float4*>(c + 8) = make_float4(v[4], v[5], v[6], v[7]);
+            } else {
+                const auto lo = __builtin_amdgcn_permlane32_swap(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[4], v[5]), false, false);
+                const auto up = __builtin_amdgcn_permlane32_swap(pack_bf16x2(v[2], v[3]), pack_bf16x2(v[6], v[7]), false, false);
+                if (m < t.m1 && n + 8 * hi < p.N)
+                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(p.c) + (int64_t)m * p.ldc + n + 8 * hi) =
+                        make_uint4(lo[0], up[0], lo[1], up[1]);
+            }
+        });
+    });
 }
 
 // Few rows (decode): the weights are read once, straight into registers, by waves
@@ -337,7 +538,7 @@ __global__ void __launch_bounds__(64 * W) k_i8_stream(I8Args p) {
 
 template <int TM, int TN, bool GROUPED, bool GATHER>
 hipError_t tile(const I8Args& p, bool out32, hipStream_t st) {
-    constexpr int BM = 32 * TM, BN = 32 * TN;
+    constexpr int BM = 64 * TM, BN = 64 * TN;
     const int64_t ntn = (p.N + BN - 1) / BN;
     int64_t blocks = ((int64_t)p.M + BM - 1) / BM * ntn;
     if (GROUPED) blocks = (((int64_t)p.M / BM + std::min<int64_t>(p.G, p.M)) * ntn + 7) / 8 * 8;   // at most this many tiles
@@ -361,8 +562,8 @@ hipError_t launch(const I8Args& p, bool out32, hipStream_t st) {
     if (rows <= 16) return stream<1, 1, 8, GROUPED, GATHER>(p, out32, st);
     if (rows <= 64) return stream<4, 1, 8, GROUPED, GATHER>(p, out32, st);
     const int64_t big = ((int64_t)p.M + 255) / 256 * ((p.N + 255) / 256);
-    if (big >= 128) return tile<8, 8, GROUPED, GATHER>(p, out32, st);
-    return tile<4, 4, GROUPED, GATHER>(p, out32, st);
+    if (big >= 128) return tile<4, 4, GROUPED, GATHER>(p, out32, st);
+    return tile<2, 2, GROUPED, GATHER>(p, out32, st);
 }
 
 }  // namespace
