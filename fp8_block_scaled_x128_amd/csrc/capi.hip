@@ -1161,11 +1161,11 @@ fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* 
     uint8_t* qx = static_cast<uint8_t*>(ws) + i8_linear_scales(rows);
     if ((v = i8_operand_args(rows, K, reinterpret_cast<const int8_t*>(qx), K, sx)) != FP8BS_OK) return v;
     if ((v = check_device()) != FP8BS_OK) return v;
-    const hipError_t e = launch_i8_quant_rows(x, rows, cols, ld_x, qx, K, sx, stream);
-    if (e != hipSuccess) return launched(e, "int8_linear");
     const I8GemmArgs g{rows, N, K, qx, K, sx, reinterpret_cast<const uint8_t*>(w), ld_w, 0, sw, 0, y, ld_y,
                        out == FP8BS_OUT_FP32, 0, nullptr, nullptr};
-    return launched(launch_i8_gemm(g, stream), "int8_linear");
+    if (i8_linear_fused(rows, cols)) return launched(launch_i8_linear_fused(g, x, ld_x, cols, stream), "int8_linear");
+    const hipError_t e = launch_i8_quant_rows(x, rows, cols, ld_x, qx, K, sx, stream);
+    return launched(e != hipSuccess ? e : launch_i8_gemm(g, stream), "int8_linear");
 }
 
 fp8bs_status int8_grouped_gemm(int64_t total_rows, int64_t N, int64_t K, int32_t G, const int32_t* offsets,

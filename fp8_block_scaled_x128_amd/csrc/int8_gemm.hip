@@ -23,7 +23,7 @@
 #include <algorithm>
 #include <utility>
 
-#include "device_common.h"
+#include "int8_common.h"
 #include "internal.h"
 #include "reduce.h"
 
@@ -456,17 +456,52 @@ __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p
 }
 
 // Few rows (decode): the weights are read once, straight into registers, by waves
-// that split K and meet in LDS.  A workgroup takes 16 NT weight rows; a wave
-// takes every W-th run of 64 bytes of K and feeds it to NT x MT matrix
-// instructions.  Grouped: grid row y is a group; its rows go in passes of 16 MT.
-template <int MT, int NT, int W, bool GROUPED, bool GATHER, bool OUT32>
+// that split K and meet in LDS.  A workgroup takes 16 weight rows; a wave takes every
+// W-th run of 128 bytes of K, a whole cache line of each row, and feeds it to two
+// matrix instructions per 16 activation rows.  Lane quarter q has bytes 32 q to
+// 32 q + 31 of a run from both operands: any order of K will do for a sum of integers.
+constexpr int kRun = 128;
+
+struct Run {
+    i32x4 lo, hi;
+};
+// A lane's 32 bytes at `row` + k; zeros past the end (K % 16 == 0), without a read.
+__device__ __forceinline__ Run load_run(const uint8_t* row, int k, int K, int q) {
+    const i32x4 zero = {0, 0, 0, 0};
+    const int at = k + 32 * q;
+    return {at < K ? *reinterpret_cast<const i32x4*>(row + at) : zero,
+            at + 16 < K ? *reinterpret_cast<const i32x4*>(row + at + 16) : zero};
+}
+
+// The waves' partial sums of MT tiles, added in LDS, scaled and stored.
+template <int MT, int W, bool GATHER, bool OUT32>
+__device__ __forceinline__ void join_waves(const I8Args& p, const i32x4 (&acc)[MT], i32x4* part, int m0, int m1, int n0,
+                                           const float* sa, const float* sb) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int j = 0; j < MT; ++j) part[(wave * MT + j) * 64 + lane] = acc[j];
+    __syncthreads();
+    for (int o = threadIdx.x; o < MT * 64; o += 64 * W) {
+        const int l = o & 63, m = m0 + 16 * (o >> 6) + (l & 15), n = n0 + 4 * (l >> 4);
+        i32x4 v = part[o];
+#pragma unroll
+        for (int w = 1; w < W; ++w) v += part[w * MT * 64 + o];
+        if (m < m1 && n < p.N) {
+            const float s = sa[GATHER ? p.a_rows[m] : m];
+            const float f[4] = {(float)v[0] * s * sb[n], (float)v[1] * s * sb[n + 1], (float)v[2] * s * sb[n + 2],
+                                (float)v[3] * s * sb[n + 3]};
+            store4<OUT32>(p.c, (int64_t)m * p.ldc + n, f);
+        }
+    }
+}
+
+// U runs in flight.  Grouped: grid row y is a group; its rows go in passes of 16 MT.
+template <int MT, int W, int U, bool GROUPED, bool GATHER, bool OUT32>
 __global__ void __launch_bounds__(64 * W) k_i8_stream(I8Args p) {
-    constexpr int kOut = NT * MT * 64;              // 16-byte pieces of a wave's partial sums
-    __shared__ __attribute__((aligned(16))) i32x4 part[W][kOut];
+    __shared__ __attribute__((aligned(16))) i32x4 part[W * MT * 64];
     const int lane = threadIdx.x & 63;
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int q = lane >> 4, r16 = lane & 15;
-    const int n0 = blockIdx.x * 16 * NT;
+    const int q = lane >> 4, r16 = lane & 15, n0 = blockIdx.x * 16;
     int m0 = 0, m1 = p.M;
     const uint8_t* b = p.b;
     const float* sb = p.sb;
@@ -476,64 +511,108 @@ __global__ void __launch_bounds__(64 * W) k_i8_stream(I8Args p) {
         b += (int64_t)blockIdx.y * p.b_sg;
         sb += (int64_t)blockIdx.y * p.sb_sg;
     }
-    const uint8_t* brow[NT];
-#pragma unroll
-    for (int i = 0; i < NT; ++i) brow[i] = b + (int64_t)min(n0 + 16 * i + r16, p.N - 1) * p.ldb + 16 * q;
-    const int steps = (p.K + 63) / 64;
+    const uint8_t* brow = b + (int64_t)min(n0 + r16, p.N - 1) * p.ldb;
     for (; m0 < m1; m0 += 16 * MT) {
         const uint8_t* arow[MT];
 #pragma unroll
         for (int j = 0; j < MT; ++j) {
             int m = min(m0 + 16 * j + r16, m1 - 1);
             if (GATHER) m = p.a_rows[m];
-            arow[j] = p.a + (int64_t)m * p.lda + 16 * q;
+            arow[j] = p.a + (int64_t)m * p.lda;
         }
-        i32x4 acc[NT][MT];
+        i32x4 acc[MT];
 #pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < MT; ++j) acc[i][j] = i32x4{0, 0, 0, 0};
-        constexpr int U = 4;                        // runs in flight
-        for (int s = wave; s < steps; s += W * U) {
-            i32x4 fb[U][NT], fa[U][MT];
-            const i32x4 zero = {0, 0, 0, 0};
+        for (int j = 0; j < MT; ++j) acc[j] = i32x4{0, 0, 0, 0};
+        for (int k = wave * kRun; k < p.K; k += W * U * kRun) {
+            Run fb[U], fa[U][MT];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                // past K: nothing is read, and zeros add nothing
-                const int k = (s + u * W) * 64;
-                const bool in = k + 16 * q < p.K;
+                fb[u] = load_run(brow, k + u * W * kRun, p.K, q);
 #pragma unroll
-                for (int i = 0; i < NT; ++i) fb[u][i] = in ? *reinterpret_cast<const i32x4*>(brow[i] + k) : zero;
-#pragma unroll
-                for (int j = 0; j < MT; ++j) fa[u][j] = in ? *reinterpret_cast<const i32x4*>(arow[j] + k) : zero;
+                for (int j = 0; j < MT; ++j) fa[u][j] = load_run(arow[j], k + u * W * kRun, p.K, q);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
 #pragma unroll
-                for (int i = 0; i < NT; ++i)
-#pragma unroll
-                    for (int j = 0; j < MT; ++j) acc[i][j] = mfma(fb[u][i], fa[u][j], acc[i][j]);
+                for (int j = 0; j < MT; ++j)
+                    acc[j] = mfma(fb[u].hi, fa[u][j].hi, mfma(fb[u].lo, fa[u][j].lo, acc[j]));
         }
-#pragma unroll
-        for (int i = 0; i < NT; ++i)
-#pragma unroll
-            for (int j = 0; j < MT; ++j) part[wave][(i * MT + j) * 64 + lane] = acc[i][j];
-        __syncthreads();
-        for (int o = threadIdx.x; o < kOut; o += 64 * W) {
-            i32x4 v = part[0][o];
-#pragma unroll
-            for (int w = 1; w < W; ++w) v += part[w][o];
-            const int l = o & 63, i = (o >> 6) / MT, j = (o >> 6) % MT;
-            const int m = m0 + 16 * j + (l & 15), n = n0 + 16 * i + 4 * (l >> 4);
-            if (m < m1 && n < p.N) {
-                const float sam = p.sa[GATHER ? p.a_rows[m] : m];
-                const float f[4] = {(float)v[0] * sam * sb[n], (float)v[1] * sam * sb[n + 1],
-                                    (float)v[2] * sam * sb[n + 2], (float)v[3] * sam * sb[n + 3]};
-                store4<OUT32>(p.c, (int64_t)m * p.ldc + n, f);
-            }
-        }
+        join_waves<MT, W, GATHER, OUT32>(p, acc, part, m0, m1, n0, p.sa, sb);
         __syncthreads();
     }
+}
+
+// The same for a few bf16 rows that every workgroup quantizes for itself into LDS
+// (kFusedCodes of them at most: a second or so of L2 reads in the shadow of the first
+// weights), which saves the launch before.
+constexpr int kFusedRows = 16, kFusedCodes = 16384;
+template <int W, int U, bool OUT32>
+__global__ void __launch_bounds__(64 * W) k_i8_stream_x(I8Args p, const uint16_t* x, int64_t ld_x, int32_t cols) {
+    constexpr int kChunks = kFusedCodes / 8 / (64 * W);     // chunks of eight values per thread
+    __shared__ __attribute__((aligned(16))) uint8_t codes[kFusedCodes + 15 * kFusedRows];
+    __shared__ __attribute__((aligned(16))) i32x4 part[W * 64];
+    __shared__ uint32_t top[kFusedRows];
+    __shared__ float scale[kFusedRows];
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int q = lane >> 4, r16 = lane & 15, n0 = blockIdx.x * 16;
+    const uint8_t* brow = p.b + (int64_t)min(n0 + r16, p.N - 1) * p.ldb;
+    const int chunks = cols / 8, all = p.M * chunks;
+    uint4 w[kChunks];
+    int row[kChunks];
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = threadIdx.x + i * 64 * W;
+        row[i] = c / chunks;
+        w[i] = make_uint4(0, 0, 0, 0);
+        if (c < all) w[i] = *reinterpret_cast<const uint4*>(x + (int64_t)row[i] * ld_x + (c - row[i] * chunks) * 8);
+    }
+    Run fb[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) fb[u] = load_run(brow, (wave + u * W) * kRun, p.K, q);
+    if (threadIdx.x < kFusedRows) top[threadIdx.x] = 0;
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const u16x2 m = absmax_bits(u16x2{0, 0}, w[i]);
+        // a wave's chunks are mostly of one row: its maximum goes to LDS once
+        const int first = __builtin_amdgcn_readfirstlane(row[i]);
+        const uint32_t mine = max((uint32_t)m.x, (uint32_t)m.y);
+        const uint32_t both = lanes_umax<64>(row[i] == first ? mine : 0u);
+        if (lane == 0 && first < p.M) atomicMax(&top[first], both);
+        if (row[i] != first && row[i] < p.M) atomicMax(&top[row[i]], mine);
+    }
+    __syncthreads();
+    if (threadIdx.x < p.M) scale[threadIdx.x] = i8_scale_of(top[threadIdx.x]);
+#pragma unroll
+    for (int i = 0; i < kChunks; ++i) {
+        const int c = threadIdx.x + i * 64 * W;
+        if (c < all) {
+            const I8Scale sc = i8_scale(i8_scale_of(top[row[i]]));
+            float v[8];
+            unpack8(w[i], v);
+            uint8_t* to = codes + row[i] * p.K + (c - row[i] * chunks) * 8;
+            *reinterpret_cast<uint2*>(to) = i8_codes8<0>(v, &sc);
+            if (p.K != cols && (c + 1) % chunks == 0) *reinterpret_cast<uint2*>(to + 8) = make_uint2(0, 0);
+        }
+    }
+    __syncthreads();
+    const uint8_t* arow = codes + min(r16, p.M - 1) * p.K;
+    i32x4 acc[1] = {i32x4{0, 0, 0, 0}};
+    for (int k = wave * kRun; k < p.K; k += W * U * kRun) {
+        Run now[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            now[u] = fb[u];
+            fb[u] = load_run(brow, k + (u + U) * W * kRun, p.K, q);
+        }
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            const Run fa = load_run(arow, k + u * W * kRun, p.K, q);
+            acc[0] = mfma(now[u].hi, fa.hi, mfma(now[u].lo, fa.lo, acc[0]));
+        }
+    }
+    join_waves<1, W, false, OUT32>(p, acc, part, 0, p.M, n0, scale, p.sb);
 }
 
 template <int TM, int TN, bool GROUPED, bool GATHER>
@@ -547,11 +626,11 @@ hipError_t tile(const I8Args& p, bool out32, hipStream_t st) {
     return hipGetLastError();
 }
 
-template <int MT, int NT, int W, bool GROUPED, bool GATHER>
+template <int MT, int W, int U, bool GROUPED, bool GATHER>
 hipError_t stream(const I8Args& p, bool out32, hipStream_t st) {
-    const dim3 grid((unsigned)((p.N + 16 * NT - 1) / (16 * NT)), (unsigned)(GROUPED ? p.G : 1));
-    if (out32) hipLaunchKernelGGL((k_i8_stream<MT, NT, W, GROUPED, GATHER, true>), grid, dim3(64 * W), 0, st, p);
-    else hipLaunchKernelGGL((k_i8_stream<MT, NT, W, GROUPED, GATHER, false>), grid, dim3(64 * W), 0, st, p);
+    const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)(GROUPED ? p.G : 1));
+    if (out32) hipLaunchKernelGGL((k_i8_stream<MT, W, U, GROUPED, GATHER, true>), grid, dim3(64 * W), 0, st, p);
+    else hipLaunchKernelGGL((k_i8_stream<MT, W, U, GROUPED, GATHER, false>), grid, dim3(64 * W), 0, st, p);
     return hipGetLastError();
 }
 
@@ -559,8 +638,8 @@ template <bool GROUPED, bool GATHER>
 hipError_t launch(const I8Args& p, bool out32, hipStream_t st) {
     // rows per product, or on average per group
     const int64_t rows = GROUPED ? ((int64_t)p.M + p.G - 1) / p.G : p.M;
-    if (rows <= 16) return stream<1, 1, 8, GROUPED, GATHER>(p, out32, st);
-    if (rows <= 64) return stream<4, 1, 8, GROUPED, GATHER>(p, out32, st);
+    if (rows <= 16) return stream<1, 8, 4, GROUPED, GATHER>(p, out32, st);
+    if (rows <= 64) return stream<4, 16, 2, GROUPED, GATHER>(p, out32, st);
     const int64_t big = ((int64_t)p.M + 255) / 256 * ((p.N + 255) / 256);
     if (big >= 128) return tile<4, 4, GROUPED, GATHER>(p, out32, st);
     return tile<2, 2, GROUPED, GATHER>(p, out32, st);
@@ -574,6 +653,17 @@ hipError_t launch_i8_gemm(const I8GemmArgs& g, hipStream_t st) {
                    g.c, g.ldc, g.G, g.offsets, g.a_rows};
     if (g.G == 0) return launch<false, false>(p, g.out_f32, st);
     return g.a_rows ? launch<true, true>(p, g.out_f32, st) : launch<true, false>(p, g.out_f32, st);
+}
+
+bool i8_linear_fused(int64_t rows, int64_t cols) { return rows <= kFusedRows && rows * cols <= kFusedCodes && cols > 0; }
+
+hipError_t launch_i8_linear_fused(const I8GemmArgs& g, const uint16_t* x, int64_t ld_x, int64_t cols, hipStream_t st) {
+    const I8Args p{(int32_t)g.M, (int32_t)g.N, (int32_t)g.K, nullptr, 0, nullptr, g.b, g.ldb, 0, g.sb, 0, g.c, g.ldc, 0,
+                   nullptr, nullptr};
+    const dim3 grid((unsigned)((g.N + 15) / 16));
+    if (g.out_f32) hipLaunchKernelGGL((k_i8_stream_x<8, 4, true>), grid, dim3(512), 0, st, p, x, ld_x, (int32_t)cols);
+    else hipLaunchKernelGGL((k_i8_stream_x<8, 4, false>), grid, dim3(512), 0, st, p, x, ld_x, (int32_t)cols);
+    return hipGetLastError();
 }
 
 }  // namespace fp8bs

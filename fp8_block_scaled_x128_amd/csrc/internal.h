@@ -65,6 +65,10 @@ struct I8GemmArgs {
     int32_t G; const int32_t* offsets; const int32_t* a_rows;   // G 0: dense
 };
 hipError_t launch_i8_gemm(const I8GemmArgs& g, hipStream_t st);
+// The product of bf16 rows that are few enough to be quantized by every workgroup
+// for itself; g.a and g.sa are not read.
+bool i8_linear_fused(int64_t rows, int64_t cols);
+hipError_t launch_i8_linear_fused(const I8GemmArgs& g, const uint16_t* x, int64_t ld_x, int64_t cols, hipStream_t st);
 
 // moe.hip
 hipError_t launch_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y, const int32_t* pos,

@@ -28,7 +28,7 @@ constexpr float kEps = 1e-20f;
 // Lanes: group = l / q; its part l % q holds `w` experts (fewer at the group's end).
 struct GateLanes {
     int per, q, w;
-    bool vec;                       // rows in pieces of four logits
+    bool vec, vec_bias;             // rows, and the bias, in pieces of four
 };
 
 struct Score {
@@ -67,11 +67,26 @@ __device__ __forceinline__ float lane_at(float v, int lane) { return __shfl(v, l
 __device__ __forceinline__ double lane_at(double v, int lane) { return __shfl(v, lane, 64); }
 template <int L>
 __device__ __forceinline__ uint32_t lanes_kmax(uint32_t v) { return lanes_umax<L>(v); }
+template <int CTRL>
+__device__ __forceinline__ uint64_t dpp_mov64(uint64_t v) {
+    return (uint64_t)dpp_mov<CTRL>((uint32_t)(v >> 32)) << 32 | dpp_mov<CTRL>((uint32_t)v);
+}
 template <int L>
 __device__ __forceinline__ uint64_t lanes_kmax(uint64_t v) {
-#pragma unroll
-    for (int d = 1; d < L; d <<= 1) v = max(v, lane_xor(v, d));
-    return v;
+    static_assert(L == 64, "one token per wave");
+    v = max(v, dpp_mov64<kDppXor1>(v));
+    v = max(v, dpp_mov64<kDppXor2>(v));
+    v = max(v, dpp_mov64<kDppHalfMirror>(v));
+    v = max(v, dpp_mov64<kDppMirror>(v));
+    auto at = [&](int lane) { return (uint64_t)lane_value((uint32_t)(v >> 32), lane) << 32 | lane_value((uint32_t)v, lane); };
+    return max(max(at(0), at(16)), max(at(32), at(48)));
+}
+__device__ __forceinline__ uint32_t lane_dpp(uint32_t v, int d) {
+    return d == 1 ? dpp_mov<kDppXor1>(v) : d == 2 ? dpp_mov<kDppXor2>(v) : d == 4 ? dpp_mov<kDppHalfMirror>(v)
+                                                                                    : dpp_mov<kDppMirror>(v);
+}
+__device__ __forceinline__ uint64_t lane_dpp(uint64_t v, int d) {
+    return (uint64_t)lane_dpp((uint32_t)(v >> 32), d) << 32 | lane_dpp((uint32_t)v, d);
 }
 template <int L>
 __device__ __forceinline__ double lanes_sum64(double v) {
@@ -100,10 +115,15 @@ __device__ __forceinline__ bool pick(K (&left)[V], const GateArgs& g, const Gate
             m2 = max(m2, min(m1, left[i]));
             m1 = max(m1, left[i]);
         }
-        for (int d = 1; d < n.q; d <<= 1) {
-            const K a = lane_xor(m1, d), b = lane_xor(m2, d);
-            m2 = max(min(m1, a), max(m2, b));
-            m1 = max(m1, a);
+        // inside sixteen lanes the steps are lane moves: once pairs (quads, ...) agree,
+        // a mirror image serves as the other pair (quad, ...)
+#pragma unroll
+        for (int d = 1; d < L; d <<= 1) {
+            if (d < n.q) {
+                const K a = d < 16 ? lane_dpp(m1, d) : lane_xor(m1, d), b = d < 16 ? lane_dpp(m2, d) : lane_xor(m2, d);
+                m2 = max(min(m1, a), max(m2, b));
+                m1 = max(m1, a);
+            }
         }
         int rank = 0;
         if (EXACT && !g.top2) {                     // by the logits' 32-bit keys
@@ -189,46 +209,62 @@ __device__ __forceinline__ float logit_at(const void* base, int64_t at) {
                : __uint_as_float((uint32_t)static_cast<const uint16_t*>(base)[at] << 16);
 }
 
-// The selection again with values in 64 bits, for the wave's tokens.
-template <int L, int V, bool F32, bool SIG>
-__device__ __noinline__ void pick_again(const GateArgs& g, const GateLanes& n, int l, int e0, int cnt, int64_t t,
-                                        bool have, float m, bool (&ok)[2], uint32_t (&esel)[2]) {
+// One token's selection with values in 64 bits, by the whole wave (n: its 64 lanes
+// dealt to the groups).  Lane j returns slot j's expert, or -1.
+template <int V, bool F32, bool SIG>
+__device__ __forceinline__ int pick_again(const GateArgs& g, const GateLanes& n, int64_t t, float m) {
+    const int l = threadIdx.x & 63, group = l / n.q, part = l % n.q;
+    const int e0 = group < g.groups ? group * n.per + part * n.w : 0;
+    const int cnt = group < g.groups ? max(min(n.per - part * n.w, n.w), 0) : 0;
     float z[V];
     load_run<V, F32>(g.r.logits, t * g.r.ld, e0, g.r.E, n.vec, z);
     double sum = 1.0;
     if (!SIG) {
         sum = 0.0;
+#pragma unroll 1
+        for (int i = 0; i < cnt; ++i) {
+            float x = z[0];
 #pragma unroll
-        for (int i = 0; i < V; ++i) sum += i < cnt ? exp((double)z[i] - (double)m) : 0.0;
-        sum = lanes_sum64<L>(sum);
+            for (int u = 1; u < V; ++u) x = i == u ? z[u] : x;
+            sum += exp((double)x - (double)m);
+        }
+        sum = lanes_sum64<64>(sum);
     }
     auto score = [&](float x) {
         return SIG ? 1.0 / (1.0 + exp(-(double)x)) : exp((double)x - (double)m) / sum;
     };
+    uint32_t esel[2];
+    bool ok;
     if (g.bias) {
         uint64_t left[V], ksel[2];
 #pragma unroll
-        for (int i = 0; i < V; ++i) {
-            const bool there = have && i < cnt && !(z[i] == -INFINITY);
-            left[i] = there ? value_key(score(z[i]) + (double)g.bias[min(e0 + i, g.r.E - 1)]) : 0;
+        for (int i = 0; i < V; ++i) left[i] = 0;
+        // one exponential in the code, not V of them
+#pragma unroll 1
+        for (int i = 0; i < cnt; ++i) {
+            float x = z[0];
+#pragma unroll
+            for (int u = 1; u < V; ++u) x = i == u ? z[u] : x;
+            const uint64_t key = x == -INFINITY ? 0 : value_key(score(x) + (double)g.bias[e0 + i]);
+#pragma unroll
+            for (int u = 0; u < V; ++u) left[u] = i == u ? key : left[u];
         }
-        pick<L, V, false>(left, g, n, l, e0, 0.0, [](uint64_t k) { return key_value(k); }, ksel, esel);
-        ok[0] = ksel[0] > kKeyNegInf64;
-        ok[1] = ksel[1] > kKeyNegInf64;
+        pick<64, V, false>(left, g, n, l, e0, 0.0, [](uint64_t k) { return key_value(k); }, ksel, esel);
+        ok = ksel[0] > kKeyNegInf64;
     } else {
         uint32_t left[V], ksel[2];
 #pragma unroll
-        for (int i = 0; i < V; ++i) left[i] = have && i < cnt ? logit_key(z[i]) : 0u;
-        pick<L, V, true>(left, g, n, l, e0, 0.0, [&](uint32_t k) { return score(key_logit(k)); }, ksel, esel);
-        ok[0] = ksel[0] > kKeyNegInf;
-        ok[1] = ksel[1] > kKeyNegInf;
+        for (int i = 0; i < V; ++i) left[i] = i < cnt ? logit_key(z[i]) : 0u;
+        pick<64, V, true>(left, g, n, l, e0, 0.0, [&](uint32_t k) { return score(key_logit(k)); }, ksel, esel);
+        ok = ksel[0] > kKeyNegInf;
     }
+    return ok ? (int)esel[0] : -1;
 }
 
 // As the plain router's selection: masks and probability sums in LDS, {sum of
 // lse^2, routed tokens} to every thread.
-template <int L, int V, bool F32, bool SIG>
-__device__ __forceinline__ float2 gate_tokens(const GateArgs& g, const GateLanes& n, int64_t t0,
+template <int L, int V, int VW, bool F32, bool SIG>
+__device__ __forceinline__ float2 gate_tokens(const GateArgs& g, const GateLanes& n, const GateLanes& nw, int64_t t0,
                                               unsigned long long* mask, float* psum) {
     constexpr int kGroups = kThreads / L;
     const RouteArgs& p = g.r;
@@ -247,6 +283,8 @@ __device__ __forceinline__ float2 gate_tokens(const GateArgs& g, const GateLanes
         const bool have = t0 + tt < p.T && (!p.mask || p.mask[t]);
         float s[V];
         load_run<V, F32>(p.logits, t * p.ld, e0, p.E, n.vec, s);
+        float b[V];
+        if (g.bias) load_run<V, true>(g.bias, 0, e0, p.E, n.vec_bias, b);
         uint32_t left[V], best = 0;
 #pragma unroll
         for (int i = 0; i < V; ++i) {
@@ -279,7 +317,7 @@ __device__ __forceinline__ float2 gate_tokens(const GateArgs& g, const GateLanes
         if (g.bias) {
 #pragma unroll
             for (int i = 0; i < V; ++i) {
-                const float v = s[i] + g.bias[min(e0 + i, p.E - 1)];
+                const float v = s[i] + b[i];
                 left[i] = left[i] > kKeyNegInf ? logit_key(v) : 0u;
             }
             close = pick<L, V, false>(left, g, n, l, e0, tol0, [](uint32_t k) { return key_logit(k); }, ksel, esel);
@@ -291,7 +329,20 @@ __device__ __forceinline__ float2 gate_tokens(const GateArgs& g, const GateLanes
         }
         ok[0] = ksel[0] > kKeyNegInf;
         ok[1] = ksel[1] > kKeyNegInf;
-        if (__any(close)) pick_again<L, V, F32, SIG>(g, n, l, e0, cnt, t, have, m, ok, esel);
+        // the tokens of this wave whose order fp32 leaves open, one after the other
+        for (unsigned long long open = __ballot(close); open;) {
+            const int row = (__ffsll(open) - 1) & ~(L - 1);
+            open &= L == 64 ? 0 : ~(((1ull << (L & 63)) - 1) << row);
+            const int e = pick_again<VW, F32, SIG>(g, nw, (int64_t)__builtin_amdgcn_readlane((int)t, row), lane_at(m, row));
+#pragma unroll
+            for (int u = 0; u < 2; ++u) {
+                const int got = __shfl(e, l + u * L, 64);
+                if ((int)(threadIdx.x & 63 & ~(L - 1)) == row) {
+                    ok[u] = got >= 0 && l + u * L < 64;
+                    esel[u] = (uint32_t)max(got, 0);
+                }
+            }
+        }
         float w[2], wsum = 0.0f;
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
@@ -353,19 +404,19 @@ __device__ __forceinline__ float2 gate_tokens(const GateArgs& g, const GateLanes
     return make_float2(sums[0], sums[1]);
 }
 
-template <int L, int V, bool F32, bool SIG>
-__global__ void __launch_bounds__(kThreads) k_gate_one(GateArgs g, GateLanes n) {
+template <int L, int V, int VW, bool F32, bool SIG>
+__global__ void __launch_bounds__(kThreads) k_gate_one(GateArgs g, GateLanes n, GateLanes nw) {
     extern __shared__ __align__(16) unsigned char dyn[];
     route_one(g.r, dyn, kHalf * g.r.E, [&](unsigned long long* mask, float* psum) {
-        return gate_tokens<L, V, F32, SIG>(g, n, 0, mask, psum);
+        return gate_tokens<L, V, VW, F32, SIG>(g, n, nw, 0, mask, psum);
     });
 }
 
-template <int L, int V, bool F32, bool SIG>
-__global__ void __launch_bounds__(kThreads) k_gate_select(GateArgs g, GateLanes n, RouteWs ws) {
+template <int L, int V, int VW, bool F32, bool SIG>
+__global__ void __launch_bounds__(kThreads) k_gate_select(GateArgs g, GateLanes n, GateLanes nw, RouteWs ws) {
     extern __shared__ __align__(16) unsigned char dyn[];
     route_select(g.r, ws, dyn, [&](unsigned long long* mask, float* psum) {
-        return gate_tokens<L, V, F32, SIG>(g, n, (int64_t)blockIdx.x * kTok, mask, psum);
+        return gate_tokens<L, V, VW, F32, SIG>(g, n, nw, (int64_t)blockIdx.x * kTok, mask, psum);
     });
 }
 
@@ -510,23 +561,25 @@ __global__ void __launch_bounds__(1024) k_bias_update(float* bias, const int32_t
     if (e < E && c * E != sum) bias[e] += c * E < sum ? rate : -rate;
 }
 
-template <int L, int V, bool SIG>
-hipError_t run_gate(const GateArgs& g, const GateLanes& n, const RouteWs& ws, int nblk, hipStream_t st) {
+template <int L, int V, int VW, bool SIG>
+hipError_t run_gate(const GateArgs& g, const GateLanes& n, const GateLanes& nw, const RouteWs& ws, int nblk, hipStream_t st) {
     size_t lds = select_lds(g.r.E, g.r.E);
     if (nblk <= 1) {
         lds += (size_t)g.r.E * 8 + 8;
-        if (g.r.logits32) hipLaunchKernelGGL((k_gate_one<L, V, true, SIG>), dim3(1), dim3(kThreads), lds, st, g, n);
-        else hipLaunchKernelGGL((k_gate_one<L, V, false, SIG>), dim3(1), dim3(kThreads), lds, st, g, n);
+        if (g.r.logits32) hipLaunchKernelGGL((k_gate_one<L, V, VW, true, SIG>), dim3(1), dim3(kThreads), lds, st, g, n, nw);
+        else hipLaunchKernelGGL((k_gate_one<L, V, VW, false, SIG>), dim3(1), dim3(kThreads), lds, st, g, n, nw);
     } else {
-        if (g.r.logits32) hipLaunchKernelGGL((k_gate_select<L, V, true, SIG>), dim3(nblk), dim3(kThreads), lds, st, g, n, ws);
-        else hipLaunchKernelGGL((k_gate_select<L, V, false, SIG>), dim3(nblk), dim3(kThreads), lds, st, g, n, ws);
+        if (g.r.logits32)
+            hipLaunchKernelGGL((k_gate_select<L, V, VW, true, SIG>), dim3(nblk), dim3(kThreads), lds, st, g, n, nw, ws);
+        else
+            hipLaunchKernelGGL((k_gate_select<L, V, VW, false, SIG>), dim3(nblk), dim3(kThreads), lds, st, g, n, nw, ws);
     }
     return hipGetLastError();
 }
 
-template <int L, int V>
-hipError_t run_gate(const GateArgs& g, const GateLanes& n, const RouteWs& ws, int nblk, hipStream_t st) {
-    return g.sigmoid ? run_gate<L, V, true>(g, n, ws, nblk, st) : run_gate<L, V, false>(g, n, ws, nblk, st);
+template <int L, int V, int VW>
+hipError_t run_gate(const GateArgs& g, const GateLanes& n, const GateLanes& nw, const RouteWs& ws, int nblk, hipStream_t st) {
+    return g.sigmoid ? run_gate<L, V, VW, true>(g, n, nw, ws, nblk, st) : run_gate<L, V, VW, false>(g, n, nw, ws, nblk, st);
 }
 
 template <int L, int V>
@@ -552,32 +605,32 @@ hipError_t run_bwd(const GateBwdArgs& p, hipStream_t st) {
 hipError_t launch_moe_route_grouped(const GateArgs& g, void* wsp, hipStream_t st) {
     const int nblk = (int)((g.r.T + kTok - 1) / kTok);
     const RouteWs ws = route_workspace(g.r.T, g.r.E, wsp);
-    GateLanes n{};
-    n.per = g.r.E / g.groups;
+    const int per = g.r.E / g.groups;
     int lanes = 1;                                  // groups, rounded up to a power of two
     while (lanes < g.groups) lanes *= 2;
-    auto deal = [&](int L) {
-        n.q = L / lanes;
-        n.w = (n.per + n.q - 1) / n.q;
-        if (n.per % 4 == 0) n.w = (n.w + 3) / 4 * 4;
-    };
-    // sixteen lanes per token while they hold it in 32 values each, as the plain
-    // router's; 64 lanes always do (1024 experts in 2^k + 1 groups: 32)
-    bool wide = lanes > 16;
-    if (!wide) {
-        deal(16);
-        wide = n.w > 32;
-    }
-    if (wide) deal(64);
     const uintptr_t align = g.r.logits32 ? 16 : 8;
-    n.vec = n.per % 4 == 0 && g.r.ld % 4 == 0 && reinterpret_cast<uintptr_t>(g.r.logits) % align == 0;
+    const bool vec = per % 4 == 0 && g.r.ld % 4 == 0 && reinterpret_cast<uintptr_t>(g.r.logits) % align == 0;
+    const bool vec_bias = per % 4 == 0 && reinterpret_cast<uintptr_t>(g.bias) % 16 == 0;
+    auto deal = [&](int L) {
+        GateLanes n{per, L / lanes, 0, vec, vec_bias};
+        n.w = (per + n.q - 1) / n.q;
+        if (per % 4 == 0) n.w = (n.w + 3) / 4 * 4;
+        return n;
+    };
+    // sixteen lanes per token while they hold it in 16 values each; 32 would spill
+    // registers (16384 tokens of 512 experts 86 us, with 64 lanes 68).  64 lanes hold
+    // every token in 32 (1024 experts in 2^k + 1 groups), and a token that is selected
+    // again has them anyway.
+    const GateLanes nw = deal(64);
+    const bool wide = lanes > 16 || deal(16).w > 16;
+    const GateLanes n = wide ? nw : deal(16);
     hipError_t e;
-    if (wide) e = n.w <= 8 ? run_gate<64, 8>(g, n, ws, nblk, st) : n.w <= 16 ? run_gate<64, 16>(g, n, ws, nblk, st)
-                                                                             : run_gate<64, 32>(g, n, ws, nblk, st);
-    else if (n.w <= 4) e = run_gate<16, 4>(g, n, ws, nblk, st);
-    else if (n.w <= 8) e = run_gate<16, 8>(g, n, ws, nblk, st);
-    else if (n.w <= 16) e = run_gate<16, 16>(g, n, ws, nblk, st);
-    else e = run_gate<16, 32>(g, n, ws, nblk, st);
+    if (wide) e = n.w <= 8 ? run_gate<64, 8, 8>(g, n, nw, ws, nblk, st)
+                           : n.w <= 16 ? run_gate<64, 16, 16>(g, n, nw, ws, nblk, st)
+                                       : run_gate<64, 32, 32>(g, n, nw, ws, nblk, st);
+    else if (n.w <= 4) e = run_gate<16, 4, 4>(g, n, nw, ws, nblk, st);
+    else if (n.w <= 8) e = run_gate<16, 8, 4>(g, n, nw, ws, nblk, st);
+    else e = run_gate<16, 16, 4>(g, n, nw, ws, nblk, st);
     return e != hipSuccess || nblk <= 1 ? e : launch_route_rows(g.r, ws, st);
 }
 
