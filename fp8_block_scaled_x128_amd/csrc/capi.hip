@@ -1116,24 +1116,46 @@ static fp8bs_status i8_operand_args(int64_t arows, int64_t K, const int8_t* a, i
 }
 
 fp8bs_status int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* sa, const int8_t* b,
-                       int64_t ldb, const float* sb, void* c, int64_t ldc, fp8bs_out out, hipStream_t stream) {
+                       int64_t ldb, const float* sb, void* c, int64_t ldc, fp8bs_out out, void* ws, size_t ws_bytes,
+                       hipStream_t stream) {
     fp8bs_status v = i8_product_args(M, N, K, b, ldb, sb, c, ldc, out);
     if (v != FP8BS_OK) return v;
     if (M == 0 || N == 0) return ok();
     if ((v = i8_operand_args(M, K, a, lda, sa)) != FP8BS_OK) return v;
+    if (ws && !aligned(ws, 16)) return fail(FP8BS_ERR_ALIGN, "ws must be 16-byte aligned");
+    const size_t need = i8_gemm_ws_bytes(M, N, K);
+    if (ws && ws_bytes < need) return fail(FP8BS_ERR_SHAPE, "ws_bytes %zu < %zu", ws_bytes, need);
     if ((v = check_device()) != FP8BS_OK) return v;
     const I8GemmArgs g{M, N, K, reinterpret_cast<const uint8_t*>(a), lda, sa, reinterpret_cast<const uint8_t*>(b), ldb,
                        0, sb, 0, c, ldc, out == FP8BS_OUT_FP32, 0, nullptr, nullptr};
-    return launched(launch_i8_gemm(g, stream), "int8_gemm");
+    return launched(launch_i8_gemm(g, ws, stream), "int8_gemm");
 }
 
+// Sizes that int8_gemm and int8_linear take (their workspaces' sizes are asked for
+// without pointers).
+static fp8bs_status i8_ws_shape(int64_t M, int64_t N, int64_t K) {
+    if (M < 0 || N < 0 || K < 0 || M > INT32_MAX / 2 || N > INT32_MAX / 2 || K > 131056)
+        return fail(FP8BS_ERR_SHAPE, "M=%lld N=%lld K=%lld", (long long)M, (long long)N, (long long)K);
+    return FP8BS_OK;
+}
+
+fp8bs_status int8_gemm_ws_size(int64_t M, int64_t N, int64_t K, size_t* bytes) {
+    if (!bytes) return fail(FP8BS_ERR_NULL, "bytes is required");
+    const fp8bs_status v = i8_ws_shape(M, N, K);
+    if (v != FP8BS_OK) return v;
+    *bytes = i8_gemm_ws_bytes(M, N, K);
+    return ok();
+}
+
+// Workspace: the rows' scales, their codes, the sums of K ranges.
 static size_t i8_linear_scales(int64_t rows) { return (size_t)(rows + 3) / 4 * 16; }
 
-fp8bs_status int8_linear_ws_size(int64_t rows, int64_t cols, size_t* bytes) {
+fp8bs_status int8_linear_ws_size(int64_t rows, int64_t N, int64_t cols, size_t* bytes) {
     if (!bytes) return fail(FP8BS_ERR_NULL, "bytes is required");
-    if (rows < 0 || cols < 0 || rows > INT32_MAX / 2 || cols > INT32_MAX / 2)
-        return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
-    *bytes = i8_linear_scales(rows) + (size_t)rows * (size_t)((cols + 15) / 16 * 16);
+    const fp8bs_status v = i8_ws_shape(rows, N, cols);
+    if (v != FP8BS_OK) return v;
+    const int64_t K = (cols + 15) / 16 * 16;
+    *bytes = i8_linear_scales(rows) + (size_t)rows * (size_t)K + i8_gemm_ws_bytes(rows, N, K);
     return ok();
 }
 
@@ -1153,7 +1175,7 @@ fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* 
         if (ld_x % 8 || !aligned(x, 16)) return fail(FP8BS_ERR_ALIGN, "x must be 16-byte aligned with ld_x %% 8 == 0");
     }
     size_t need = 0;
-    if ((v = int8_linear_ws_size(rows, cols, &need)) != FP8BS_OK) return v;
+    if ((v = int8_linear_ws_size(rows, N, cols, &need)) != FP8BS_OK) return v;
     if (!ws) return fail(FP8BS_ERR_NULL, "a workspace of %zu bytes is required", need);
     if (ws_bytes < need) return fail(FP8BS_ERR_SHAPE, "ws_bytes %zu < %zu", ws_bytes, need);
     if (!aligned(ws, 16)) return fail(FP8BS_ERR_ALIGN, "ws must be 16-byte aligned");
@@ -1165,7 +1187,7 @@ fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* 
                        out == FP8BS_OUT_FP32, 0, nullptr, nullptr};
     if (i8_linear_fused(rows, cols)) return launched(launch_i8_linear_fused(g, x, ld_x, cols, stream), "int8_linear");
     const hipError_t e = launch_i8_quant_rows(x, rows, cols, ld_x, qx, K, sx, stream);
-    return launched(e != hipSuccess ? e : launch_i8_gemm(g, stream), "int8_linear");
+    return launched(e != hipSuccess ? e : launch_i8_gemm(g, qx + (size_t)rows * K, stream), "int8_linear");
 }
 
 fp8bs_status int8_grouped_gemm(int64_t total_rows, int64_t N, int64_t K, int32_t G, const int32_t* offsets,
@@ -1187,7 +1209,7 @@ fp8bs_status int8_grouped_gemm(int64_t total_rows, int64_t N, int64_t K, int32_t
     const I8GemmArgs g{total_rows, N, K, reinterpret_cast<const uint8_t*>(a), lda, sa,
                        reinterpret_cast<const uint8_t*>(b), ldb, b_stride_g, sb, sb_stride_g, c, ldc,
                        out == FP8BS_OUT_FP32, G, offsets, a_rows};
-    return launched(launch_i8_gemm(g, stream), "int8_grouped_gemm");
+    return launched(launch_i8_gemm(g, nullptr, stream), "int8_grouped_gemm");
 }
 
 fp8bs_status fp8bs_e4m3_encode(const float* in, uint8_t* out, int64_t n, hipStream_t stream) {

@@ -35,6 +35,7 @@ typedef int i32x16 __attribute__((ext_vector_type(16)));
 typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 constexpr int BK = 128;                 // K bytes per slice
+constexpr int kCUs = 256;
 
 
 
@@ -44,7 +45,11 @@ struct I8Args {
     const uint8_t* b; int64_t ldb; int64_t b_sg; const float* sb; int64_t sb_sg;
     void* c; int64_t ldc;
     int32_t G; const int32_t* offsets; const int32_t* a_rows;
+    int32_t splits;                     // dense: K ranges, one per grid row (OUT_SUMS)
 };
+
+// What a tile leaves: scaled outputs, or the sums themselves as [splits][M][N].
+enum { OUT_BF16, OUT_FP32, OUT_SUMS };
 
 __device__ __forceinline__ uint32_t lds_addr(const uint8_t* p) { return (uint32_t)(uintptr_t)(const lds_u8*)p; }
 __device__ __forceinline__ i32x4 lds_read16(uint32_t addr) {
@@ -152,7 +157,7 @@ __device__ __forceinline__ int group_tiles(const I8Args& p, int g) {
     return g < p.G ? (p.offsets[g + 1] - p.offsets[g] + BM - 1) / BM : 0;
 }
 
-template <int TM, int TN, bool GROUPED, bool GATHER, bool OUT32>
+template <int TM, int TN, bool GROUPED, bool GATHER, int OUT>
 __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p) {
     constexpr int BM = 64 * TM, BN = 64 * TN;
     constexpr int kABytes = BM * BK, kBBytes = BN * BK;
@@ -230,8 +235,17 @@ __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p
     // repeat its last row, their outputs are not stored.
     uint32_t offA[2 * TM], offB[2 * TN];
     const int sub = lane >> 3, chunk = (lane & 7) ^ sub;
-    const int ntail = p.K % BK / 16;                // chunks of the last slice, 0: all eight
-    const int nk = (p.K + BK - 1) / BK;
+    int ntail = p.K % BK / 16;                      // chunks of the last slice, 0: all eight
+    int nk = (p.K + BK - 1) / BK;
+    const uint8_t* pa = p.a;
+    if (OUT == OUT_SUMS) {
+        // this grid row's slices: the first nk % splits ranges have one more
+        const int y = blockIdx.y, per = nk / p.splits, more = nk % p.splits, k0 = y * per + min(y, more);
+        nk = per + (y < more);
+        if (y != p.splits - 1) ntail = 0;
+        pa += (int64_t)k0 * BK;
+        t.b += (int64_t)k0 * BK;
+    }
 #pragma unroll
     for (int j = 0; j < 2 * TM; ++j) {
         int m = min(t.m0 + 8 * (wave + 4 * j) + sub, t.m1 - 1);
@@ -258,7 +272,7 @@ __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p
         }
         unrolled<2 * TM>([&](auto j) {
             constexpr int J = decltype(j)::value;
-            if (acts) copy16<32 * J * BK>(p.a + (int64_t)kb * BK, offA[J], bufA(kb) + mine);
+            if (acts) copy16<32 * J * BK>(pa + (int64_t)kb * BK, offA[J], bufA(kb) + mine);
         });
         unrolled<2 * TN>([&](auto j) {
             constexpr int J = decltype(j)::value;
@@ -337,7 +351,7 @@ __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p
         const uint32_t rowsB = lds0 + 2 * kABytes + wn * 32 * TN * BK;
         const Frag ha = frag(bufA(kb + 1) + wm * 32 * TM * BK), hb = frag(rowsB + wb * kBBytes);
         const Frag hn = frag(rowsB + wb1 * kBBytes);
-        const uint8_t* baseA = p.a + (int64_t)(kb + 3) * BK;
+        const uint8_t* baseA = pa + (int64_t)(kb + 3) * BK;
         const uint8_t* baseB = t.b + (int64_t)(kb + 2) * BK;
         const uint32_t dstA = bufA(kb + 1) + mine, dstB = lds0 + 2 * kABytes + wb2 * kBBytes + mine;
         unrolled<kSteps>([&](auto step) {
@@ -353,21 +367,20 @@ __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p
             unrolled<kSpan>([&](auto vv) {
                 constexpr int v = decltype(vv)::value, u = v / TM;
                 add(std::integral_constant<int, i / 2 * TM + v % TM>{}, fb[i & 1][u], fa[2 * (i % 2) + u][v % TM]);
-                if constexpr (v < 2) {
-                    // (after the last slice: whatever is there, and not used)
-                    if constexpr (i < kSteps - 1) nb[v] = lds_read16(hb.at[2 * ((i + 1) % 2) + v] + (i + 1) / 2 * 32 * BK);
-                    else nb[v] = lds_read16(hn.at[v]);
-                }
-                constexpr int w = v - 2 + 2 * (kSpan == 4);       // spans of four: reads and copies share the places
-                if constexpr (w >= 0 && i < kMid) {
-                    constexpr int n = kSpan == 4 ? 1 : kReads / 2;    // next activations, in two places
-                    if constexpr (w < kReads / n) {
-                        unrolled<n>([&](auto x) {
-                            constexpr int r = i * kReads + w * n + decltype(x)::value;
+                // reads spread over the span: the next weights, then the next activations
+                constexpr int kAll = 2 + (i < kMid ? kReads : 0), kOver = kAll > kSpan ? kAll : kSpan;
+                unrolled<kAll>([&](auto xx) {
+                    constexpr int x = decltype(xx)::value, r = i * kReads + x - 2;
+                    if constexpr (x * kSpan / kOver == v) {
+                        if constexpr (x >= 2) {
                             if constexpr (r < 4 * TM) na[r / TM][r % TM] = lds_read16(ha.at[r / TM] + (r % TM) * 32 * BK);
-                        });
+                        } else if constexpr (i < kSteps - 1) {
+                            nb[x] = lds_read16(hb.at[2 * ((i + 1) % 2) + x] + (i + 1) / 2 * 32 * BK);
+                        } else {
+                            nb[x] = lds_read16(hn.at[x]);    // (after the last slice: whatever is there, not used)
+                        }
                     }
-                }
+                });
                 constexpr int c = kSpan - 1 - v;    // copies from the span's end on
                 if constexpr (i < kMid && c < kStepB) {
                     constexpr int j = i * kStepB + c;
@@ -433,14 +446,18 @@ __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p
             constexpr int j = decltype(col)::value, at = i * TM + j;
             const int m = mw + 32 * j, n = nw + 32 * i + 8 * g;
             float v[8];
+            int sum[8];
             unrolled<8>([&](auto rr) {
                 constexpr int r = decltype(rr)::value;
-                int sum;
-                if constexpr (kAcc) sum = acc_read<16 * at + 4 * g + r>();
-                else sum = own[at][4 * g + r];
-                v[r] = (float)sum * sam[j] * sbn[r];
+                if constexpr (kAcc) sum[r] = acc_read<16 * at + 4 * g + r>();
+                else sum[r] = own[at][4 * g + r];
+                v[r] = (float)sum[r] * sam[j] * sbn[r];
             });
-            if constexpr (OUT32) {
+            if constexpr (OUT == OUT_SUMS) {
+                int32_t* c = static_cast<int32_t*>(p.c) + ((int64_t)blockIdx.y * p.M + m) * p.N + n + 4 * hi;
+                if (m < t.m1 && n < p.N) *reinterpret_cast<i32x4*>(c) = i32x4{sum[0], sum[1], sum[2], sum[3]};
+                if (m < t.m1 && n + 8 < p.N) *reinterpret_cast<i32x4*>(c + 8) = i32x4{sum[4], sum[5], sum[6], sum[7]};
+            } else if constexpr (OUT == OUT_FP32) {
                 float* c = static_cast<float*>(p.c) + (int64_t)m * p.ldc + n + 4 * hi;
                 if (m < t.m1 && n < p.N) *reinterpret_cast<float4*>(c) = make_float4(v[0], v[1], v[2], v[3]);
                 if (m < t.m1 && n + 8 < p.N) *reinterpret_cast<float4*>(c + 8) = make_float4(v[4], v[5], v[6], v[7]);
@@ -465,12 +482,20 @@ constexpr int kRun = 128;
 struct Run {
     i32x4 lo, hi;
 };
-// A lane's 32 bytes at `row` + k; zeros past the end (K % 16 == 0), without a read.
-__device__ __forceinline__ Run load_run(const uint8_t* row, int k, int K, int q) {
-    const i32x4 zero = {0, 0, 0, 0};
+// A lane's 32 bytes at `row` + k (K % 16 == 0).  Past the end weights are those of the
+// row's last 16 bytes, so that no load waits for a comparison, and activations zeros:
+// zero times any code is zero.
+__device__ __forceinline__ Run weight_run(const uint8_t* row, int k, int K, int q) {
     const int at = k + 32 * q;
-    return {at < K ? *reinterpret_cast<const i32x4*>(row + at) : zero,
-            at + 16 < K ? *reinterpret_cast<const i32x4*>(row + at + 16) : zero};
+    return {*reinterpret_cast<const i32x4*>(row + min(at, K - 16)), *reinterpret_cast<const i32x4*>(row + min(at + 16, K - 16))};
+}
+__device__ __forceinline__ Run act_run(const uint8_t* row, int k, int K, int q) {
+    const int at = k + 32 * q;
+    Run r = weight_run(row, k, K, q);
+    const i32x4 zero = {0, 0, 0, 0};
+    r.lo = at < K ? r.lo : zero;
+    r.hi = at + 16 < K ? r.hi : zero;
+    return r;
 }
 
 // The waves' partial sums of MT tiles, added in LDS, scaled and stored.
@@ -527,9 +552,9 @@ __global__ void __launch_bounds__(64 * W) k_i8_stream(I8Args p) {
             Run fb[U], fa[U][MT];
 #pragma unroll
             for (int u = 0; u < U; ++u) {
-                fb[u] = load_run(brow, k + u * W * kRun, p.K, q);
+                fb[u] = weight_run(brow, k + u * W * kRun, p.K, q);
 #pragma unroll
-                for (int j = 0; j < MT; ++j) fa[u][j] = load_run(arow[j], k + u * W * kRun, p.K, q);
+                for (int j = 0; j < MT; ++j) fa[u][j] = act_run(arow[j], k + u * W * kRun, p.K, q);
             }
 #pragma unroll
             for (int u = 0; u < U; ++u)
@@ -569,7 +594,7 @@ __global__ void __launch_bounds__(64 * W) k_i8_stream_x(I8Args p, const uint16_t
     }
     Run fb[U];
 #pragma unroll
-    for (int u = 0; u < U; ++u) fb[u] = load_run(brow, (wave + u * W) * kRun, p.K, q);
+    for (int u = 0; u < U; ++u) fb[u] = weight_run(brow, (wave + u * W) * kRun, p.K, q);
     if (threadIdx.x < kFusedRows) top[threadIdx.x] = 0;
     __syncthreads();
 #pragma unroll
@@ -604,15 +629,31 @@ __global__ void __launch_bounds__(64 * W) k_i8_stream_x(I8Args p, const uint16_t
 #pragma unroll
         for (int u = 0; u < U; ++u) {
             now[u] = fb[u];
-            fb[u] = load_run(brow, k + (u + U) * W * kRun, p.K, q);
+            fb[u] = weight_run(brow, k + (u + U) * W * kRun, p.K, q);
         }
 #pragma unroll
         for (int u = 0; u < U; ++u) {
-            const Run fa = load_run(arow, k + u * W * kRun, p.K, q);
+            const Run fa = act_run(arow, k + u * W * kRun, p.K, q);
             acc[0] = mfma(now[u].hi, fa.hi, mfma(now[u].lo, fa.lo, acc[0]));
         }
     }
     join_waves<1, W, false, OUT32>(p, acc, part, 0, p.M, n0, scale, p.sb);
+}
+
+// The K ranges' sums [splits][M][N], added, scaled and stored: four outputs a thread.
+template <bool OUT32>
+__global__ void __launch_bounds__(256) k_i8_join(I8Args p, const i32x4* sums, int64_t quads) {
+    const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+    if (i >= quads) return;
+    const int64_t m = i * 4 / p.N;
+    const int n = (int)(i * 4 - m * p.N);
+    i32x4 v = sums[i];
+#pragma unroll 4
+    for (int s = 1; s < p.splits; ++s) v += sums[s * quads + i];
+    const float sa = p.sa[m];
+    const float f[4] = {(float)v[0] * sa * p.sb[n], (float)v[1] * sa * p.sb[n + 1], (float)v[2] * sa * p.sb[n + 2],
+                        (float)v[3] * sa * p.sb[n + 3]};
+    store4<OUT32>(p.c, m * p.ldc + n, f);
 }
 
 template <int TM, int TN, bool GROUPED, bool GATHER>
@@ -621,8 +662,32 @@ hipError_t tile(const I8Args& p, bool out32, hipStream_t st) {
     const int64_t ntn = (p.N + BN - 1) / BN;
     int64_t blocks = ((int64_t)p.M + BM - 1) / BM * ntn;
     if (GROUPED) blocks = (((int64_t)p.M / BM + std::min<int64_t>(p.G, p.M)) * ntn + 7) / 8 * 8;   // at most this many tiles
-    if (out32) hipLaunchKernelGGL((k_i8_tile<TM, TN, GROUPED, GATHER, true>), dim3((unsigned)blocks), dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((k_i8_tile<TM, TN, GROUPED, GATHER, false>), dim3((unsigned)blocks), dim3(256), 0, st, p);
+    if (out32) hipLaunchKernelGGL((k_i8_tile<TM, TN, GROUPED, GATHER, OUT_FP32>), dim3((unsigned)blocks), dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((k_i8_tile<TM, TN, GROUPED, GATHER, OUT_BF16>), dim3((unsigned)blocks), dim3(256), 0, st, p);
+    return hipGetLastError();
+}
+
+// K ranges for products with few tiles and a long K: tiles of 64 x 128, about two for
+// each compute unit, of four slices at least.
+int split_count(int64_t M, int64_t N, int64_t K) {
+    const int64_t tiles = (M + 63) / 64 * ((N + 127) / 128), nk = (K + BK - 1) / BK;
+    if (M <= 16 || M > 512 || tiles >= 256 || nk < 16) return 1;
+    return (int)std::max<int64_t>(1, std::min<int64_t>(2 * kCUs / tiles, nk / 4));
+}
+
+hipError_t split(I8Args p, bool out32, int splits, void* ws, hipStream_t st) {
+    I8Args q = p;
+    q.c = ws;
+    q.splits = p.splits = splits;
+    const dim3 grid((unsigned)((p.M + 63) / 64 * ((p.N + 127) / 128)), (unsigned)splits);
+    hipLaunchKernelGGL((k_i8_tile<1, 2, false, false, OUT_SUMS>), grid, dim3(256), 0, st, q);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int64_t quads = (int64_t)p.M * p.N / 4;
+    const dim3 join((unsigned)((quads + 255) / 256));
+    const i32x4* sums = static_cast<const i32x4*>(ws);
+    if (out32) hipLaunchKernelGGL(k_i8_join<true>, join, dim3(256), 0, st, p, sums, quads);
+    else hipLaunchKernelGGL(k_i8_join<false>, join, dim3(256), 0, st, p, sums, quads);
     return hipGetLastError();
 }
 
@@ -639,7 +704,7 @@ hipError_t launch(const I8Args& p, bool out32, hipStream_t st) {
     // rows per product, or on average per group
     const int64_t rows = GROUPED ? ((int64_t)p.M + p.G - 1) / p.G : p.M;
     if (rows <= 16) return stream<1, 8, 4, GROUPED, GATHER>(p, out32, st);
-    if (rows <= 64) return stream<4, 16, 2, GROUPED, GATHER>(p, out32, st);
+    if (rows <= 64 && (GROUPED || p.K <= 2048)) return stream<4, 16, 2, GROUPED, GATHER>(p, out32, st);
     const int64_t big = ((int64_t)p.M + 255) / 256 * ((p.N + 255) / 256);
     if (big >= 128) return tile<4, 4, GROUPED, GATHER>(p, out32, st);
     return tile<2, 2, GROUPED, GATHER>(p, out32, st);
@@ -647,11 +712,19 @@ hipError_t launch(const I8Args& p, bool out32, hipStream_t st) {
 
 }  // namespace
 
-hipError_t launch_i8_gemm(const I8GemmArgs& g, hipStream_t st) {
+size_t i8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K) {
+    const int n = M == 0 || N == 0 ? 1 : split_count(M, N, K);
+    return n > 1 ? (size_t)n * (size_t)M * (size_t)N * 4 : 0;
+}
+
+hipError_t launch_i8_gemm(const I8GemmArgs& g, void* ws, hipStream_t st) {
     if (g.M == 0 || g.N == 0) return hipSuccess;
     const I8Args p{(int32_t)g.M, (int32_t)g.N, (int32_t)g.K, g.a, g.lda, g.sa, g.b, g.ldb, g.b_sg, g.sb, g.sb_sg,
-                   g.c, g.ldc, g.G, g.offsets, g.a_rows};
-    if (g.G == 0) return launch<false, false>(p, g.out_f32, st);
+                   g.c, g.ldc, g.G, g.offsets, g.a_rows, 1};
+    if (g.G == 0) {
+        const int n = ws ? split_count(g.M, g.N, g.K) : 1;
+        return n > 1 ? split(p, g.out_f32, n, ws, st) : launch<false, false>(p, g.out_f32, st);
+    }
     return g.a_rows ? launch<true, true>(p, g.out_f32, st) : launch<true, false>(p, g.out_f32, st);
 }
 
@@ -659,7 +732,7 @@ bool i8_linear_fused(int64_t rows, int64_t cols) { return rows <= kFusedRows && 
 
 hipError_t launch_i8_linear_fused(const I8GemmArgs& g, const uint16_t* x, int64_t ld_x, int64_t cols, hipStream_t st) {
     const I8Args p{(int32_t)g.M, (int32_t)g.N, (int32_t)g.K, nullptr, 0, nullptr, g.b, g.ldb, 0, g.sb, 0, g.c, g.ldc, 0,
-                   nullptr, nullptr};
+                   nullptr, nullptr, 1};
     const dim3 grid((unsigned)((g.N + 15) / 16));
     if (g.out_f32) hipLaunchKernelGGL((k_i8_stream_x<8, 4, true>), grid, dim3(512), 0, st, p, x, ld_x, (int32_t)cols);
     else hipLaunchKernelGGL((k_i8_stream_x<8, 4, false>), grid, dim3(512), 0, st, p, x, ld_x, (int32_t)cols);

@@ -128,11 +128,10 @@ hipError_t launch_rows(const RowArgs& p, hipStream_t st) {
 }
 
 // ------------------------------------------------------------------ columns
-// A tile is 128 rows x 64 columns: a thread takes eight columns of four
-// consecutive rows, so that a column's four codes are one word of the LDS tile
-// (column stride 33 words: the 64 writes of a wave hit 64 banks), which leaves
-// for memory as 128 consecutive bytes per column.
-constexpr int kTileRows = 128, kTileCols = 64, kColWords = kTileRows / 4 + 1;
+// A thread takes eight columns of four consecutive rows, so that a column's four
+// codes are one word of an LDS tile of 64 columns (column stride odd: the 64 writes of
+// a wave hit 64 banks), which leaves for memory as whole lines per column.
+constexpr int kTileCols = 64;
 
 struct ColArgs {
     const uint16_t* x; int64_t rows; int32_t cols; int64_t ld_x;
@@ -140,78 +139,93 @@ struct ColArgs {
 };
 
 __device__ __forceinline__ uint4 col_chunk(const ColArgs& p, int64_t row, int col) {
-    if (row < p.rows && col < p.cols) return *reinterpret_cast<const uint4*>(p.x + row * p.ld_x + col);
+    if (row < p.rows && col < p.cols) return load_nt16(p.x + row * p.ld_x + col);
     return make_uint4(0, 0, 0, 0);
 }
+__device__ __forceinline__ void max_words(uint32_t (&m)[4], const uint4 w) {
+    const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+        m[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m[i]),
+                                                                       __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu)));
+}
 
-__device__ __forceinline__ void encode_tile(const ColArgs& p, int64_t row0, int col0, const I8Scale (&sc)[8],
-                                            uint32_t* tile) {
+// Codes of 4 ROWQ rows x 64 columns, whose values are in w (rows row0 + 4 (t / 8) + j,
+// columns col0 + 8 (t % 8)), through the tile.
+template <int ROWQ>
+__device__ __forceinline__ void encode_tile(const ColArgs& p, int64_t row0, int col0, const uint4 (&w)[4],
+                                            const I8Scale (&sc)[8], uint32_t* tile) {
+    constexpr int kStride = ROWQ + 1, kThreads = 8 * ROWQ;
     const int c = threadIdx.x & 7, rq = threadIdx.x >> 3;
-    uint2 w[4];
+    uint2 b[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         float v[8];
-        unpack8(col_chunk(p, row0 + 4 * rq + j, col0 + 8 * c), v);
-        w[j] = i8_codes8<1>(v, sc);
+        unpack8(w[j], v);
+        b[j] = i8_codes8<1>(v, sc);
     }
-    __syncthreads();                        // the tile's last readers are done
 #pragma unroll
     for (int i = 0; i < 8; ++i) {
         const uint32_t sel = (uint32_t)(i & 3) | (uint32_t)(4 + (i & 3)) << 8 | 0x0c0c0000u;
-        const uint32_t a = i < 4 ? w[0].x : w[0].y, b = i < 4 ? w[1].x : w[1].y;
-        const uint32_t d = i < 4 ? w[2].x : w[2].y, e = i < 4 ? w[3].x : w[3].y;
-        tile[(8 * c + i) * kColWords + rq] =
-            __builtin_amdgcn_perm(b, a, sel) | __builtin_amdgcn_perm(e, d, sel) << 16;
+        const uint32_t lo = __builtin_amdgcn_perm(i < 4 ? b[1].x : b[1].y, i < 4 ? b[0].x : b[0].y, sel);
+        const uint32_t hi = __builtin_amdgcn_perm(i < 4 ? b[3].x : b[3].y, i < 4 ? b[2].x : b[2].y, sel);
+        tile[(8 * c + i) * kStride + rq] = lo | hi << 16;
     }
     __syncthreads();
     const int64_t padded = (p.rows + 15) & ~15ll;
+    constexpr int kPieces = ROWQ / 4;               // of sixteen rows, per column
 #pragma unroll
-    for (int u = 0; u < 2; ++u) {
-        const int piece = threadIdx.x + u * 256, col = piece >> 3, at = (piece & 7) * 16;
-        const uint32_t* t = tile + col * kColWords + (at >> 2);
-        if (col0 + col < p.cols && row0 + at < padded)
-            *reinterpret_cast<uint4*>(p.q + (int64_t)(col0 + col) * p.ld_q + row0 + at) = make_uint4(t[0], t[1], t[2], t[3]);
+    for (int u = 0; u < kTileCols * kPieces / kThreads; ++u) {
+        const int piece = threadIdx.x + u * kThreads, col = piece / kPieces, at = piece % kPieces;
+        const uint32_t* t = tile + col * kStride + 4 * at;
+        if (col0 + col < p.cols && row0 + 16 * at < padded)
+            *reinterpret_cast<uint4*>(p.q + (int64_t)(col0 + col) * p.ld_q + row0 + 16 * at) = make_uint4(t[0], t[1], t[2], t[3]);
     }
 }
 
-// Maxima of a thread's eight columns over its rows row0 + (t / 8), + 32, ...
-__device__ __forceinline__ void col_maxima(const ColArgs& p, int64_t row0, int64_t row1, int col0, uint32_t (&m)[4]) {
+// Maxima m of a thread's eight columns, joined over the row lanes t / LC of a
+// workgroup of WAVES waves: the pattern of column t (t < 8 LC).
+template <int LC, int WAVES>
+__device__ __forceinline__ uint32_t join_maxima(uint32_t (&m)[4], uint32_t* lds) {
+    // row lanes of a wave first
 #pragma unroll
-    for (int i = 0; i < 4; ++i) m[i] = 0;
-    const int col = col0 + 8 * (threadIdx.x & 7);
-#pragma unroll 4
-    for (int64_t r = row0 + (threadIdx.x >> 3); r < row1; r += 32) {
-        const uint4 w = col_chunk(p, r, col);
-        const uint32_t v[4] = {w.x, w.y, w.z, w.w};
+    for (int d = LC; d < 64; d <<= 1) {
 #pragma unroll
         for (int i = 0; i < 4; ++i)
             m[i] = __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, m[i]),
-                                                                           __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu)));
+                                                                           __builtin_bit_cast(u16x2, (uint32_t)__shfl_xor((int)m[i], d, 64))));
     }
-}
-// ... joined over the workgroup's 32 row lanes: the pattern of column t (t < 64).
-__device__ __forceinline__ uint32_t join_maxima(const uint32_t (&m)[4], uint32_t* lds) {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    if (lane < LC) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) lds[(threadIdx.x >> 3) * kColWords + 4 * (threadIdx.x & 7) + i] = m[i];
+        for (int i = 0; i < 4; ++i) lds[wave * 4 * LC + 4 * lane + i] = m[i];
+    }
     __syncthreads();
     uint32_t top = 0;
-    if (threadIdx.x < kTileCols) {
-        for (int r = 0; r < 32; ++r) {
-            const uint32_t w = lds[r * kColWords + (threadIdx.x >> 1)];
+    if (threadIdx.x < 8 * LC) {
+#pragma unroll
+        for (int r = 0; r < WAVES; ++r) {
+            const uint32_t w = lds[r * 4 * LC + (threadIdx.x >> 1)];
             top = max(top, (threadIdx.x & 1) ? w >> 16 : w & 0xffffu);
         }
     }
     return top;
 }
 
-// Few rows: a workgroup takes 64 columns whole, maximum first, codes after.
-__global__ void __launch_bounds__(256) k_i8_cols(ColArgs p) {
-    __shared__ uint32_t tile[kTileCols * kColWords];
+// Up to 512 rows: a workgroup holds 64 columns whole, from the one read to the codes.
+constexpr int kFewRows = 512;
+__global__ void __launch_bounds__(1024) k_i8_cols(ColArgs p) {
+    __shared__ uint32_t tile[kTileCols * (kFewRows / 4 + 1)];
+    __shared__ uint32_t part[16 * 32];
     __shared__ float scale[kTileCols];
-    const int col0 = blockIdx.x * kTileCols;
-    uint32_t m[4];
-    col_maxima(p, 0, p.rows, col0, m);
-    const uint32_t top = join_maxima(m, tile);
+    const int col0 = blockIdx.x * kTileCols, c = threadIdx.x & 7, rq = threadIdx.x >> 3;
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = col_chunk(p, 4 * rq + j, col0 + 8 * c);
+    uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int j = 0; j < 4; ++j) max_words(m, w[j]);
+    const uint32_t top = join_maxima<8, 16>(m, part);
     if (threadIdx.x < kTileCols) {
         const float s = i8_scale_of(top);
         scale[threadIdx.x] = s;
@@ -220,39 +234,50 @@ __global__ void __launch_bounds__(256) k_i8_cols(ColArgs p) {
     __syncthreads();
     I8Scale sc[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) sc[i] = i8_scale(scale[8 * (threadIdx.x & 7) + i]);
-    for (int64_t r = 0; r < p.rows; r += kTileRows) encode_tile(p, r, col0, sc, tile);
+    for (int i = 0; i < 8; ++i) sc[i] = i8_scale(scale[8 * c + i]);
+    encode_tile<kFewRows / 4>(p, 0, col0, w, sc, tile);
 }
 
-// Many rows, in three launches: zeros into s; the maxima of runs of kMaxRows
-// rows, joined by integer atomics on the scales' patterns (rounding is monotone,
-// so the largest run's scale is the scale of the maximum, and the order of the
-// joins does not matter; NaN's pattern is above infinity's); the codes.
+// More rows: zeros into s; the maxima of runs of kMaxRows rows, joined by integer
+// atomics on the scales' patterns (the division is monotone, so the largest run's
+// scale is the scale of the maximum, and the order of the joins does not matter; NaN's
+// pattern is above infinity's); the codes.  One workgroup of 1024 per strip of columns
+// without atomics and zeros was slower (4096 x 9728: 33 against 25 + 4 us; 9728 x 2560:
+// 37 against 18 + 4).
 constexpr int kMaxRows = 256;
 __global__ void __launch_bounds__(256) k_i8_zero(float* s, int64_t n) {
     const int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (i < n) s[i] = 0.0f;
 }
 __global__ void __launch_bounds__(256) k_i8_col_max(ColArgs p) {
-    __shared__ uint32_t lds[32 * kColWords];
-    const int col0 = blockIdx.x * kTileCols;
-    const int64_t r0 = (int64_t)blockIdx.y * kMaxRows;
-    uint32_t m[4];
-    col_maxima(p, r0, min(r0 + kMaxRows, p.rows), col0, m);
-    const uint32_t top = join_maxima(m, lds);
+    __shared__ uint32_t part[4 * 32];
+    const int col0 = blockIdx.x * kTileCols, col = col0 + 8 * (threadIdx.x & 7);
+    const int64_t r0 = (int64_t)blockIdx.y * kMaxRows + (threadIdx.x >> 3);
+    uint4 w[kMaxRows / 32];
+#pragma unroll
+    for (int u = 0; u < kMaxRows / 32; ++u) {       // past the last row or column: those again
+        w[u] = *reinterpret_cast<const uint4*>(p.x + min(r0 + 32 * u, p.rows - 1) * p.ld_x + min(col, p.cols - 8));
+    }
+    uint32_t m[4] = {0, 0, 0, 0};
+#pragma unroll
+    for (int u = 0; u < kMaxRows / 32; ++u) max_words(m, w[u]);
+    const uint32_t top = join_maxima<8, 4>(m, part);
     if (threadIdx.x < kTileCols && col0 + (int)threadIdx.x < p.cols)
         atomicMax(reinterpret_cast<uint32_t*>(p.s) + col0 + threadIdx.x, __float_as_uint(i8_scale_of(top)));
 }
+
+// Last launch: the codes, 128 rows x 64 columns per workgroup.
 __global__ void __launch_bounds__(256) k_i8_col_codes(ColArgs p) {
-    __shared__ uint32_t tile[kTileCols * kColWords];
-    const int col0 = blockIdx.x * kTileCols;
+    __shared__ uint32_t tile[kTileCols * 33];
+    const int col0 = blockIdx.x * kTileCols, c = threadIdx.x & 7, rq = threadIdx.x >> 3;
+    const int64_t row0 = (int64_t)blockIdx.y * 128;
+    uint4 w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) w[j] = col_chunk(p, row0 + 4 * rq + j, col0 + 8 * c);
     I8Scale sc[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const int col = col0 + 8 * (threadIdx.x & 7) + i;
-        sc[i] = i8_scale(col < p.cols ? p.s[col] : 0.0f);
-    }
-    encode_tile(p, (int64_t)blockIdx.y * kTileRows, col0, sc, tile);
+    for (int i = 0; i < 8; ++i) sc[i] = i8_scale(p.s[min(col0 + 8 * c + i, p.cols - 1)]);
+    encode_tile<32>(p, row0, col0, w, sc, tile);
 }
 
 }  // namespace
@@ -271,13 +296,15 @@ hipError_t launch_i8_quant_cols(const uint16_t* x, int64_t rows, int64_t cols, i
                                 float* s, hipStream_t st) {
     const ColArgs p{x, rows, (int32_t)cols, ld_x, q, ld_q, s};
     const unsigned strips = (unsigned)((cols + kTileCols - 1) / kTileCols);
-    if (rows <= 512) {
-        hipLaunchKernelGGL(k_i8_cols, dim3(strips), dim3(256), 0, st, p);
+    if (rows <= kFewRows) {
+        hipLaunchKernelGGL(k_i8_cols, dim3(strips), dim3(1024), 0, st, p);
         return hipGetLastError();
     }
     hipLaunchKernelGGL(k_i8_zero, dim3((unsigned)((cols + 255) / 256)), dim3(256), 0, st, s, cols);
     hipLaunchKernelGGL(k_i8_col_max, dim3(strips, (unsigned)((rows + kMaxRows - 1) / kMaxRows)), dim3(256), 0, st, p);
-    hipLaunchKernelGGL(k_i8_col_codes, dim3(strips, (unsigned)((rows + kTileRows - 1) / kTileRows)), dim3(256), 0, st, p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    hipLaunchKernelGGL(k_i8_col_codes, dim3(strips, (unsigned)((rows + 127) / 128)), dim3(256), 0, st, p);
     return hipGetLastError();
 }
 

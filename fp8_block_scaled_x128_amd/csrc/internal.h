@@ -64,7 +64,9 @@ struct I8GemmArgs {
     void* c; int64_t ldc; int out_f32;
     int32_t G; const int32_t* offsets; const int32_t* a_rows;   // G 0: dense
 };
-hipError_t launch_i8_gemm(const I8GemmArgs& g, hipStream_t st);
+// ws: i8_gemm_ws_bytes for the sums of K ranges (dense), or null: no ranges.
+hipError_t launch_i8_gemm(const I8GemmArgs& g, void* ws, hipStream_t st);
+size_t i8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
 // The product of bf16 rows that are few enough to be quantized by every workgroup
 // for itself; g.a and g.sa are not read.
 bool i8_linear_fused(int64_t rows, int64_t cols);

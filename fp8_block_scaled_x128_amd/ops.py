@@ -36,7 +36,7 @@ EXPORTS = ["fp8_quant_rowblock", "fp8_quant_block2d", "fp8_quant_linear", "fp8_q
            "fp8_block_norm", "fp8_block_norm_backward", "fp8_block_norm_backward_ws_size", "mxfp8_quant", "mxfp8_quant_t",
            "fp8_quant_dual_axis", "fp8_transpose_codes", "fp8_quant_linear_pow2",
            "fp8_quant_pow2", "fp8_blockscaled_gemm_pow2", "mxfp8_gemm", "int8_quant",
-           "int8_silu_mul_quant", "int8_gemm", "int8_linear", "int8_linear_ws_size", "int8_grouped_gemm",
+           "int8_silu_mul_quant", "int8_gemm", "int8_gemm_ws_size", "int8_linear", "int8_linear_ws_size", "int8_grouped_gemm",
            "fp8bs_e4m3_encode",
            "fp8bs_status_string", "fp8bs_last_error_detail"]
 
@@ -111,9 +111,10 @@ def load():
             "mxfp8_gemm": [I64, I64, I64, I32, P, P, I64, P, I64, P, I64, P, I64, I64, P, I64, I64, P, I64, INT, P],
             "int8_quant": [P, I64, I64, I64, INT, P, I64, P, P],
             "int8_silu_mul_quant": [P, I64, I64, I64, P, P, I64, P, P, I64, P],
-            "int8_gemm": [I64, I64, I64, P, I64, P, P, I64, P, P, I64, INT, P],
+            "int8_gemm": [I64, I64, I64, P, I64, P, P, I64, P, P, I64, INT, P, ctypes.c_size_t, P],
+            "int8_gemm_ws_size": [I64, I64, I64, P],
             "int8_linear": [I64, I64, I64, P, I64, P, I64, P, P, I64, INT, P, ctypes.c_size_t, P],
-            "int8_linear_ws_size": [I64, I64, P],
+            "int8_linear_ws_size": [I64, I64, I64, P],
             "int8_grouped_gemm": [I64, I64, I64, I32, P, P, I64, P, I64, P, P, I64, I64, P, I64, P, I64, INT, P],
             "fp8bs_e4m3_encode": [P, P, I64, P],
         }
@@ -426,9 +427,17 @@ def int8_silu_mul_quant(gate_up, rows, I, ld_in, live_rows, q, ld_q, s, h_out, l
     return _check("int8_silu_mul_quant", st, raise_on_error)
 
 
-def int8_gemm(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, out, stream=None, raise_on_error=True):
-    st = load().int8_gemm(M, N, K, _p(a), lda, _p(sa), _p(b), ldb, _p(sb), _p(c), ldc, out, _stream(stream))
+def int8_gemm(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, out, ws, ws_bytes, stream=None, raise_on_error=True):
+    st = load().int8_gemm(M, N, K, _p(a), lda, _p(sa), _p(b), ldb, _p(sb), _p(c), ldc, out, _p(ws), ws_bytes,
+                          _stream(stream))
     return _check("int8_gemm", st, raise_on_error)
+
+
+def int8_gemm_ws_size(M, N, K):
+    """Workspace bytes that int8_gemm has use for (host only)."""
+    out = ctypes.c_size_t(0)
+    _check("int8_gemm_ws_size", load().int8_gemm_ws_size(M, N, K, ctypes.byref(out)))
+    return out.value
 
 
 def int8_linear(rows, N, cols, x, ld_x, w, ld_w, sw, y, ld_y, out, ws, ws_bytes, stream=None, raise_on_error=True):
@@ -437,10 +446,10 @@ def int8_linear(rows, N, cols, x, ld_x, w, ld_w, sw, y, ld_y, out, ws, ws_bytes,
     return _check("int8_linear", st, raise_on_error)
 
 
-def int8_linear_ws_size(rows, cols):
+def int8_linear_ws_size(rows, N, cols):
     """Workspace bytes of int8_linear (host only)."""
     out = ctypes.c_size_t(0)
-    _check("int8_linear_ws_size", load().int8_linear_ws_size(rows, cols, ctypes.byref(out)))
+    _check("int8_linear_ws_size", load().int8_linear_ws_size(rows, N, cols, ctypes.byref(out)))
     return out.value
 
 
@@ -1055,17 +1064,22 @@ def i8_quant(x, axis: int = AXIS_ROW, out=None):
     return out
 
 
-def i8_gemm(a, sa, b, sb, out_dtype=torch.bfloat16, out=None):
+def i8_gemm(a, sa, b, sb, out_dtype=torch.bfloat16, out=None, ws=None):
     """C [M, N] = diag(sa) (A B^T) diag(sb) for int8 codes a [M, K], b [N, K] and
-    fp32 scales sa [M], sb [N] (see int8_gemm)."""
+    fp32 scales sa [M], sb [N] (see int8_gemm).  ws: int8_gemm_ws_size bytes (uint8);
+    made here where the call has use for it."""
     (M, K), N, dev = a.shape, b.shape[0], _device()
     ap, lda = _mat("a", a, M, K, dev, _I8)
     bp, ldb = _mat("b", b, N, K, dev, _I8)
     if out is None:
         out = torch.empty((M, N), dtype=out_dtype, device=a.device)
     cp, ldc = _mat("out", out, M, N, dev, out_dtype)
+    if ws is None:
+        need = int8_gemm_ws_size(M, N, K)
+        ws = _u8((need,), a.device) if need else None
+    wsp, wsn = _workspace(ws, dev)
     st = load().int8_gemm(M, N, K, ap, lda, _arr("sa", sa, (M,), dev, _F32), bp, ldb, _arr("sb", sb, (N,), dev, _F32),
-                          cp, ldc, _otype(out_dtype), _stream())
+                          cp, ldc, _otype(out_dtype), wsp, wsn, _stream())
     if st:
         _check("int8_gemm", st)
     return out
@@ -1087,7 +1101,7 @@ def i8_linear(x, qw, sw, out_dtype=torch.bfloat16, out: Optional[I8Linear] = Non
     wp, ld_w = _mat("qw", qw, N, _pad16(cols), dev, _I8)
     if out is None:
         out = I8Linear(torch.empty((rows, N), dtype=out_dtype, device=x.device),
-                       _u8((int8_linear_ws_size(rows, cols),), x.device))
+                       _u8((int8_linear_ws_size(rows, N, cols),), x.device))
     yp, ld_y = _mat("out.y", out.y, rows, N, dev, out_dtype)
     wsp, wsn = _workspace(out.ws, dev)
     st = load().int8_linear(rows, N, cols, xp, ld_x, wp, ld_w, _arr("sw", sw, (N,), dev, _F32), yp, ld_y,
@@ -1105,11 +1119,13 @@ def i8_linear_forward(x, w, out_dtype=torch.bfloat16):
 
 
 class I8LinearGrads(NamedTuple):
-    """Outputs of i8_linear_backward; codes and scales are its workspaces: (q, s)
-    of dY per token, dY per output channel, W and X per input channel."""
+    """Outputs of i8_linear_backward and its workspaces: codes and scales (q, s) of
+    dY per token, dY per output channel, W and X per input channel, and what the
+    product needs."""
     dx: torch.Tensor
     dw: torch.Tensor
     codes: tuple
+    ws: Optional[torch.Tensor]
 
 
 def i8_linear_backward(dy, saved, out: Optional[I8LinearGrads] = None) -> I8LinearGrads:
@@ -1124,13 +1140,14 @@ def i8_linear_backward(dy, saved, out: Optional[I8LinearGrads] = None) -> I8Line
                                                                               tuple(x.shape)))
     if out is None:
         e = lambda r, c: torch.empty((r, c), dtype=_F32, device=dy.device)
-        out = I8LinearGrads(e(T, I), e(O, I), (None,) * 4)
+        need = max(int8_gemm_ws_size(T, I, _pad16(O)), int8_gemm_ws_size(O, I, _pad16(T)))
+        out = I8LinearGrads(e(T, I), e(O, I), (None,) * 4, _u8((need,), dy.device) if need else None)
     dyr, dyc, wc, xc = out.codes
     dyr, dyc = i8_quant(dy, AXIS_ROW, dyr), i8_quant(dy, AXIS_COL, dyc)
     wc, xc = i8_quant(w, AXIS_COL, wc), i8_quant(x, AXIS_COL, xc)
-    i8_gemm(*dyr, *wc, _F32, out.dx)
-    i8_gemm(*dyc, *xc, _F32, out.dw)
-    return I8LinearGrads(out.dx, out.dw, (dyr, dyc, wc, xc))
+    i8_gemm(*dyr, *wc, _F32, out.dx, out.ws)
+    i8_gemm(*dyc, *xc, _F32, out.dw, out.ws)
+    return I8LinearGrads(out.dx, out.dw, (dyr, dyc, wc, xc), out.ws)
 
 
 def i8_grouped_gemm(a, sa, b, sb, offsets, row_token=None, out_dtype=torch.bfloat16, out=None):

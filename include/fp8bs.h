@@ -939,13 +939,19 @@ fp8bs_status int8_silu_mul_quant(const uint16_t* gate_up, int64_t rows, int64_t 
  *
  * a : int8 [M][lda], sa fp32 [M];  b : int8 [N][ldb], sb fp32 [N], K contiguous.
  * c : [M][ldc], bf16 or fp32 per `out`.
+ * ws : nullable device workspace of int8_gemm_ws_size bytes, 16-byte aligned: with it
+ *      a product of few rows and a long K is computed in ranges of K (the results are
+ *      the same bits); contents on entry are ignored.  Calls that overlap in time need
+ *      separate workspaces.
  * Requirements: M, N >= 0; 0 <= K <= 131056; K % 16 == 0 (int8_quant pads codes
  * with zeros); N % 8 == 0; lda, ldb >= K, % 16 == 0, a and b 16-byte aligned and
  * below 4 GiB each; ldc >= N, ldc % 8 == 0, c 16-byte aligned.
  * ------------------------------------------------------------------------ */
 fp8bs_status int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* sa,
                        const int8_t* b, int64_t ldb, const float* sb, void* c, int64_t ldc, fp8bs_out out,
-                       hipStream_t stream);
+                       void* ws, size_t ws_bytes, hipStream_t stream);
+/* Host only: the workspace int8_gemm has use for (0: none). */
+fp8bs_status int8_gemm_ws_size(int64_t M, int64_t N, int64_t K, size_t* bytes);
 
 /* ------------------------------------------------------------------------
  * int8_linear -- Y = X W^T with X bf16 quantized per token on the way (int8_quant,
@@ -962,7 +968,7 @@ fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* 
                          int64_t ld_w, const float* sw, void* y, int64_t ld_y, fp8bs_out out, void* ws,
                          size_t ws_bytes, hipStream_t stream);
 /* Host only: the workspace int8_linear needs. */
-fp8bs_status int8_linear_ws_size(int64_t rows, int64_t cols, size_t* bytes);
+fp8bs_status int8_linear_ws_size(int64_t rows, int64_t N, int64_t cols, size_t* bytes);
 
 /* ------------------------------------------------------------------------
  * int8_grouped_gemm -- int8_gemm over G expert groups of rows: row r of group g
@@ -972,6 +978,7 @@ fp8bs_status int8_linear_ws_size(int64_t rows, int64_t cols, size_t* bytes);
  *
  * b : expert g's [N][ldb] codes at b + g * b_stride_g, its scales at
  *     sb + g * sb_stride_g.
+ * There is no workspace.
  * Requirements: as int8_gemm; 1 <= G <= 65535; b_stride_g >= 0, % 16 == 0;
  * sb_stride_g >= 0.
  * ------------------------------------------------------------------------ */

@@ -36,8 +36,8 @@ def test_silu_refuses(want, a):
     assert silu(**a) == want
 
 
-def gemm(M=4, N=64, K=64, a=P, lda=64, sa=P, b=P, ldb=64, sb=P, c=P, ldc=64, out=0):
-    return ops.int8_gemm(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, out, stream=0, raise_on_error=False)
+def gemm(M=4, N=64, K=64, a=P, lda=64, sa=P, b=P, ldb=64, sb=P, c=P, ldc=64, out=0, ws=None, wsn=0):
+    return ops.int8_gemm(M, N, K, a, lda, sa, b, ldb, sb, c, ldc, out, ws, wsn, stream=0, raise_on_error=False)
 
 
 PRODUCT = [(SHAPE, dict(M=-1)), (SHAPE, dict(K=72, lda=80, ldb=80)), (SHAPE, dict(N=60)),
@@ -49,9 +49,21 @@ PRODUCT = [(SHAPE, dict(M=-1)), (SHAPE, dict(K=72, lda=80, ldb=80)), (SHAPE, dic
            (SHAPE, dict(ldb=GIB4 // 64))]
 
 
-@pytest.mark.parametrize("want,a", PRODUCT)
+@pytest.mark.parametrize("want,a", PRODUCT + [(ALIGN, dict(ws=P + 8, wsn=1 << 20)),
+                                              (SHAPE, dict(M=64, K=1024, lda=1024, ldb=1024, ws=P, wsn=16))])
 def test_gemm_refuses(want, a):
     assert gemm(**a) == want
+
+
+def test_workspace_sizes():
+    assert ops.int8_gemm_ws_size(0, 64, 64) == 0 and ops.int8_gemm_ws_size(4096, 9728, 2560) == 0
+    n = ops.int8_gemm_ws_size(64, 2560, 9728)
+    assert n > 0 and n % (64 * 2560 * 4) == 0
+    for bad in ((-1, 8, 16), (8, -8, 16), (8, 8, -16), (8, 8, 131072), (1 << 31, 8, 16)):
+        with pytest.raises(ops.Fp8bsError):
+            ops.int8_gemm_ws_size(*bad)
+        with pytest.raises(ops.Fp8bsError):
+            ops.int8_linear_ws_size(*bad)
 
 
 def grouped(M=4, N=64, K=64, G=2, offsets=P, rows=None, count=0, a=P, lda=64, sa=P, b=P, ldb=64, bsg=4096, sb=P, ssg=64,
@@ -83,7 +95,7 @@ def test_linear_refuses(want, a):
 def test_empty_calls_need_no_device():
     assert quant(rows=0) == 0 and quant(axis=1, cols=0, ld=0) == 0 and silu(rows=0) == 0
     assert gemm(M=0) == 0 and gemm(N=0) == 0 and grouped(M=0) == 0 and linear(rows=0) == 0
-    assert ops.int8_linear_ws_size(0, 64) == 0 and ops.int8_linear_ws_size(5, 40) == 32 + 5 * 48
+    assert ops.int8_linear_ws_size(0, 8, 64) == 0 and ops.int8_linear_ws_size(5, 8, 40) == 32 + 5 * 48
 
 
 def test_reference_codes():
