@@ -1185,7 +1185,7 @@ fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* 
     if ((v = check_device()) != FP8BS_OK) return v;
     const I8GemmArgs g{rows, N, K, qx, K, sx, reinterpret_cast<const uint8_t*>(w), ld_w, 0, sw, 0, y, ld_y,
                        out == FP8BS_OUT_FP32, 0, nullptr, nullptr};
-    if (i8_linear_fused(rows, cols)) return launched(launch_i8_linear_fused(g, x, ld_x, cols, stream), "int8_linear");
+    if (i8_linear_fused(rows, cols)) return launched(launch_i8_linear_fused(g, x, cols, stream), "int8_linear");
     const hipError_t e = launch_i8_quant_rows(x, rows, cols, ld_x, qx, K, sx, stream);
     return launched(e != hipSuccess ? e : launch_i8_gemm(g, qx + (size_t)rows * K, stream), "int8_linear");
 }

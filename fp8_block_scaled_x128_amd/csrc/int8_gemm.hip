@@ -520,7 +520,10 @@ __device__ __forceinline__ void join_waves(const I8Args& p, const i32x4 (&acc)[M
     }
 }
 
-// U runs in flight.  Grouped: grid row y is a group; its rows go in passes of 16 MT.
+// Up to U runs in flight: passes of U, then one of the runs that are left, so that no
+// load is made in vain (a kernel that read the last 16 bytes again instead took 91 us
+// where this takes 63 on 110 groups of 1536 x 2048 weights).  Grouped: grid row y is a
+// group, whose rows go in passes of 16 MT; dense: grid row y is such a pass.
 template <int MT, int W, int U, bool GROUPED, bool GATHER, bool OUT32>
 __global__ void __launch_bounds__(64 * W) k_i8_stream(I8Args p) {
     __shared__ __attribute__((aligned(16))) i32x4 part[W * MT * 64];
@@ -535,6 +538,9 @@ __global__ void __launch_bounds__(64 * W) k_i8_stream(I8Args p) {
         m1 = p.offsets[blockIdx.y + 1];
         b += (int64_t)blockIdx.y * p.b_sg;
         sb += (int64_t)blockIdx.y * p.sb_sg;
+    } else {
+        m0 = blockIdx.y * 16 * MT;
+        m1 = min(m1, m0 + 16 * MT);
     }
     const uint8_t* brow = b + (int64_t)min(n0 + r16, p.N - 1) * p.ldb;
     for (; m0 < m1; m0 += 16 * MT) {
@@ -548,96 +554,126 @@ __global__ void __launch_bounds__(64 * W) k_i8_stream(I8Args p) {
         i32x4 acc[MT];
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[j] = i32x4{0, 0, 0, 0};
-        for (int k = wave * kRun; k < p.K; k += W * U * kRun) {
-            Run fb[U], fa[U][MT];
+        auto pass = [&](auto count, int k) {
+            constexpr int C = decltype(count)::value;
+            Run fb[C], fa[C][MT];
 #pragma unroll
-            for (int u = 0; u < U; ++u) {
+            for (int u = 0; u < C; ++u) {
                 fb[u] = weight_run(brow, k + u * W * kRun, p.K, q);
 #pragma unroll
                 for (int j = 0; j < MT; ++j) fa[u][j] = act_run(arow[j], k + u * W * kRun, p.K, q);
             }
 #pragma unroll
-            for (int u = 0; u < U; ++u)
+            for (int u = 0; u < C; ++u)
 #pragma unroll
                 for (int j = 0; j < MT; ++j)
                     acc[j] = mfma(fb[u].hi, fa[u][j].hi, mfma(fb[u].lo, fa[u][j].lo, acc[j]));
-        }
+        };
+        int k = wave * kRun, left = ((p.K + kRun - 1) / kRun - wave + W - 1) / W;
+        for (; left >= U; left -= U, k += U * W * kRun) pass(std::integral_constant<int, U>{}, k);
+        unrolled<U - 1>([&](auto c) {
+            if (left == decltype(c)::value + 1) pass(std::integral_constant<int, decltype(c)::value + 1>{}, k);
+        });
         join_waves<MT, W, GATHER, OUT32>(p, acc, part, m0, m1, n0, p.sa, sb);
         __syncthreads();
     }
 }
 
-// The same for a few bf16 rows that every workgroup quantizes for itself into LDS
-// (kFusedCodes of them at most: a second or so of L2 reads in the shadow of the first
-// weights), which saves the launch before.
-constexpr int kFusedRows = 16, kFusedCodes = 16384;
-template <int W, int U, bool OUT32>
-__global__ void __launch_bounds__(64 * W) k_i8_stream_x(I8Args p, const uint16_t* x, int64_t ld_x, int32_t cols) {
-    constexpr int kChunks = kFusedCodes / 8 / (64 * W);     // chunks of eight values per thread
-    __shared__ __attribute__((aligned(16))) uint8_t codes[kFusedCodes + 15 * kFusedRows];
-    __shared__ __attribute__((aligned(16))) i32x4 part[W * 64];
-    __shared__ uint32_t top[kFusedRows];
-    __shared__ float scale[kFusedRows];
-    const int lane = threadIdx.x & 63;
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int q = lane >> 4, r16 = lane & 15, n0 = blockIdx.x * 16;
-    const uint8_t* brow = p.b + (int64_t)min(n0 + r16, p.N - 1) * p.ldb;
-    const int chunks = cols / 8, all = p.M * chunks;
-    uint4 w[kChunks];
-    int row[kChunks];
+// One or two rows (decode).  A wave takes R whole rows of weights, a kilobyte of each
+// at a time and up to P in flight, and multiplies them by every activation row with
+// v_dot4: reading whole rows is what pays (25 MB cold: 5.3 us, in the fragments of a
+// matrix instruction 7.4), and 16 cycles per kilobyte and row hide behind the reads.
+// FUSED: one row that comes in bf16 and that every workgroup quantizes for itself into
+// LDS (kFusedCodes at most) in the shadow of its first weights, which saves a launch.
+constexpr int kFusedCodes = 16384;
+template <int MT, int R, int P, int W, bool FUSED, bool OUT32>
+__global__ void __launch_bounds__(64 * W) k_i8_dot(I8Args p, const uint16_t* x, int32_t cols) {
+    static_assert(MT == 1 || !FUSED, "one row");
+    constexpr int kChunks = FUSED ? kFusedCodes / 8 / (64 * W) : 1;     // chunks of eight values per thread
+    __shared__ __attribute__((aligned(16))) uint8_t codes[FUSED ? kFusedCodes : 16];
+    __shared__ uint32_t top[W];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n0 = (blockIdx.x * W + wave) * R;
+    const uint8_t* brow = p.b + (int64_t)min(n0, p.N - R) * p.ldb;
+    i32x4 w[R][P];
+    int pieces = (p.K + 1023) / 1024;
+    auto load = [&](int k) {
+        unrolled<P>([&](auto c) {
+            constexpr int i = decltype(c)::value;
+            if (i < pieces)
 #pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int c = threadIdx.x + i * 64 * W;
-        row[i] = c / chunks;
-        w[i] = make_uint4(0, 0, 0, 0);
-        if (c < all) w[i] = *reinterpret_cast<const uint4*>(x + (int64_t)row[i] * ld_x + (c - row[i] * chunks) * 8);
-    }
-    Run fb[U];
+                for (int r = 0; r < R; ++r)
+                    w[r][i] = *reinterpret_cast<const i32x4*>(brow + r * p.ldb + min(k + 1024 * i + 16 * lane, p.K - 16));
+        });
+    };
+    load(0);
+    float scale = 0;
+    if constexpr (FUSED) {
+        const int chunks = cols / 8;
+        uint4 v[kChunks];
+        u16x2 m = {0, 0};
 #pragma unroll
-    for (int u = 0; u < U; ++u) fb[u] = weight_run(brow, (wave + u * W) * kRun, p.K, q);
-    if (threadIdx.x < kFusedRows) top[threadIdx.x] = 0;
-    __syncthreads();
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const u16x2 m = absmax_bits(u16x2{0, 0}, w[i]);
-        // a wave's chunks are mostly of one row: its maximum goes to LDS once
-        const int first = __builtin_amdgcn_readfirstlane(row[i]);
-        const uint32_t mine = max((uint32_t)m.x, (uint32_t)m.y);
-        const uint32_t both = lanes_umax<64>(row[i] == first ? mine : 0u);
-        if (lane == 0 && first < p.M) atomicMax(&top[first], both);
-        if (row[i] != first && row[i] < p.M) atomicMax(&top[row[i]], mine);
-    }
-    __syncthreads();
-    if (threadIdx.x < p.M) scale[threadIdx.x] = i8_scale_of(top[threadIdx.x]);
-#pragma unroll
-    for (int i = 0; i < kChunks; ++i) {
-        const int c = threadIdx.x + i * 64 * W;
-        if (c < all) {
-            const I8Scale sc = i8_scale(i8_scale_of(top[row[i]]));
-            float v[8];
-            unpack8(w[i], v);
-            uint8_t* to = codes + row[i] * p.K + (c - row[i] * chunks) * 8;
-            *reinterpret_cast<uint2*>(to) = i8_codes8<0>(v, &sc);
-            if (p.K != cols && (c + 1) % chunks == 0) *reinterpret_cast<uint2*>(to + 8) = make_uint2(0, 0);
+        for (int i = 0; i < kChunks; ++i) {
+            v[i] = make_uint4(0, 0, 0, 0);
+            const int c = threadIdx.x + i * 64 * W;
+            if (c < chunks) v[i] = *reinterpret_cast<const uint4*>(x + c * 8);
+            m = absmax_bits(m, v[i]);
         }
-    }
-    __syncthreads();
-    const uint8_t* arow = codes + min(r16, p.M - 1) * p.K;
-    i32x4 acc[1] = {i32x4{0, 0, 0, 0}};
-    for (int k = wave * kRun; k < p.K; k += W * U * kRun) {
-        Run now[U];
+        const uint32_t mine = lanes_umax<64>(max((uint32_t)m.x, (uint32_t)m.y));
+        if (lane == 0) top[wave] = mine;
+        __syncthreads();
+        uint32_t all = top[0];
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            now[u] = fb[u];
-            fb[u] = weight_run(brow, k + (u + U) * W * kRun, p.K, q);
-        }
+        for (int i = 1; i < W; ++i) all = max(all, top[i]);
+        scale = i8_scale_of(all);
+        const I8Scale sc = i8_scale(scale);
 #pragma unroll
-        for (int u = 0; u < U; ++u) {
-            const Run fa = act_run(arow, k + u * W * kRun, p.K, q);
-            acc[0] = mfma(now[u].hi, fa.hi, mfma(now[u].lo, fa.lo, acc[0]));
+        for (int i = 0; i < kChunks; ++i) {
+            const int c = threadIdx.x + i * 64 * W;
+            if (c >= p.K / 8) break;                            // past cols: zeros
+            float f[8];
+            unpack8(v[i], f);
+            *reinterpret_cast<uint2*>(codes + c * 8) = i8_codes8<0>(f, &sc);
         }
+        __syncthreads();
     }
-    join_waves<1, W, false, OUT32>(p, acc, part, 0, p.M, n0, scale, p.sb);
+    int acc[R][MT] = {};
+    for (int k = 0;;) {
+        unrolled<P>([&](auto c) {
+            constexpr int i = decltype(c)::value;
+            if (i >= pieces) return;
+            const int at = k + 1024 * i + 16 * lane;
+#pragma unroll
+            for (int m = 0; m < MT; ++m) {
+                const uint8_t* row = FUSED ? codes : p.a + m * p.lda;
+                i32x4 a = *reinterpret_cast<const i32x4*>(row + min(at, p.K - 16));
+                if (at >= p.K) a = i32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int r = 0; r < R; ++r)
+#pragma unroll
+                    for (int b = 0; b < 4; ++b) acc[r][m] = __builtin_amdgcn_sdot4(w[r][i][b], a[b], acc[r][m], false);
+            }
+        });
+        pieces -= P;
+        if (pieces <= 0) break;
+        k += 1024 * P;
+        load(k);
+    }
+    // output m * R + r on lane m * R + r
+    int sum = 0;
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+            const int v = (int)lanes_usum((uint32_t)acc[r][m]);
+            sum = lane == m * R + r ? v : sum;
+        }
+    const int m = lane / R, n = n0 + lane % R;
+    if (m < MT && n < p.N) {
+        const float f = (float)sum * (FUSED ? scale : p.sa[m]) * p.sb[n];
+        if (OUT32) static_cast<float*>(p.c)[m * p.ldc + n] = f;
+        else static_cast<uint16_t*>(p.c)[m * p.ldc + n] = (uint16_t)pack_bf16x2(f, f);
+    }
 }
 
 // The K ranges' sums [splits][M][N], added, scaled and stored: four outputs a thread.
@@ -667,12 +703,21 @@ hipError_t tile(const I8Args& p, bool out32, hipStream_t st) {
     return hipGetLastError();
 }
 
+// Products of so little work (M N K) that tiles of 128 x 128 leave most compute units
+// idle, or wait for each slice: 205 x 1008 by 1512 6.0 us in the waves' K ranges and 8.6
+// in tiles, 128 x 2048 by 2560 10.9 and 12.2, 32 x 4096 by 4096 8.4 and 11.7 (K split);
+// past it 205 x 2048 by 2560 14 and 12.2, 32 x 2560 by 9728 16.2 and 13.7.
+bool little(int64_t M, int64_t N, int64_t K) { return M * N * K <= 640000000; }
+
 // K ranges for products with few tiles and a long K: tiles of 64 x 128, about two for
-// each compute unit, of four slices at least.
+// each compute unit, of four slices at least.  The join and the sums' way through
+// memory cost as much as 16 slices, so as many are to be saved: 64 x 9728 by 2560 16 us
+// for 45, 205 x 4096 by 4096 19.6 for 20.2; 333 x 2048 by 2560 would take 17.2 for 12.4.
 int split_count(int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = (M + 63) / 64 * ((N + 127) / 128), nk = (K + BK - 1) / BK;
-    if (M <= 16 || M > 512 || tiles >= 256 || nk < 16) return 1;
-    return (int)std::max<int64_t>(1, std::min<int64_t>(2 * kCUs / tiles, nk / 4));
+    if (M <= 16 || M > 512 || tiles >= 256 || little(M, N, K)) return 1;
+    const int64_t n = std::min<int64_t>(2 * kCUs / tiles, nk / 4);
+    return n > 1 && nk - nk / n >= 16 ? (int)n : 1;
 }
 
 hipError_t split(I8Args p, bool out32, int splits, void* ws, hipStream_t st) {
@@ -693,21 +738,49 @@ hipError_t split(I8Args p, bool out32, int splits, void* ws, hipStream_t st) {
 
 template <int MT, int W, int U, bool GROUPED, bool GATHER>
 hipError_t stream(const I8Args& p, bool out32, hipStream_t st) {
-    const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)(GROUPED ? p.G : 1));
+    const dim3 grid((unsigned)((p.N + 15) / 16), (unsigned)(GROUPED ? p.G : (p.M + 16 * MT - 1) / (16 * MT)));
     if (out32) hipLaunchKernelGGL((k_i8_stream<MT, W, U, GROUPED, GATHER, true>), grid, dim3(64 * W), 0, st, p);
     else hipLaunchKernelGGL((k_i8_stream<MT, W, U, GROUPED, GATHER, false>), grid, dim3(64 * W), 0, st, p);
     return hipGetLastError();
 }
 
-template <bool GROUPED, bool GATHER>
-hipError_t launch(const I8Args& p, bool out32, hipStream_t st) {
-    // rows per product, or on average per group
-    const int64_t rows = GROUPED ? ((int64_t)p.M + p.G - 1) / p.G : p.M;
-    if (rows <= 16) return stream<1, 8, 4, GROUPED, GATHER>(p, out32, st);
-    if (rows <= 64 && (GROUPED || p.K <= 2048)) return stream<4, 16, 2, GROUPED, GATHER>(p, out32, st);
+template <int MT, int R, int P, int W, bool FUSED>
+hipError_t dot(const I8Args& p, bool out32, const uint16_t* x, int64_t cols, hipStream_t st) {
+    const dim3 grid((unsigned)((p.N + W * R - 1) / (W * R)));
+    if (out32) hipLaunchKernelGGL((k_i8_dot<MT, R, P, W, FUSED, true>), grid, dim3(64 * W), 0, st, p, x, (int32_t)cols);
+    else hipLaunchKernelGGL((k_i8_dot<MT, R, P, W, FUSED, false>), grid, dim3(64 * W), 0, st, p, x, (int32_t)cols);
+    return hipGetLastError();
+}
+template <int MT, int W, bool FUSED>
+hipError_t dot(const I8Args& p, bool out32, const uint16_t* x, int64_t cols, hipStream_t st) {
+    if (p.K > 5120) return dot<MT, 1, 10, W, FUSED>(p, out32, x, cols, st);
+    return dot<MT, 2, 5, W, FUSED>(p, out32, x, cols, st);
+}
+
+hipError_t launch_dense(const I8Args& p, bool out32, hipStream_t st) {
+    if (p.M == 1) return dot<1, 4, false>(p, out32, nullptr, 0, st);
+    if (p.M == 2) return dot<2, 4, false>(p, out32, nullptr, 0, st);
+    if (p.M <= 16)      // four waves where they have all their runs in flight at once
+        return p.K <= 2560 ? stream<1, 4, 5, false, false>(p, out32, st) : stream<1, 16, 5, false, false>(p, out32, st);
+    if (little(p.M, p.N, p.K))      // passes of 32 rows, or of 64 where one holds all (64 x 2048 by 2560 7.2 us, 8.2)
+        return p.M > 32 && p.M <= 64 ? stream<4, 8, 2, false, false>(p, out32, st) : stream<2, 8, 3, false, false>(p, out32, st);
+    // tiles of 256 x 256 where half of the compute units have one
     const int64_t big = ((int64_t)p.M + 255) / 256 * ((p.N + 255) / 256);
-    if (big >= 128) return tile<4, 4, GROUPED, GATHER>(p, out32, st);
-    return tile<2, 2, GROUPED, GATHER>(p, out32, st);
+    return big >= 128 ? tile<4, 4, false, false>(p, out32, st) : tile<2, 2, false, false>(p, out32, st);
+}
+
+// By the rows of a group on average.  128 groups of 1536 x 2048 weights, in us:
+//   rows per group     1    2    4    8   16   32   64  128  256
+//   stream            38   58   72   90  124  209
+//   tile 64 x 128     38   66   73   74   78   79  104  142  232
+//   tile 128 x 128    41   73   77   82   82   81   90  122  203
+//   tile 256 x 256    59  102  106  102  103  108  113  122  178
+template <bool GATHER>
+hipError_t launch_grouped(const I8Args& p, bool out32, hipStream_t st) {
+    const int64_t rows = ((int64_t)p.M + p.G - 1) / p.G;
+    if (rows <= 4) return stream<1, 4, 4, true, GATHER>(p, out32, st);
+    if (rows <= 32) return tile<1, 2, true, GATHER>(p, out32, st);
+    return rows < 128 ? tile<2, 2, true, GATHER>(p, out32, st) : tile<4, 4, true, GATHER>(p, out32, st);
 }
 
 }  // namespace
@@ -723,20 +796,17 @@ hipError_t launch_i8_gemm(const I8GemmArgs& g, void* ws, hipStream_t st) {
                    g.c, g.ldc, g.G, g.offsets, g.a_rows, 1};
     if (g.G == 0) {
         const int n = ws ? split_count(g.M, g.N, g.K) : 1;
-        return n > 1 ? split(p, g.out_f32, n, ws, st) : launch<false, false>(p, g.out_f32, st);
+        return n > 1 ? split(p, g.out_f32, n, ws, st) : launch_dense(p, g.out_f32, st);
     }
-    return g.a_rows ? launch<true, true>(p, g.out_f32, st) : launch<true, false>(p, g.out_f32, st);
+    return g.a_rows ? launch_grouped<true>(p, g.out_f32, st) : launch_grouped<false>(p, g.out_f32, st);
 }
 
-bool i8_linear_fused(int64_t rows, int64_t cols) { return rows <= kFusedRows && rows * cols <= kFusedCodes && cols > 0; }
+bool i8_linear_fused(int64_t rows, int64_t cols) { return rows == 1 && cols <= kFusedCodes && cols > 0; }
 
-hipError_t launch_i8_linear_fused(const I8GemmArgs& g, const uint16_t* x, int64_t ld_x, int64_t cols, hipStream_t st) {
+hipError_t launch_i8_linear_fused(const I8GemmArgs& g, const uint16_t* x, int64_t cols, hipStream_t st) {
     const I8Args p{(int32_t)g.M, (int32_t)g.N, (int32_t)g.K, nullptr, 0, nullptr, g.b, g.ldb, 0, g.sb, 0, g.c, g.ldc, 0,
                    nullptr, nullptr, 1};
-    const dim3 grid((unsigned)((g.N + 15) / 16));
-    if (g.out_f32) hipLaunchKernelGGL((k_i8_stream_x<8, 4, true>), grid, dim3(512), 0, st, p, x, ld_x, (int32_t)cols);
-    else hipLaunchKernelGGL((k_i8_stream_x<8, 4, false>), grid, dim3(512), 0, st, p, x, ld_x, (int32_t)cols);
-    return hipGetLastError();
+    return dot<1, 8, true>(p, g.out_f32, x, cols, st);
 }
 
 }  // namespace fp8bs

@@ -70,7 +70,7 @@ size_t i8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
 // The product of bf16 rows that are few enough to be quantized by every workgroup
 // for itself; g.a and g.sa are not read.
 bool i8_linear_fused(int64_t rows, int64_t cols);
-hipError_t launch_i8_linear_fused(const I8GemmArgs& g, const uint16_t* x, int64_t ld_x, int64_t cols, hipStream_t st);
+hipError_t launch_i8_linear_fused(const I8GemmArgs& g, const uint16_t* x, int64_t cols, hipStream_t st);
 
 // moe.hip
 hipError_t launch_moe_combine(const uint16_t* y, int64_t rows, int64_t H, int64_t ld_y, const int32_t* pos,

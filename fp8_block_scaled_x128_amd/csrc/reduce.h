@@ -127,6 +127,14 @@ __device__ __forceinline__ float lanes_sum(float v) {
     }
     return v;
 }
+// Sum of a wave's 64 integers.
+__device__ __forceinline__ uint32_t lanes_usum(uint32_t v) {
+    v += dpp_mov<kDppXor1>(v);
+    v += dpp_mov<kDppXor2>(v);
+    v += dpp_mov<kDppHalfMirror>(v);
+    v += dpp_mov<kDppMirror>(v);
+    return lane_value(v, 0) + lane_value(v, 16) + lane_value(v, 32) + lane_value(v, 48);
+}
 template <int LANES>
 __device__ __forceinline__ uint32_t lanes_umax(uint32_t v) {
     v = row16_umax(v);
