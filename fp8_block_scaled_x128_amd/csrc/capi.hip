@@ -1,6 +1,7 @@
 // C ABI of libfp8bs: argument validation, device check and dispatch to the
 // kernel launchers.  Declarations and the contract of every entry point are
 // in include/fp8bs.h.
+#include <algorithm>
 #include <atomic>
 #include <cstdarg>
 #include <cstdio>
@@ -1188,6 +1189,84 @@ fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* 
     if (i8_linear_fused(rows, cols)) return launched(launch_i8_linear_fused(g, x, cols, stream), "int8_linear");
     const hipError_t e = launch_i8_quant_rows(x, rows, cols, ld_x, qx, K, sx, stream);
     return launched(e != hipSuccess ? e : launch_i8_gemm(g, qx + (size_t)rows * K, stream), "int8_linear");
+}
+
+// Workspace of the gradient: scales, codes and maxima of its four operands, the sums of
+// K ranges; each part starts at a multiple of 16 bytes.
+struct I8GradWs {
+    size_t s_dyr, s_dyc, s_w, s_x, dyr, dyc, w, x, p_dy, p_w, p_x, sums, bytes;
+};
+static I8GradWs i8_grad_ws(int64_t T, int64_t O, int64_t I) {
+    size_t at = 0;
+    const auto take = [&](size_t n) { const size_t r = at; at += (n + 15) / 16 * 16; return r; };
+    const int64_t Tp = (T + 15) / 16 * 16, Op = (O + 15) / 16 * 16;
+    I8GradWs l;
+    l.s_dyr = take((size_t)T * 4); l.s_dyc = take((size_t)O * 4); l.s_w = take((size_t)I * 4); l.s_x = take((size_t)I * 4);
+    l.dyr = take((size_t)T * Op); l.dyc = take((size_t)O * Tp); l.w = take((size_t)I * Op); l.x = take((size_t)I * Tp);
+    l.p_dy = take(i8_cols_part_bytes(T, O)); l.p_w = take(i8_cols_part_bytes(O, I)); l.p_x = take(i8_cols_part_bytes(T, I));
+    l.sums = take(std::max(i8_gemm_ws_bytes(T, I, Op), i8_gemm_ws_bytes(O, I, Tp)));
+    l.bytes = at;
+    return l;
+}
+static fp8bs_status i8_grad_shape(int64_t T, int64_t O, int64_t I) {
+    if (T < 0 || O < 0 || I < 0) return fail(FP8BS_ERR_SHAPE, "negative size");
+    if (O % 8 || I % 8) return fail(FP8BS_ERR_SHAPE, "O and I must be multiples of 8 (O=%lld I=%lld)", (long long)O, (long long)I);
+    if (T > 131056 || O > 131056) return fail(FP8BS_ERR_SHAPE, "T=%lld or O=%lld > 131056: a sum could leave 32 bits", (long long)T, (long long)O);
+    if (I > INT32_MAX / 2) return fail(FP8BS_ERR_SHAPE, "size too large");
+    const uint64_t Tp = (T + 15) / 16 * 16, Op = (O + 15) / 16 * 16;
+    if ((uint64_t)T * Op >= (1ull << 32) || (uint64_t)O * Tp >= (1ull << 32) || (uint64_t)I * std::max(Tp, Op) >= (1ull << 32))
+        return fail(FP8BS_ERR_SHAPE, "an operand's codes exceed 4 GiB");
+    return FP8BS_OK;
+}
+
+fp8bs_status int8_linear_backward_ws_size(int64_t T, int64_t O, int64_t I, size_t* bytes) {
+    if (!bytes) return fail(FP8BS_ERR_NULL, "bytes is required");
+    const fp8bs_status v = i8_grad_shape(T, O, I);
+    if (v != FP8BS_OK) return v;
+    *bytes = i8_grad_ws(T, O, I).bytes;
+    return ok();
+}
+
+fp8bs_status int8_linear_backward(int64_t T, int64_t O, int64_t I, const uint16_t* dy, int64_t ld_dy, const uint16_t* w,
+                                  int64_t ld_w, const uint16_t* x, int64_t ld_x, float* dx, int64_t ld_dx, float* dw,
+                                  int64_t ld_dw, void* ws, size_t ws_bytes, hipStream_t stream) {
+    fp8bs_status v = i8_grad_shape(T, O, I);
+    if (v != FP8BS_OK) return v;
+    if (I == 0 || (T == 0 && O == 0)) return ok();
+    const struct { const char* name; const void* p; int64_t rows, cols, ld; } in[] = {
+        {"dy", dy, T, O, ld_dy}, {"w", w, O, I, ld_w}, {"x", x, T, I, ld_x}, {"dx", dx, T, I, ld_dx}, {"dw", dw, O, I, ld_dw}};
+    for (const auto& t : in) {
+        if (t.rows == 0 || t.cols == 0) continue;
+        if (!t.p) return fail(FP8BS_ERR_NULL, "%s is required", t.name);
+        if (t.ld < t.cols) return fail(FP8BS_ERR_STRIDE, "%s's leading dimension is less than its columns", t.name);
+        if (t.ld % 8 || !aligned(t.p, 16)) return fail(FP8BS_ERR_ALIGN, "%s must be 16-byte aligned with a leading dimension %% 8 == 0", t.name);
+    }
+    const I8GradWs l = i8_grad_ws(T, O, I);
+    if (l.bytes && !ws) return fail(FP8BS_ERR_NULL, "a workspace of %zu bytes is required", l.bytes);
+    if (ws_bytes < l.bytes) return fail(FP8BS_ERR_SHAPE, "ws_bytes %zu < %zu", ws_bytes, l.bytes);
+    if (!aligned(ws, 16)) return fail(FP8BS_ERR_ALIGN, "ws must be 16-byte aligned");
+    if ((v = check_device()) != FP8BS_OK) return v;
+    uint8_t* b = static_cast<uint8_t*>(ws);
+    const auto f = [&](size_t at) { return reinterpret_cast<float*>(b + at); };
+    const auto h = [&](size_t at) { return reinterpret_cast<uint16_t*>(b + at); };
+    const int64_t Tp = (T + 15) / 16 * 16, Op = (O + 15) / 16 * 16;
+    const I8GemmArgs gx{T, I, Op, b + l.dyr, Op, f(l.s_dyr), b + l.w, Op, 0, f(l.s_w), 0, dx, ld_dx, 1, 0, nullptr, nullptr};
+    const I8GemmArgs gw{O, I, Tp, b + l.dyc, Tp, f(l.s_dyc), b + l.x, Tp, 0, f(l.s_x), 0, dw, ld_dw, 1, 0, nullptr, nullptr};
+    // without tokens or outputs one of the two is a sum over nothing and the other empty
+    if (T == 0 || O == 0) {
+        const I8GemmArgs& g = T ? gx : gw;
+        const hipError_t e = T ? launch_i8_quant_rows(dy, T, 0, ld_dy, b + l.dyr, Op, f(l.s_dyr), stream)
+                               : launch_i8_quant_cols(dy, 0, O, ld_dy, b + l.dyc, Tp, f(l.s_dyc), stream);
+        const hipError_t e2 = e != hipSuccess ? e : T ? launch_i8_quant_cols(w, 0, I, ld_w, b + l.w, Op, f(l.s_w), stream)
+                                                      : launch_i8_quant_cols(x, 0, I, ld_x, b + l.x, Tp, f(l.s_x), stream);
+        return launched(e2 != hipSuccess ? e2 : launch_i8_gemm(g, nullptr, stream), "int8_linear_backward");
+    }
+    const I8Cols cols[] = {{dy, T, O, ld_dy, b + l.dyc, Tp, f(l.s_dyc), h(l.p_dy)},
+                           {w, O, I, ld_w, b + l.w, Op, f(l.s_w), h(l.p_w)},
+                           {x, T, I, ld_x, b + l.x, Tp, f(l.s_x), h(l.p_x)}};
+    hipError_t e = launch_i8_quant_cols3(cols, stream);
+    if (e == hipSuccess) e = launch_i8_quant_rows(dy, T, O, ld_dy, b + l.dyr, Op, f(l.s_dyr), stream);
+    return launched(e != hipSuccess ? e : launch_i8_gemm_pair(gx, gw, b + l.sums, stream), "int8_linear_backward");
 }
 
 fp8bs_status int8_grouped_gemm(int64_t total_rows, int64_t N, int64_t K, int32_t G, const int32_t* offsets,

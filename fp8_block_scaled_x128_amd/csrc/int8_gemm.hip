@@ -157,11 +157,11 @@ __device__ __forceinline__ int group_tiles(const I8Args& p, int g) {
     return g < p.G ? (p.offsets[g + 1] - p.offsets[g] + BM - 1) / BM : 0;
 }
 
+// Tile `bid` of a product, or K range blockIdx.y of it (OUT_SUMS).
 template <int TM, int TN, bool GROUPED, bool GATHER, int OUT>
-__global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p) {
+__device__ __forceinline__ void tile_product(const I8Args& p, const int bid, uint8_t* smem) {
     constexpr int BM = 64 * TM, BN = 64 * TN;
     constexpr int kABytes = BM * BK, kBBytes = BN * BK;
-    __shared__ __attribute__((aligned(16))) uint8_t smem[2 * kABytes + 3 * kBBytes];
     int* s_found = reinterpret_cast<int*>(smem);    // before the first copy
 
     const int lane = threadIdx.x & 63;
@@ -176,7 +176,7 @@ __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p
         // consecutive tiles on one XCD (workgroups are dealt round-robin to the
         // eight), in groups of 8 row tiles that sweep n: the tiles an XCD runs at
         // a time share their panels in its L2
-        const int ntm = (p.M + BM - 1) / BM, nblk = ntn * ntm, per = nblk / 8, bid = blockIdx.x;
+        const int ntm = (p.M + BM - 1) / BM, nblk = ntn * ntm, per = nblk / 8;
         const int id = bid < per * 8 ? (bid % 8) * per + bid / 8 : bid;
         const int gsz = 8 * ntn, first = id / gsz * 8, rows = min(ntm - first, 8);
         t.m0 = (first + id % gsz % rows) * BM;
@@ -189,7 +189,6 @@ __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p
         // turn, in eight runs, one per XCD; the first wave adds up the groups'
         // tile counts
         if (wave == 0) {
-            const int bid = blockIdx.x;
             int total = 0;
             for (int gb = 0; gb < p.G; gb += 64) total += group_tiles<BM>(p, gb + lane);
             total = (int)lane_value((uint32_t)wave_scan(total), 63);
@@ -472,6 +471,33 @@ __global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p
     });
 }
 
+template <int TM, int TN>
+constexpr int kTileLds = (2 * TM + 3 * TN) * 64 * BK;
+template <int TM, int TN, bool GROUPED, bool GATHER, int OUT>
+__global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile(I8Args p) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kTileLds<TM, TN>];
+    tile_product<TM, TN, GROUPED, GATHER, OUT>(p, blockIdx.x, smem);
+}
+
+// Two products in one launch, the first's tiles (blocks below `first`, the longer K)
+// before the second's, so that the second's fill the units that the first leaves idle:
+// the gradients of 4096 x 2560 by 9728, 160 tiles of 76 slices and 380 of 32 on 256
+// units, 191 to 210 us where one after the other took 250.
+struct I8Pair {
+    I8Args p[2];
+    int32_t first;
+};
+template <int TM, int TN>
+__global__ void __launch_bounds__(256, (TM * TN > 4 ? 1 : 2)) k_i8_tile_pair(I8Pair g) {
+    __shared__ __attribute__((aligned(16))) uint8_t smem[kTileLds<TM, TN>];
+    const bool b = (int)blockIdx.x >= g.first;
+    const I8Args &u = g.p[0], &v = g.p[1];
+    const I8Args p{b ? v.M : u.M, b ? v.N : u.N, b ? v.K : u.K, b ? v.a : u.a, b ? v.lda : u.lda, b ? v.sa : u.sa,
+                   b ? v.b : u.b, b ? v.ldb : u.ldb, 0, b ? v.sb : u.sb, 0, b ? v.c : u.c, b ? v.ldc : u.ldc, 0,
+                   nullptr, nullptr, 1};
+    tile_product<TM, TN, false, false, OUT_FP32>(p, (int)blockIdx.x - (b ? g.first : 0), smem);
+}
+
 // Few rows (decode): the weights are read once, straight into registers, by waves
 // that split K and meet in LDS.  A workgroup takes 16 weight rows; a wave takes every
 // W-th run of 128 bytes of K, a whole cache line of each row, and feeds it to two
@@ -706,8 +732,9 @@ hipError_t tile(const I8Args& p, bool out32, hipStream_t st) {
 // Products of so little work (M N K) that tiles of 128 x 128 leave most compute units
 // idle, or wait for each slice: 205 x 1008 by 1512 6.0 us in the waves' K ranges and 8.6
 // in tiles, 128 x 2048 by 2560 10.9 and 12.2, 32 x 4096 by 4096 8.4 and 11.7 (K split);
-// past it 205 x 2048 by 2560 14 and 12.2, 32 x 2560 by 9728 16.2 and 13.7.
-bool little(int64_t M, int64_t N, int64_t K) { return M * N * K <= 640000000; }
+// past it 205 x 2048 by 2560 14 and 12.2, 32 x 2560 by 9728 16.2 and 13.7.  Eight waves
+// need a run each.
+bool little(int64_t M, int64_t N, int64_t K) { return K > 7 * kRun && M * N * K <= 640000000; }
 
 // K ranges for products with few tiles and a long K: tiles of 64 x 128, about two for
 // each compute unit, of four slices at least.  The join and the sums' way through
@@ -799,6 +826,22 @@ hipError_t launch_i8_gemm(const I8GemmArgs& g, void* ws, hipStream_t st) {
         return n > 1 ? split(p, g.out_f32, n, ws, st) : launch_dense(p, g.out_f32, st);
     }
     return g.a_rows ? launch_grouped<true>(p, g.out_f32, st) : launch_grouped<false>(p, g.out_f32, st);
+}
+
+hipError_t launch_i8_gemm_pair(const I8GemmArgs& g, const I8GemmArgs& h, void* ws, hipStream_t st) {
+    const auto tiles = [](const I8GemmArgs& x) { return (x.M + 255) / 256 * ((x.N + 255) / 256); };
+    if (tiles(g) + tiles(h) < kCUs) {
+        const hipError_t e = launch_i8_gemm(g, ws, st);
+        return e != hipSuccess ? e : launch_i8_gemm(h, ws, st);
+    }
+    const auto args = [](const I8GemmArgs& x) {
+        return I8Args{(int32_t)x.M, (int32_t)x.N, (int32_t)x.K, x.a, x.lda, x.sa, x.b, x.ldb, 0, x.sb, 0, x.c, x.ldc, 0,
+                      nullptr, nullptr, 1};
+    };
+    const bool swap = h.K > g.K;
+    const I8Pair p{{args(swap ? h : g), args(swap ? g : h)}, (int32_t)tiles(swap ? h : g)};
+    hipLaunchKernelGGL((k_i8_tile_pair<4, 4>), dim3((unsigned)(tiles(g) + tiles(h))), dim3(256), 0, st, p);
+    return hipGetLastError();
 }
 
 bool i8_linear_fused(int64_t rows, int64_t cols) { return rows == 1 && cols <= kFusedCodes && cols > 0; }

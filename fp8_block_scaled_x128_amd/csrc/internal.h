@@ -52,6 +52,16 @@ hipError_t launch_i8_quant_rows(const uint16_t* x, int64_t rows, int64_t cols, i
                                 float* s, hipStream_t st);
 hipError_t launch_i8_quant_cols(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, uint8_t* q, int64_t ld_q,
                                 float* s, hipStream_t st);
+// The column form of three tensors at once (none of them empty); part:
+// i8_cols_part_bytes each.
+constexpr int kI8ColTensors = 3;
+struct I8Cols {
+    const uint16_t* x; int64_t rows, cols, ld_x;
+    uint8_t* q; int64_t ld_q; float* s;
+    uint16_t* part;
+};
+size_t i8_cols_part_bytes(int64_t rows, int64_t cols);
+hipError_t launch_i8_quant_cols3(const I8Cols (&t)[kI8ColTensors], hipStream_t st);
 // SiLU*mul, then the row form; rows from *live on (nullable) are left alone.
 hipError_t launch_i8_silu_mul_quant(const uint16_t* gu, int64_t rows, int64_t I, int64_t ld_in, const int32_t* live,
                                     uint8_t* q, int64_t ld_q, float* s, uint16_t* h, int64_t ld_h, hipStream_t st);
@@ -67,6 +77,8 @@ struct I8GemmArgs {
 // ws: i8_gemm_ws_bytes for the sums of K ranges (dense), or null: no ranges.
 hipError_t launch_i8_gemm(const I8GemmArgs& g, void* ws, hipStream_t st);
 size_t i8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
+// Two dense products with fp32 outputs; ws: the larger of their two.
+hipError_t launch_i8_gemm_pair(const I8GemmArgs& g, const I8GemmArgs& h, void* ws, hipStream_t st);
 // The product of bf16 rows that are few enough to be quantized by every workgroup
 // for itself; g.a and g.sa are not read.
 bool i8_linear_fused(int64_t rows, int64_t cols);

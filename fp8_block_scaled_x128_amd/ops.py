@@ -36,7 +36,8 @@ EXPORTS = ["fp8_quant_rowblock", "fp8_quant_block2d", "fp8_quant_linear", "fp8_q
            "fp8_block_norm", "fp8_block_norm_backward", "fp8_block_norm_backward_ws_size", "mxfp8_quant", "mxfp8_quant_t",
            "fp8_quant_dual_axis", "fp8_transpose_codes", "fp8_quant_linear_pow2",
            "fp8_quant_pow2", "fp8_blockscaled_gemm_pow2", "mxfp8_gemm", "int8_quant",
-           "int8_silu_mul_quant", "int8_gemm", "int8_gemm_ws_size", "int8_linear", "int8_linear_ws_size", "int8_grouped_gemm",
+           "int8_silu_mul_quant", "int8_gemm", "int8_gemm_ws_size", "int8_linear", "int8_linear_ws_size",
+           "int8_linear_backward", "int8_linear_backward_ws_size", "int8_grouped_gemm",
            "fp8bs_e4m3_encode",
            "fp8bs_status_string", "fp8bs_last_error_detail"]
 
@@ -115,6 +116,8 @@ def load():
             "int8_gemm_ws_size": [I64, I64, I64, P],
             "int8_linear": [I64, I64, I64, P, I64, P, I64, P, P, I64, INT, P, ctypes.c_size_t, P],
             "int8_linear_ws_size": [I64, I64, I64, P],
+            "int8_linear_backward": [I64, I64, I64, P, I64, P, I64, P, I64, P, I64, P, I64, P, ctypes.c_size_t, P],
+            "int8_linear_backward_ws_size": [I64, I64, I64, P],
             "int8_grouped_gemm": [I64, I64, I64, I32, P, P, I64, P, I64, P, P, I64, I64, P, I64, P, I64, INT, P],
             "fp8bs_e4m3_encode": [P, P, I64, P],
         }
@@ -450,6 +453,20 @@ def int8_linear_ws_size(rows, N, cols):
     """Workspace bytes of int8_linear (host only)."""
     out = ctypes.c_size_t(0)
     _check("int8_linear_ws_size", load().int8_linear_ws_size(rows, N, cols, ctypes.byref(out)))
+    return out.value
+
+
+def int8_linear_backward(T, O, I, dy, ld_dy, w, ld_w, x, ld_x, dx, ld_dx, dw, ld_dw, ws, ws_bytes, stream=None,
+                         raise_on_error=True):
+    st = load().int8_linear_backward(T, O, I, _p(dy), ld_dy, _p(w), ld_w, _p(x), ld_x, _p(dx), ld_dx, _p(dw), ld_dw,
+                                     _p(ws), ws_bytes, _stream(stream))
+    return _check("int8_linear_backward", st, raise_on_error)
+
+
+def int8_linear_backward_ws_size(T, O, I):
+    """Workspace bytes of int8_linear_backward (host only)."""
+    out = ctypes.c_size_t(0)
+    _check("int8_linear_backward_ws_size", load().int8_linear_backward_ws_size(T, O, I, ctypes.byref(out)))
     return out.value
 
 
@@ -1119,35 +1136,34 @@ def i8_linear_forward(x, w, out_dtype=torch.bfloat16):
 
 
 class I8LinearGrads(NamedTuple):
-    """Outputs of i8_linear_backward and its workspaces: codes and scales (q, s) of
-    dY per token, dY per output channel, W and X per input channel, and what the
-    product needs."""
+    """Outputs of i8_linear_backward and its workspace."""
     dx: torch.Tensor
     dw: torch.Tensor
-    codes: tuple
-    ws: Optional[torch.Tensor]
+    ws: torch.Tensor
 
 
 def i8_linear_backward(dy, saved, out: Optional[I8LinearGrads] = None) -> I8LinearGrads:
     """dX = dY W and dW = dY^T X, both fp32, of Y = X W^T in 8-bit integers, each
     operand with a scale per row of the product it enters: dY per token and W per
     input channel for dX, dY per output channel and X per input channel, both over
-    the tokens, for dW (rounding to codes is passed straight through)."""
+    the tokens, for dW (rounding to codes is passed straight through).  `out` is an
+    earlier result for the same sizes whose tensors are written again (two calls in
+    flight need two)."""
     w, x = saved
-    (T, O), I = dy.shape, x.shape[1]
-    if x.shape[0] != T or w.shape != (O, I):
-        raise ValueError("dy %s, w %s and x %s do not belong to one layer" % (tuple(dy.shape), tuple(w.shape),
-                                                                              tuple(x.shape)))
+    (T, O), I, dev = dy.shape, x.shape[1], _device()
+    dyp, ld_dy = _mat("dy", dy, T, O, dev, _BF)
+    wp, ld_w = _mat("w", w, O, I, dev, _BF)
+    xp, ld_x = _mat("x", x, T, I, dev, _BF)
     if out is None:
         e = lambda r, c: torch.empty((r, c), dtype=_F32, device=dy.device)
-        need = max(int8_gemm_ws_size(T, I, _pad16(O)), int8_gemm_ws_size(O, I, _pad16(T)))
-        out = I8LinearGrads(e(T, I), e(O, I), (None,) * 4, _u8((need,), dy.device) if need else None)
-    dyr, dyc, wc, xc = out.codes
-    dyr, dyc = i8_quant(dy, AXIS_ROW, dyr), i8_quant(dy, AXIS_COL, dyc)
-    wc, xc = i8_quant(w, AXIS_COL, wc), i8_quant(x, AXIS_COL, xc)
-    i8_gemm(*dyr, *wc, _F32, out.dx, out.ws)
-    i8_gemm(*dyc, *xc, _F32, out.dw, out.ws)
-    return I8LinearGrads(out.dx, out.dw, (dyr, dyc, wc, xc), out.ws)
+        out = I8LinearGrads(e(T, I), e(O, I), _u8((int8_linear_backward_ws_size(T, O, I),), dy.device))
+    dxp, ld_dx = _mat("out.dx", out.dx, T, I, dev, _F32)
+    dwp, ld_dw = _mat("out.dw", out.dw, O, I, dev, _F32)
+    wsp, wsn = _workspace(out.ws, dev)
+    st = load().int8_linear_backward(T, O, I, dyp, ld_dy, wp, ld_w, xp, ld_x, dxp, ld_dx, dwp, ld_dw, wsp, wsn, _stream())
+    if st:
+        _check("int8_linear_backward", st)
+    return out
 
 
 def i8_grouped_gemm(a, sa, b, sb, offsets, row_token=None, out_dtype=torch.bfloat16, out=None):

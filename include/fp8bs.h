@@ -971,6 +971,27 @@ fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* 
 fp8bs_status int8_linear_ws_size(int64_t rows, int64_t N, int64_t cols, size_t* bytes);
 
 /* ------------------------------------------------------------------------
+ * int8_linear_backward -- the gradient of Y = X W^T in 8-bit integers: dX = dY W and
+ * dW = dY^T X, both fp32, each operand quantized with a scale per row of the product
+ * it enters (int8_quant): dY per token and W per input channel for dX, dY per output
+ * channel and X per input channel, both over the tokens, for dW.  The results are
+ * those of int8_quant and int8_gemm called for each.
+ *
+ * T tokens, O outputs, I inputs.  dy : bf16 [T][ld_dy].   w : bf16 [O][ld_w].
+ * x : bf16 [T][ld_x].   dx : fp32 [T][ld_dx].   dw : fp32 [O][ld_dw].
+ * ws : device workspace of int8_linear_backward_ws_size bytes, 16-byte aligned;
+ *      contents on entry are ignored.  Calls that overlap in time need separate ones.
+ * Requirements: O and I % 8 == 0; T and O <= 131056; every tensor 16-byte aligned with
+ * a leading dimension % 8 == 0; no operand's codes exceed 4 GiB.  Without tokens (T 0)
+ * dW is zeros, without outputs (O 0) dX is.
+ * ------------------------------------------------------------------------ */
+fp8bs_status int8_linear_backward(int64_t T, int64_t O, int64_t I, const uint16_t* dy, int64_t ld_dy, const uint16_t* w,
+                                  int64_t ld_w, const uint16_t* x, int64_t ld_x, float* dx, int64_t ld_dx, float* dw,
+                                  int64_t ld_dw, void* ws, size_t ws_bytes, hipStream_t stream);
+/* Host only: the workspace int8_linear_backward needs. */
+fp8bs_status int8_linear_backward_ws_size(int64_t T, int64_t O, int64_t I, size_t* bytes);
+
+/* ------------------------------------------------------------------------
  * int8_grouped_gemm -- int8_gemm over G expert groups of rows: row r of group g
  * is C[r, n] = sa[t] sb_g[n] sum_k a[t, k] b_g[n, k], t = a_rows[r] (t = r without
  * a_rows).  offsets, a_rows, a_count and what is left unwritten: as in
