@@ -8,18 +8,22 @@
 // to fp32 once and multiplied by sa, then sb (three roundings), then rounded to
 // the output type: results do not depend on tile sizes or K ranges.
 //
-// Tiles (k_i8_tile).  A workgroup of four waves, two by two, computes 32 TN weight
-// rows (n) x 32 TM activation rows (m); K advances in slices of 128 bytes that
-// global_load_lds copies straight into LDS, two slices resident.  LDS rows are 128
-// bytes with the 16-byte chunk c of row r at slot c ^ (r & 7), so the fragment
-// reads of sixteen rows hit all banks.  Weight rows are the matrix instruction's
-// first operand: a lane's four outputs are consecutive n of one m.
-// With TM = TN = 8 a wave computes 128 x 128: per slice a compute unit reads 128 KB
-// of fragments and writes 64 KB of copies (1536 cycles at 128 bytes each) beside
-// 2048 cycles of matrix work, where eight waves of 64 x 128 would read 192 KB.
-// With one wave per SIMD nothing else hides a wave's latencies, so it works half
-// a slice ahead of itself: while one half's matrix instructions run, the other
-// half's fragments are read.
+// Tiles (k_i8_tile).  A workgroup of four waves, two by two, computes 64 TN weight
+// rows (n) x 64 TM activation rows (m) with the 32 x 32 x 32 matrix instruction, which
+// reaches 5.0 POPS on 256 units where 16 x 16 x 64 reaches 2.5 (3.8 on random codes:
+// the clock falls with the power they draw).  K advances in slices of 128 bytes that
+// global_load_lds copies straight into LDS, two slices of activations and three of
+// weights resident.  LDS rows are 128 bytes with the 16-byte chunk c of row r at slot
+// c ^ (r & 7), so that fragment reads hit all banks.  Weight rows are the matrix
+// instruction's first operand: a lane's outputs are runs of four consecutive n of one
+// m.  With TM = TN = 4 a wave holds 256 sums, 128 x 128 outputs: per slice a compute
+// unit reads 128 KB of fragments and writes 64 KB of copies beside 2048 cycles of
+// matrix work.  One such workgroup fills a unit's LDS, so nothing else hides a wave's
+// latencies: it works a slice ahead of itself.  4096 x 2560 by 9728: 122 us (608 tiles
+// are 2.4 rounds of 256 units), 1.67 POPS; 131072 expert rows of 2048 by 1536 490,
+// 1.68.  TM = TN = 2 puts two workgroups on a unit and takes products with fewer
+// tiles; TM = 1, TN = 2 the K ranges and small groups.
+// Few rows are bound by the weights' way from memory, see below.
 #include <algorithm>
 #include <utility>
 
@@ -36,8 +40,6 @@ typedef __attribute__((address_space(3))) uint8_t lds_u8;
 
 constexpr int BK = 128;                 // K bytes per slice
 constexpr int kCUs = 256;
-
-
 
 struct I8Args {
     int32_t M, N, K;

@@ -79,8 +79,8 @@ hipError_t launch_i8_gemm(const I8GemmArgs& g, void* ws, hipStream_t st);
 size_t i8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
 // Two dense products with fp32 outputs; ws: the larger of their two.
 hipError_t launch_i8_gemm_pair(const I8GemmArgs& g, const I8GemmArgs& h, void* ws, hipStream_t st);
-// The product of bf16 rows that are few enough to be quantized by every workgroup
-// for itself; g.a and g.sa are not read.
+// The product of one bf16 row that every workgroup quantizes for itself; g.a and g.sa
+// are not read.
 bool i8_linear_fused(int64_t rows, int64_t cols);
 hipError_t launch_i8_linear_fused(const I8GemmArgs& g, const uint16_t* x, int64_t cols, hipStream_t st);
 

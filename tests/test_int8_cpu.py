@@ -50,7 +50,7 @@ PRODUCT = [(SHAPE, dict(M=-1)), (SHAPE, dict(K=72, lda=80, ldb=80)), (SHAPE, dic
 
 
 @pytest.mark.parametrize("want,a", PRODUCT + [(ALIGN, dict(ws=P + 8, wsn=1 << 20)),
-                                              (SHAPE, dict(M=64, K=1024, lda=1024, ldb=1024, ws=P, wsn=16))])
+                                              (SHAPE, dict(M=64, N=2560, K=9728, lda=9728, ldb=9728, ldc=2560, ws=P, wsn=16))])
 def test_gemm_refuses(want, a):
     assert gemm(**a) == want
 
@@ -90,6 +90,30 @@ def linear(rows=4, N=64, cols=64, x=P, ldx=64, w=P, ldw=64, sw=P, y=P, ldy=64, o
     (STRIDE, dict(cols=56, ldx=56, ldw=56)), (ALIGN, dict(x=P + 8)), (UNSUPPORTED, dict(out=7))])
 def test_linear_refuses(want, a):
     assert linear(**a) == want
+
+
+def backward(T=4, O=64, I=32, dy=P, ld_dy=64, w=P, ld_w=32, x=P, ld_x=32, dx=P, ld_dx=32, dw=P, ld_dw=32, ws=P, wsn=1 << 20):
+    return ops.int8_linear_backward(T, O, I, dy, ld_dy, w, ld_w, x, ld_x, dx, ld_dx, dw, ld_dw, ws, wsn, stream=0,
+                                    raise_on_error=False)
+
+
+@pytest.mark.parametrize("want,a", [
+    (SHAPE, dict(T=-1)), (SHAPE, dict(O=60)), (SHAPE, dict(I=20)), (SHAPE, dict(T=131057)), (SHAPE, dict(O=131064, ld_dy=131064)),
+    (SHAPE, dict(T=131056, I=65536, ld_x=65536, ld_w=65536)), (NULL, dict(dy=None)), (NULL, dict(w=None)), (NULL, dict(x=None)),
+    (NULL, dict(dx=None)), (NULL, dict(dw=None)), (NULL, dict(ws=None)), (SHAPE, dict(wsn=100)), (STRIDE, dict(ld_dy=56)),
+    (STRIDE, dict(ld_w=24)), (STRIDE, dict(ld_x=24)), (STRIDE, dict(ld_dx=24)), (STRIDE, dict(ld_dw=24)), (ALIGN, dict(dy=P + 8)),
+    (ALIGN, dict(w=P + 2)), (ALIGN, dict(ld_x=36)), (ALIGN, dict(dx=P + 8)), (ALIGN, dict(dw=P + 4)), (ALIGN, dict(ws=P + 8))])
+def test_linear_backward_refuses(want, a):
+    assert backward(**a) == want
+
+
+def test_linear_backward_workspace():
+    # scales (4 + 64 + 2 x 32 floats), codes (4 x 64, 64 x 16, 32 x 64, 32 x 16), the runs' maxima
+    assert ops.int8_linear_backward_ws_size(4, 64, 32) == 16 + 256 + 256 + 256 + 1024 + 2048 + 512 + 128 + 64 + 64
+    assert backward(I=0) == 0 and backward(T=0, O=0) == 0
+    for bad in ((-1, 8, 8), (8, 12, 8), (8, 8, 4), (1 << 20, 8, 8)):
+        with pytest.raises(ops.Fp8bsError):
+            ops.int8_linear_backward_ws_size(*bad)
 
 
 def test_empty_calls_need_no_device():
