@@ -1029,6 +1029,10 @@ fp8bs_status mxfp8_grouped_gemm_swiglu_quant(int64_t total_rows, int64_t I, int6
                     "mxfp8_grouped_gemm_swiglu_quant");
 }
 
+// A launch has fewer than 2^32 threads: 256 a row, or 64 up to 4096 columns.
+static bool i8_rows_too_many(int64_t rows, int64_t cols) {
+    return cols > INT32_MAX / 4 || rows >= (cols > 4096 ? 1ll << 24 : 1ll << 26);
+}
 // Codes of int8_quant and int8_silu_mul_quant: `len` of them per output row.
 static fp8bs_status i8_codes_args(int64_t len, const int8_t* q, int64_t ld_q, const float* s) {
     if (!s || (len > 0 && !q)) return fail(FP8BS_ERR_NULL, "q and s are required");
@@ -1043,7 +1047,7 @@ fp8bs_status int8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t l
     if (axis != FP8BS_AXIS_ROW && axis != FP8BS_AXIS_COL) return fail(FP8BS_ERR_UNSUPPORTED, "axis %d", (int)axis);
     if (rows < 0 || cols < 0) return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
     if (cols % 8) return fail(FP8BS_ERR_SHAPE, "cols %% 8 != 0 (cols=%lld)", (long long)cols);
-    if (rows > INT32_MAX / 2 || cols > INT32_MAX / 2 || (axis == FP8BS_AXIS_COL && rows > 65535ll * 128))
+    if (axis == FP8BS_AXIS_ROW ? i8_rows_too_many(rows, cols) : rows > 65535ll * 128 || cols >= 1ll << 28)
         return fail(FP8BS_ERR_SHAPE, "tensor too large");
     const bool by_row = axis == FP8BS_AXIS_ROW;
     if ((by_row ? rows : cols) == 0) return ok();
@@ -1067,7 +1071,7 @@ fp8bs_status int8_silu_mul_quant(const uint16_t* gate_up, int64_t rows, int64_t 
                                  int64_t ld_h, hipStream_t stream) {
     if (rows < 0 || I < 0) return fail(FP8BS_ERR_SHAPE, "rows=%lld I=%lld", (long long)rows, (long long)I);
     if (I % 8) return fail(FP8BS_ERR_SHAPE, "I %% 8 != 0 (I=%lld)", (long long)I);
-    if (rows > INT32_MAX / 2 || I > INT32_MAX / 4) return fail(FP8BS_ERR_SHAPE, "tensor too large");
+    if (i8_rows_too_many(rows, I)) return fail(FP8BS_ERR_SHAPE, "tensor too large");
     if (rows == 0) return ok();
     if (I > 0) {
         if (!gate_up) return fail(FP8BS_ERR_NULL, "gate_up is required");
@@ -1092,7 +1096,7 @@ static fp8bs_status i8_product_args(int64_t M, int64_t N, int64_t K, const int8_
     if (K % 16) return fail(FP8BS_ERR_SHAPE, "K %% 16 != 0 (K=%lld)", (long long)K);
     if (K > 131056) return fail(FP8BS_ERR_SHAPE, "K=%lld > 131056: the sum could leave 32 bits", (long long)K);
     if (N % 8) return fail(FP8BS_ERR_SHAPE, "N %% 8 != 0 (N=%lld)", (long long)N);
-    if (M > INT32_MAX / 2 || N > INT32_MAX / 2) return fail(FP8BS_ERR_SHAPE, "size too large");
+    if (M > INT32_MAX / 2 || N > 1ll << 26) return fail(FP8BS_ERR_SHAPE, "size too large");
     if (out != FP8BS_OUT_BF16 && out != FP8BS_OUT_FP32) return fail(FP8BS_ERR_UNSUPPORTED, "out %d", (int)out);
     if (M == 0 || N == 0) return FP8BS_OK;
     if (!c || !sb || (K > 0 && !b)) return fail(FP8BS_ERR_NULL, "b, sb and c are required");
@@ -1163,7 +1167,7 @@ fp8bs_status int8_linear_ws_size(int64_t rows, int64_t N, int64_t cols, size_t* 
 fp8bs_status int8_linear(int64_t rows, int64_t N, int64_t cols, const uint16_t* x, int64_t ld_x, const int8_t* w,
                          int64_t ld_w, const float* sw, void* y, int64_t ld_y, fp8bs_out out, void* ws, size_t ws_bytes,
                          hipStream_t stream) {
-    if (rows < 0 || cols < 0 || rows > INT32_MAX / 2 || cols > INT32_MAX / 2)
+    if (rows < 0 || cols < 0 || i8_rows_too_many(rows, cols))
         return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
     if (cols % 8) return fail(FP8BS_ERR_SHAPE, "cols %% 8 != 0 (cols=%lld)", (long long)cols);
     const int64_t K = (cols + 15) / 16 * 16;
@@ -1212,7 +1216,7 @@ static fp8bs_status i8_grad_shape(int64_t T, int64_t O, int64_t I) {
     if (T < 0 || O < 0 || I < 0) return fail(FP8BS_ERR_SHAPE, "negative size");
     if (O % 8 || I % 8) return fail(FP8BS_ERR_SHAPE, "O and I must be multiples of 8 (O=%lld I=%lld)", (long long)O, (long long)I);
     if (T > 131056 || O > 131056) return fail(FP8BS_ERR_SHAPE, "T=%lld or O=%lld > 131056: a sum could leave 32 bits", (long long)T, (long long)O);
-    if (I > INT32_MAX / 2) return fail(FP8BS_ERR_SHAPE, "size too large");
+    if (I > 1ll << 26) return fail(FP8BS_ERR_SHAPE, "size too large");
     const uint64_t Tp = (T + 15) / 16 * 16, Op = (O + 15) / 16 * 16;
     if ((uint64_t)T * Op >= (1ull << 32) || (uint64_t)O * Tp >= (1ull << 32) || (uint64_t)I * std::max(Tp, Op) >= (1ull << 32))
         return fail(FP8BS_ERR_SHAPE, "an operand's codes exceed 4 GiB");

@@ -832,7 +832,9 @@ hipError_t launch_i8_gemm(const I8GemmArgs& g, void* ws, hipStream_t st) {
 
 hipError_t launch_i8_gemm_pair(const I8GemmArgs& g, const I8GemmArgs& h, void* ws, hipStream_t st) {
     const auto tiles = [](const I8GemmArgs& x) { return (x.M + 255) / 256 * ((x.N + 255) / 256); };
-    if (tiles(g) + tiles(h) < kCUs) {
+    // together they fill the units, and neither is a product of few rows, which the
+    // ways of launch_dense read faster
+    if (tiles(g) + tiles(h) < kCUs || std::min(g.M, h.M) < 256) {
         const hipError_t e = launch_i8_gemm(g, ws, st);
         return e != hipSuccess ? e : launch_i8_gemm(h, ws, st);
     }

@@ -6,7 +6,9 @@
 //
 // Bound by HBM: 2 bytes read and 1 written per value, once for rows; columns
 // need their maximum over all rows before the first code, so a long tensor is read
-// twice (the second time mostly from the last-level cache).
+// twice (the second time mostly from the last-level cache).  Rows: 4096 x 2560 9 us,
+// 4096 x 9728 21 (5.7 TB/s); columns of 4096 x 9728 26 for the maxima, 23 for the codes,
+// of 205 x 1512 7.
 #include "int8_common.h"
 #include "internal.h"
 #include "reduce.h"

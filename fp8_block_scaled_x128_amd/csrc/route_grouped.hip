@@ -18,6 +18,10 @@
 // The lanes of a token are dealt to the groups, a power of two each, and hold
 // consecutive experts, so that a group's maxima meet in a few lane steps.  The rest
 // is the plain router's: histograms, rows and losses come from the same code.
+// Bound by vector issue: a token's `k` rounds of maxima over its lanes are dependent.
+// 16384 tokens of 256 experts (16.8 MB of logits, 3 us): selection 27 us, rows 10;
+// 32 tokens of 128 in one launch 9.0; the gradient, one pass over logits and result,
+// 12 us at 16384 x 256 (2.7 TB/s) and 3.7 at 1000 x 60.
 #include "route_common.h"
 
 namespace fp8bs {

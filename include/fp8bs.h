@@ -905,7 +905,8 @@ fp8bs_status mxfp8_gemm(int64_t rows, int64_t N, int64_t K, int32_t G,
  * column's scale is 0.
  * Requirements: rows, cols >= 0; cols % 8 == 0, ld_x >= cols, ld_x % 8 == 0, x
  * 16-byte aligned; ld_q >= the padded length, ld_q % 16 == 0, q 16-byte aligned;
- * s 4-byte aligned; AXIS_COL: rows <= 65535 * 128.
+ * s 4-byte aligned; AXIS_ROW: rows < 2^26, past 4096 columns 2^24; AXIS_COL:
+ * rows <= 65535 * 128, cols < 2^28.
  * ------------------------------------------------------------------------ */
 fp8bs_status int8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, fp8bs_axis axis,
                         int8_t* q, int64_t ld_q, float* s, hipStream_t stream);
@@ -921,7 +922,7 @@ fp8bs_status int8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t l
  *             last assignment hold nothing).
  * q, ld_q, s : as in int8_quant.   h_out : nullable bf16 [rows][ld_h].
  * Requirements: I % 8 == 0; ld_in >= 2 I, ld_in % 8 == 0, gate_up 16-byte
- * aligned; ld_h >= I, ld_h % 8 == 0, h_out 16-byte aligned.
+ * aligned; ld_h >= I, ld_h % 8 == 0, h_out 16-byte aligned; rows as in int8_quant.
  * ------------------------------------------------------------------------ */
 fp8bs_status int8_silu_mul_quant(const uint16_t* gate_up, int64_t rows, int64_t I, int64_t ld_in,
                                  const int32_t* live_rows, int8_t* q, int64_t ld_q, float* s, uint16_t* h_out,
@@ -944,7 +945,7 @@ fp8bs_status int8_silu_mul_quant(const uint16_t* gate_up, int64_t rows, int64_t 
  *      the same bits); contents on entry are ignored.  Calls that overlap in time need
  *      separate workspaces.
  * Requirements: M, N >= 0; 0 <= K <= 131056; K % 16 == 0 (int8_quant pads codes
- * with zeros); N % 8 == 0; lda, ldb >= K, % 16 == 0, a and b 16-byte aligned and
+ * with zeros); N % 8 == 0, N <= 2^26; lda, ldb >= K, % 16 == 0, a and b 16-byte aligned and
  * below 4 GiB each; ldc >= N, ldc % 8 == 0, c 16-byte aligned.
  * ------------------------------------------------------------------------ */
 fp8bs_status int8_gemm(int64_t M, int64_t N, int64_t K, const int8_t* a, int64_t lda, const float* sa,
@@ -981,8 +982,8 @@ fp8bs_status int8_linear_ws_size(int64_t rows, int64_t N, int64_t cols, size_t* 
  * x : bf16 [T][ld_x].   dx : fp32 [T][ld_dx].   dw : fp32 [O][ld_dw].
  * ws : device workspace of int8_linear_backward_ws_size bytes, 16-byte aligned;
  *      contents on entry are ignored.  Calls that overlap in time need separate ones.
- * Requirements: O and I % 8 == 0; T and O <= 131056; every tensor 16-byte aligned with
- * a leading dimension % 8 == 0; no operand's codes exceed 4 GiB.  Without tokens (T 0)
+ * Requirements: O and I % 8 == 0; T and O <= 131056, I <= 2^26; every tensor 16-byte aligned
+ * with a leading dimension % 8 == 0; no operand's codes exceed 4 GiB.  Without tokens (T 0)
  * dW is zeros, without outputs (O 0) dX is.
  * ------------------------------------------------------------------------ */
 fp8bs_status int8_linear_backward(int64_t T, int64_t O, int64_t I, const uint16_t* dy, int64_t ld_dy, const uint16_t* w,

@@ -25,6 +25,13 @@ def test_quant_refuses(want, a):
     assert quant(**a) == want
 
 
+@pytest.mark.parametrize("a", [dict(rows=1 << 26), dict(rows=1 << 24, cols=4104, ld=4104, ldq=4112),
+                               dict(axis=1, cols=1 << 28, ld=1 << 28)])
+def test_quant_refuses_more_than_a_launch_holds(a):
+    assert quant(**a) == SHAPE
+    assert gemm(N=(1 << 26) + 8, ldc=1 << 27) == SHAPE and linear(rows=1 << 26) == SHAPE
+
+
 def silu(gu=P, rows=4, I=64, ld=128, live=None, q=P, ldq=64, s=P, h=None, ldh=0):
     return ops.int8_silu_mul_quant(gu, rows, I, ld, live, q, ldq, s, h, ldh, stream=0, raise_on_error=False)
 
