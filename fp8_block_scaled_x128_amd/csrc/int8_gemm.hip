@@ -738,15 +738,17 @@ hipError_t tile(const I8Args& p, bool out32, hipStream_t st) {
 // need a run each.
 bool little(int64_t M, int64_t N, int64_t K) { return K > 7 * kRun && M * N * K <= 640000000; }
 
-// K ranges for products with few tiles and a long K: tiles of 64 x 128, about two for
-// each compute unit, of four slices at least.  The join and the sums' way through
-// memory cost as much as 16 slices, so as many are to be saved: 64 x 9728 by 2560 16 us
-// for 45, 205 x 4096 by 4096 19.6 for 20.2; 333 x 2048 by 2560 would take 17.2 for 12.4.
+// K ranges for products with few tiles and a long K: tiles of 64 x 128, about one for
+// each compute unit (64 x 9728 by 2560 14.6 us, two for each 16.4; 128 x 9728 16.8 and
+// 18.3), or two where one would keep more than 32 slices (333 x 9728 by 2560 26.3, one
+// 28.4); of four slices at least.  The join and the sums' way through memory cost as
+// much as some 12 slices, so as many are to be saved: 64 x 9728 by 2560 takes 45 us
+// whole; 333 x 2048 by 2560 would take 17.2 for 12.4.
 int split_count(int64_t M, int64_t N, int64_t K) {
     const int64_t tiles = (M + 63) / 64 * ((N + 127) / 128), nk = (K + BK - 1) / BK;
-    if (M <= 16 || M > 512 || tiles >= 256 || little(M, N, K)) return 1;
-    const int64_t n = std::min<int64_t>(2 * kCUs / tiles, nk / 4);
-    return n > 1 && nk - nk / n >= 16 ? (int)n : 1;
+    if (M <= 16 || M > 512 || tiles >= kCUs || little(M, N, K)) return 1;
+    const int64_t one = kCUs / tiles, n = std::min<int64_t>(nk > 32 * one ? 2 * kCUs / tiles : one, nk / 4);
+    return n > 1 && nk - nk / n >= 12 ? (int)n : 1;
 }
 
 hipError_t split(I8Args p, bool out32, int splits, void* ws, hipStream_t st) {
