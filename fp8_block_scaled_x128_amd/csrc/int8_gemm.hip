@@ -20,8 +20,8 @@
 // unit reads 128 KB of fragments and writes 64 KB of copies beside 2048 cycles of
 // matrix work.  One such workgroup fills a unit's LDS, so nothing else hides a wave's
 // latencies: it works a slice ahead of itself.  4096 x 2560 by 9728: 122 us (608 tiles
-// are 2.4 rounds of 256 units), 1.67 POPS; 131072 expert rows of 2048 by 1536 490,
-// 1.68.  TM = TN = 2 puts two workgroups on a unit and takes products with fewer
+// are 2.4 rounds of 256 units), 1.67 POPS; 131072 expert rows of 2048 by 1536 500,
+// 1.65.  TM = TN = 2 puts two workgroups on a unit and takes products with fewer
 // tiles; TM = 1, TN = 2 the K ranges and small groups.
 // Few rows are bound by the weights' way from memory, see below.
 #include <algorithm>
