@@ -102,12 +102,13 @@ __device__ __forceinline__ double lanes_sum64(double v) {
 // One token's selection by keys (0: not there).  val maps a key to its value; the
 // values' type F says whether close ones are reported (float: they may be in the
 // wrong order; tol0 + 2^-22 |v| bounds twice a value's error) or taken as they are
-// (double).  A group's sum errs by its two values' errors and its own rounding, at most
-// tol0 + 2^-23 mag with mag = |v1| + |v2|, which biases that cancel in the sum leave
-// large: of two groups the one with the larger mag reports that they are nearer than
-// 2 tol0 + 2^-22 mag (2^-21: room for the roundings here).  EXACT: the keys' own order is the values' (no bias), so only sums of
-// values can be in doubt.  On return lane j has slot j's key and expert in ksel[0],
-// esel[0], and slot j + L's in [1].
+// (double).  Groups are compared by half their values, whose sums stay finite.  Such a
+// sum errs by its two values' errors and its own rounding, at most tol0 / 2 + 2^-23 mag
+// with mag = |v1 / 2| + |v2 / 2|, which biases that cancel in the sum leave large: of two
+// groups the one with the larger mag reports that they are nearer than tol0 + 2^-22 mag
+// (2^-21: room for the roundings here).  EXACT: the keys' own order is the values' (no
+// bias), so only sums of values can be in doubt.  On return lane j has slot j's key and
+// expert in ksel[0], esel[0], and slot j + L's in [1].
 template <int L, int V, bool EXACT, class K, class F, class VAL>
 __device__ __forceinline__ bool pick(K (&left)[V], const GateArgs& g, const GateLanes& n, int l, int e0, F tol0, VAL val,
                                      K (&ksel)[2], uint32_t (&esel)[2]) {
@@ -140,9 +141,9 @@ __device__ __forceinline__ bool pick(K (&left)[V], const GateArgs& g, const Gate
             }
         } else {
             // NaN counts as infinity, a group without experts as the least
-            F mine = m1 > kNone ? val(m1) : (F)-INFINITY, mag = mine < 0 ? -mine : mine;
+            F mine = m1 > kNone ? (F)0.5 * val(m1) : (F)-INFINITY, mag = mine < 0 ? -mine : mine;
             if (g.top2 && m2 > kNone) {
-                const F second = val(m2);
+                const F second = (F)0.5 * val(m2);
                 mine += second;
                 mag += second < 0 ? -second : second;
             }
@@ -151,7 +152,7 @@ __device__ __forceinline__ bool pick(K (&left)[V], const GateArgs& g, const Gate
                 const F o = lane_at(mine, row + j * n.q);
                 rank += o > mine || (o == mine && j < group);
                 // an infinite difference, or none between infinities, is not close
-                if (kReport) close |= j != group && fabsf((float)(o - mine)) <= 2.0f * (float)tol0 + 0x1p-21f * (float)mag;
+                if (kReport) close |= j != group && fabsf((float)(o - mine)) <= (float)tol0 + 0x1p-21f * (float)mag;
             }
             close = close && mine > (F)-INFINITY && mine < (F)INFINITY;
         }

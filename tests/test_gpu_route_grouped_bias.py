@@ -55,3 +55,13 @@ def test_every_group_cancels(E, groups, keep, k, size, score):
     bias = torch.full((groups, E // groups), -size)
     bias[:, 1] = size
     assert check(z, k, bias.reshape(-1).cuda(), groups, keep, score, size) > T // 2
+
+
+@pytest.mark.parametrize("score", ["sigmoid", "softmax"])
+@pytest.mark.parametrize("sign", [1.0, -1.0])
+def test_sums_past_the_range_of_fp32(score, sign):
+    """Two biases whose sum is no fp32 number: the groups keep their order."""
+    T = 70
+    z = torch.randn(T, 8, generator=torch.Generator().manual_seed(1)).cuda()
+    bias = sign * torch.tensor([3e38, 2e38, 2.9e38, 2.5e38, 2.8e38, 3.1e38, 2.7e38, 1e38], device="cuda")
+    assert check(z, 4, bias, 4, 2, score, 3.1e38) == T
