@@ -1029,10 +1029,12 @@ fp8bs_status mxfp8_grouped_gemm_swiglu_quant(int64_t total_rows, int64_t I, int6
                     "mxfp8_grouped_gemm_swiglu_quant");
 }
 
-// A launch has fewer than 2^32 threads: 256 a row, or 64 up to 4096 columns.
+// A launch has fewer than 2^32 threads: 256 a row, or 64 up to 4096 columns; by columns
+// up to 1024 for each 64.
 static bool i8_rows_too_many(int64_t rows, int64_t cols) {
     return cols > INT32_MAX / 4 || rows >= (cols > 4096 ? 1ll << 24 : 1ll << 26);
 }
+static bool i8_cols_too_many(int64_t rows, int64_t cols) { return rows > 65535ll * 128 || cols > (1ll << 28) - 64; }
 // Codes of int8_quant and int8_silu_mul_quant: `len` of them per output row.
 static fp8bs_status i8_codes_args(int64_t len, const int8_t* q, int64_t ld_q, const float* s) {
     if (!s || (len > 0 && !q)) return fail(FP8BS_ERR_NULL, "q and s are required");
@@ -1047,7 +1049,7 @@ fp8bs_status int8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t l
     if (axis != FP8BS_AXIS_ROW && axis != FP8BS_AXIS_COL) return fail(FP8BS_ERR_UNSUPPORTED, "axis %d", (int)axis);
     if (rows < 0 || cols < 0) return fail(FP8BS_ERR_SHAPE, "rows=%lld cols=%lld", (long long)rows, (long long)cols);
     if (cols % 8) return fail(FP8BS_ERR_SHAPE, "cols %% 8 != 0 (cols=%lld)", (long long)cols);
-    if (axis == FP8BS_AXIS_ROW ? i8_rows_too_many(rows, cols) : rows > 65535ll * 128 || cols >= 1ll << 28)
+    if (axis == FP8BS_AXIS_ROW ? i8_rows_too_many(rows, cols) : i8_cols_too_many(rows, cols))
         return fail(FP8BS_ERR_SHAPE, "tensor too large");
     const bool by_row = axis == FP8BS_AXIS_ROW;
     if ((by_row ? rows : cols) == 0) return ok();

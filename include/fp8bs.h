@@ -906,7 +906,7 @@ fp8bs_status mxfp8_gemm(int64_t rows, int64_t N, int64_t K, int32_t G,
  * Requirements: rows, cols >= 0; cols % 8 == 0, ld_x >= cols, ld_x % 8 == 0, x
  * 16-byte aligned; ld_q >= the padded length, ld_q % 16 == 0, q 16-byte aligned;
  * s 4-byte aligned; AXIS_ROW: rows < 2^26, past 4096 columns 2^24; AXIS_COL:
- * rows <= 65535 * 128, cols < 2^28.
+ * rows <= 65535 * 128, cols <= 2^28 - 64.
  * ------------------------------------------------------------------------ */
 fp8bs_status int8_quant(const uint16_t* x, int64_t rows, int64_t cols, int64_t ld_x, fp8bs_axis axis,
                         int8_t* q, int64_t ld_q, float* s, hipStream_t stream);
