@@ -1288,7 +1288,7 @@ fp8bs_status int8_grouped_gemm(int64_t total_rows, int64_t N, int64_t K, int32_t
     if (b_stride_g < 0 || sb_stride_g < 0) return fail(FP8BS_ERR_STRIDE, "negative group stride");
     if (b_stride_g % 16) return fail(FP8BS_ERR_ALIGN, "b_stride_g %% 16 != 0");
     if (a_rows && (a_count < 1 || a_count > INT32_MAX)) return fail(FP8BS_ERR_SHAPE, "a_count must be >= 1 with a_rows");
-    if (((total_rows + 63) / 64 + G) * ((N + 63) / 64) >= (1ll << 31) - 8) return fail(FP8BS_ERR_SHAPE, "too many tiles");
+    if (!i8_grouped_fits(total_rows, N, G)) return fail(FP8BS_ERR_SHAPE, "too many tiles");
     if ((v = i8_operand_args(a_rows ? a_count : total_rows, K, a, lda, sa)) != FP8BS_OK) return v;
     if ((v = check_device()) != FP8BS_OK) return v;
     const I8GemmArgs g{total_rows, N, K, reinterpret_cast<const uint8_t*>(a), lda, sa,

@@ -720,12 +720,17 @@ __global__ void __launch_bounds__(256) k_i8_join(I8Args p, const i32x4* sums, in
     store4<OUT32>(p.c, m * p.ldc + n, f);
 }
 
+// Workgroups of a launch of tiles; grouped: as many as there can be tiles.
+template <int TM, int TN>
+int64_t tile_blocks(int64_t M, int64_t N, int64_t G) {
+    constexpr int BM = 64 * TM, BN = 64 * TN;
+    const int64_t ntn = (N + BN - 1) / BN;
+    return G == 0 ? (M + BM - 1) / BM * ntn : ((M / BM + std::min(G, M)) * ntn + 7) / 8 * 8;
+}
+
 template <int TM, int TN, bool GROUPED, bool GATHER>
 hipError_t tile(const I8Args& p, bool out32, hipStream_t st) {
-    constexpr int BM = 64 * TM, BN = 64 * TN;
-    const int64_t ntn = (p.N + BN - 1) / BN;
-    int64_t blocks = ((int64_t)p.M + BM - 1) / BM * ntn;
-    if (GROUPED) blocks = (((int64_t)p.M / BM + std::min<int64_t>(p.G, p.M)) * ntn + 7) / 8 * 8;   // at most this many tiles
+    const int64_t blocks = tile_blocks<TM, TN>(p.M, p.N, GROUPED ? p.G : 0);
     if (out32) hipLaunchKernelGGL((k_i8_tile<TM, TN, GROUPED, GATHER, OUT_FP32>), dim3((unsigned)blocks), dim3(256), 0, st, p);
     else hipLaunchKernelGGL((k_i8_tile<TM, TN, GROUPED, GATHER, OUT_BF16>), dim3((unsigned)blocks), dim3(256), 0, st, p);
     return hipGetLastError();
@@ -806,15 +811,32 @@ hipError_t launch_dense(const I8Args& p, bool out32, hipStream_t st) {
 //   tile 64 x 128     38   66   73   74   78   79  104  142  232
 //   tile 128 x 128    41   73   77   82   82   81   90  122  203
 //   tile 256 x 256    59  102  106  102  103  108  113  122  178
+enum class Grouped { STREAM, TILE64, TILE128, TILE256 };
+Grouped grouped_way(int64_t M, int64_t G) {
+    const int64_t rows = (M + G - 1) / G;
+    return rows <= 4 ? Grouped::STREAM : rows <= 32 ? Grouped::TILE64 : rows < 128 ? Grouped::TILE128 : Grouped::TILE256;
+}
 template <bool GATHER>
 hipError_t launch_grouped(const I8Args& p, bool out32, hipStream_t st) {
-    const int64_t rows = ((int64_t)p.M + p.G - 1) / p.G;
-    if (rows <= 4) return stream<1, 4, 4, true, GATHER>(p, out32, st);
-    if (rows <= 32) return tile<1, 2, true, GATHER>(p, out32, st);
-    return rows < 128 ? tile<2, 2, true, GATHER>(p, out32, st) : tile<4, 4, true, GATHER>(p, out32, st);
+    switch (grouped_way(p.M, p.G)) {
+        case Grouped::STREAM: return stream<1, 4, 4, true, GATHER>(p, out32, st);
+        case Grouped::TILE64: return tile<1, 2, true, GATHER>(p, out32, st);
+        case Grouped::TILE128: return tile<2, 2, true, GATHER>(p, out32, st);
+        default: return tile<4, 4, true, GATHER>(p, out32, st);
+    }
 }
 
 }  // namespace
+
+bool i8_grouped_fits(int64_t M, int64_t N, int64_t G) {
+    constexpr int64_t kMost = 1ll << 24;            // 256 threads each
+    switch (grouped_way(M, G)) {
+        case Grouped::STREAM: return (N + 15) / 16 < kMost;
+        case Grouped::TILE64: return tile_blocks<1, 2>(M, N, G) < kMost;
+        case Grouped::TILE128: return tile_blocks<2, 2>(M, N, G) < kMost;
+        default: return tile_blocks<4, 4>(M, N, G) < kMost;
+    }
+}
 
 size_t i8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K) {
     const int n = M == 0 || N == 0 ? 1 : split_count(M, N, K);

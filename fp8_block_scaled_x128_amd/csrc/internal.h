@@ -77,6 +77,8 @@ struct I8GemmArgs {
 // ws: i8_gemm_ws_bytes for the sums of K ranges (dense), or null: no ranges.
 hipError_t launch_i8_gemm(const I8GemmArgs& g, void* ws, hipStream_t st);
 size_t i8_gemm_ws_bytes(int64_t M, int64_t N, int64_t K);
+// Whether the grouped product's launch has fewer than 2^32 threads.
+bool i8_grouped_fits(int64_t M, int64_t N, int64_t G);
 // Two dense products with fp32 outputs; ws: the larger of their two.
 hipError_t launch_i8_gemm_pair(const I8GemmArgs& g, const I8GemmArgs& h, void* ws, hipStream_t st);
 // The product of one bf16 row that every workgroup quantizes for itself; g.a and g.sa

@@ -1002,7 +1002,8 @@ fp8bs_status int8_linear_backward_ws_size(int64_t T, int64_t O, int64_t I, size_
  *     sb + g * sb_stride_g.
  * There is no workspace.
  * Requirements: as int8_gemm; 1 <= G <= 65535; b_stride_g >= 0, % 16 == 0;
- * sb_stride_g >= 0.
+ * sb_stride_g >= 0; with more than four rows per group on average fewer than 2^24 tiles,
+ * (total_rows / 64 + min(G, total_rows)) * ceil(N / 128) at most.
  * ------------------------------------------------------------------------ */
 fp8bs_status int8_grouped_gemm(int64_t total_rows, int64_t N, int64_t K, int32_t G, const int32_t* offsets,
                                const int32_t* a_rows, int64_t a_count, const int8_t* a, int64_t lda, const float* sa,
