@@ -68,7 +68,7 @@ __device__ __forceinline__ void lds_write16(uint32_t addr, i32x4 v) {
 template <int AT>
 __device__ __forceinline__ void copy16(const void* base, uint32_t off, uint32_t dst) {
     asm volatile("s_add_u32 m0, %0, %c3\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, %2"
-                 :: "s"(dst), "v"(off), "s"(base), "n"(AT) : "memory", "scc");
+                 :: "s"(dst), "v"(off), "s"(base), "n"(AT) : "memory", "scc", "m0");
 }
 // The same where `go` (uniform) is not 0.  The branch is the assembly's own: a slice
 // stays one basic block.
@@ -76,7 +76,7 @@ template <int AT>
 __device__ __forceinline__ void copy16_if(uint32_t go, const void* base, uint32_t off, uint32_t dst) {
     asm volatile("s_cmp_eq_u32 %4, 0\n\ts_cbranch_scc1 .Lskip%=\n\ts_add_u32 m0, %0, %c3\n\ts_nop 0\n\t"
                  "global_load_lds_dwordx4 %1, %2\n.Lskip%=:"
-                 :: "s"(dst), "v"(off), "s"(base), "n"(AT), "s"(go) : "memory", "scc");
+                 :: "s"(dst), "v"(off), "s"(base), "n"(AT), "s"(go) : "memory", "scc", "m0");
 }
 // All but the last N1 + N2 copies of this wave have landed where `one` and `two` are
 // not 0, the last N1 with `one` alone, all without.
@@ -94,10 +94,13 @@ __device__ __forceinline__ i32x4 mfma(i32x4 a, i32x4 b, i32x4 c) {
 
 // A wave's 256 sums in accumulation registers of our own choice, a0 to a255, which
 // take one half of its registers whole.  The compiler is told that they are used
-// (ACC_IN_USE) and has none of its values there: left to allocate the sums itself it
-// copies them between the two halves of the register file, 388 copies beside 128
-// matrix instructions a slice.  Only the functions below touch them; the waits that
-// the compiler adds around matrix instructions are theirs.
+// (ACC_IN_USE), which reserves that half and keeps its values out of it at that point;
+// that it puts none there later, values or spills, is no promise of the clobber list but
+// of the 214 registers that the kernels need of the other half, and the build checks it
+// on the listing.  Left to allocate the sums itself it copies them between the two halves
+// of the register file, 388 copies beside 128 matrix instructions in two slices.  Only
+// the functions below touch them; the waits that the compiler adds around matrix
+// instructions are theirs.
 #define FP8BS_ACC_IN_USE() asm volatile("" ::: \
         "a0", "a1", "a2", "a3", "a4", "a5", "a6", "a7", "a8", "a9", "a10", "a11", "a12", "a13", "a14", "a15", \
         "a16", "a17", "a18", "a19", "a20", "a21", "a22", "a23", "a24", "a25", "a26", "a27", "a28", "a29", "a30", "a31", \
