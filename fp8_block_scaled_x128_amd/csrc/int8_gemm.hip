@@ -19,10 +19,15 @@
 // m.  With TM = TN = 4 a wave holds 256 sums, 128 x 128 outputs: per slice a compute
 // unit reads 128 KB of fragments and writes 64 KB of copies beside 2048 cycles of
 // matrix work.  One such workgroup fills a unit's LDS, so nothing else hides a wave's
-// latencies: it works a slice ahead of itself.  4096 x 2560 by 9728: 122 us (608 tiles
-// are 2.4 rounds of 256 units), 1.67 POPS; 131072 expert rows of 2048 by 1536 500,
-// 1.65.  TM = TN = 2 puts two workgroups on a unit and takes products with fewer
-// tiles; TM = 1, TN = 2 the K ranges and small groups.
+// latencies: it works a slice ahead of itself.  4096 x 2560 by 9728: 117 to 136 us by
+// the card at hand, 1.5 to 1.7 POPS; 131072 expert rows of 2048 by 1536 495 to 531, 1.55
+// to 1.67.  Counters of the former (608 tiles, 2.4 rounds of 256 units): 250000 cycles,
+// on random codes at 2.1 GHz and on zeros at 2.5 (100 us), so power costs a sixth of the
+// clock and nothing else; a tile takes 74000 of them, of which 41000 are matrix work and
+// 30000 waits, and LDS is in use for 51000 of the 250000.  What bounds it are the waits of
+// the one workgroup that a unit holds (a tile's first copies, its barriers, its epilogue)
+// and the third round, not LDS bandwidth.  TM = TN = 2 puts two workgroups on a unit and
+// takes products with fewer tiles; TM = 1, TN = 2 the K ranges and small groups.
 // Few rows are bound by the weights' way from memory, see below.
 #include <algorithm>
 #include <utility>
@@ -741,9 +746,12 @@ hipError_t tile(const I8Args& p, bool out32, hipStream_t st) {
 
 // Products of so little work (M N K) that tiles of 128 x 128 leave most compute units
 // idle, or wait for each slice: 205 x 1008 by 1512 6.0 us in the waves' K ranges and 8.6
-// in tiles, 128 x 2048 by 2560 10.9 and 12.2, 32 x 4096 by 4096 8.4 and 11.7 (K split);
-// past it 205 x 2048 by 2560 14 and 12.2, 32 x 2560 by 9728 16.2 and 13.7.  Eight waves
-// need a run each.
+// in tiles, 32 x 4096 by 4096 8.4 and 11.7 (K split).  Just past the limit both ways win
+// somewhere: ranges at 128 x 2048 by 2560 (10.7 us, K split 11.2, tiles 12.0) and 64 x
+// 2560 by 4096 (8.4, 11.2, 14.1), tiles at 256 x 1024 by 2560 (8.2, ranges 11.0), 64 x
+// 1024 by 10240 (8.3, 9.6) and 205 x 1280 by 2560 (9.2, 11.2), K split at 32 x 8192 by
+// 2560 (12.2, 13.2) and 17 x 4096 by 9728 (14.4, 17.2); further on the ranges lose: 205 x
+// 2048 by 2560 14 and 12.2, 32 x 2560 by 9728 16.0 and 12.9.  Eight waves need a run each.
 bool little(int64_t M, int64_t N, int64_t K) { return K > 7 * kRun && M * N * K <= 640000000; }
 
 // K ranges for products with few tiles and a long K: tiles of 64 x 128, about one for

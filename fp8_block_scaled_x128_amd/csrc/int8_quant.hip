@@ -7,8 +7,10 @@
 // Bound by HBM: 2 bytes read and 1 written per value, once for rows; columns
 // need their maximum over all rows before the first code, so a long tensor is read
 // twice (the second time mostly from the last-level cache).  Rows: 4096 x 2560 9 us,
-// 4096 x 9728 21 (5.7 TB/s); columns of 4096 x 9728 26 for the maxima, 23 for the codes,
-// of 205 x 1512 7.
+// 4096 x 9728 21 (5.7 TB/s); columns of 4096 x 9728 44 in three launches (26 and 23 in a
+// trace; two reads and the writes at 5.5 TB/s are 36), of 9728 x 2560 30, of 4096 x 2560
+// 14.5, of 205 x 1512 5.5, one launch.  SiLU*mul codes: 131072 rows of 768 120 us (4.2
+// TB/s), 4096 of 9728 44 (4.6), 256 of 768 3.2.
 #include "int8_common.h"
 #include "internal.h"
 #include "reduce.h"

@@ -10,18 +10,21 @@
 //
 // Which experts are taken is decided as in 64 bits.  Without a bias the logits
 // themselves are compared, which is exact.  Else values are compared in fp32, and a
-// wave in which two of them (or two groups) come closer than the fp32 error (about
-// one token in 700 over 256 experts) repeats its selection in 64 bits: two
-// roundings would otherwise decide which expert gets the token, and with it every
-// row behind.
+// token of which two (or two groups) come closer than the fp32 error is selected again in
+// 64 bits by its whole wave: two roundings would otherwise decide which expert gets the
+// token, and with it every row behind.  That is about one token in 700 over 256 experts
+// where values are spread (fp32 logits, a bias that has moved); equal values are as close
+// as any, so bf16 logits under a bias of zeros, as at the start of training, repeat a
+// third of the tokens, and equal logits all: 16384 x 256 in 59 and 68 us, not 36 (45 with
+// equal logits and no bias, where only the groups' sums tie).
 //
 // The lanes of a token are dealt to the groups, a power of two each, and hold
 // consecutive experts, so that a group's maxima meet in a few lane steps.  The rest
 // is the plain router's: histograms, rows and losses come from the same code.
 // Bound by vector issue: a token's `k` rounds of maxima over its lanes are dependent.
 // 16384 tokens of 256 experts (16.8 MB of logits, 3 us): selection 27 us, rows 10;
-// 32 tokens of 128 in one launch 9.0; the gradient, one pass over logits and result,
-// 12 us at 16384 x 256 (2.7 TB/s) and 3.7 at 1000 x 60.
+// 32 tokens of 128 in one launch 9.0; the gradient, one pass over logits and result, a
+// load or a store per value, 12 us at 16384 x 256 (2.7 TB/s) and 3.7 at 1000 x 60.
 #include "route_common.h"
 
 namespace fp8bs {
@@ -628,10 +631,12 @@ hipError_t launch_moe_route_grouped(const GateArgs& g, void* wsp, hipStream_t st
         if (per % 4 == 0) n.w = (n.w + 3) / 4 * 4;
         return n;
     };
-    // sixteen lanes per token while they hold it in 16 values each; 32 would spill
-    // registers (16384 tokens of 512 experts 86 us, with 64 lanes 68).  64 lanes hold
-    // every token in 32 (1024 experts in 2^k + 1 groups), and a token that is selected
-    // again has them anyway.
+    // sixteen lanes per token while they hold it in 16 values each, without scratch.
+    // Beyond that every kernel spills registers: 64 lanes of 8 values 200 bytes a lane,
+    // of 16 600, of 32 1450, and sixteen lanes of 32 more than they (16384 tokens of 512
+    // experts 86 us, with 64 lanes 68; of 384 66, of 1024 165, where the plain router takes
+    // 33, 33 and 59).  64 lanes hold every token in 32 (1024 experts in 2^k + 1 groups),
+    // and a token that is selected again has them anyway.
     const GateLanes nw = deal(64);
     const bool wide = lanes > 16 || deal(16).w > 16;
     const GateLanes n = wide ? nw : deal(16);

@@ -601,9 +601,12 @@ fp8bs_status fp8_moe_route_backward(const void* logits, int64_t T, int32_t E, in
  *   loss[1]  = mean over routed tokens of total^2 (softmax), 0 (sigmoid)
  *
  * v is compared as in 64 bits: values that differ by more than a few roundings of
- * binary64 are taken in their true order.  An expert whose logit or v is -inf is
- * not taken; NaN counts as the largest (a group's sum with it as infinity) and
- * makes its token's weights, total and the losses NaN.  A slot that takes no expert has expert -1, weight 0 and row -1.
+ * binary64 are taken in their true order.  Without a bias the experts of a group, and
+ * groups by their largest value, are ordered by the logits, of which the scores are an
+ * increasing function.  An expert whose logit or v is -inf is not taken; NaN counts as
+ * the largest (a group whose value is NaN as infinity) and makes its token's weights,
+ * total and the losses NaN.  A slot that takes no expert has expert -1, weight 0 and
+ * row -1.
  * Everything else (rows, counts, offsets, masks, workspace) is as in
  * fp8_moe_route; the workspace is that of fp8_moe_route_ws_size.
  *
