@@ -22,17 +22,17 @@ def test_most_columns():
 
 
 def test_most_tiles_of_groups():
-    """65535 groups of five rows in tiles of 64 x 128, 70654 x 237 of them: one expert's
-    weights for all groups, every 4999th row against the exact product."""
-    G, N, K = 65535, 237 * 128, 16
+    """30 groups of five rows in tiles of 64 x 128, at most 32 x 524287 of them: the first
+    and last columns and every 100003rd against the exact product, and no tile left out."""
+    G, N, K = 30, 524287 * 128, 16
     M = 5 * G
     g = torch.Generator("cuda").manual_seed(2)
     a = torch.randint(-127, 128, (M, K), generator=g, device="cuda", dtype=torch.int8)
     b = torch.randint(-127, 128, (N, K), generator=g, device="cuda", dtype=torch.int8)
     sa, sb = torch.rand(M, generator=g, device="cuda"), torch.rand(N, generator=g, device="cuda")
     offsets = torch.arange(G + 1, device="cuda", dtype=torch.int32) * 5
-    c = torch.full((M, N), 3.0, dtype=torch.bfloat16, device="cuda")
+    c = torch.full((M, N), torch.nan, dtype=torch.bfloat16, device="cuda")
     ops.int8_grouped_gemm(M, N, K, G, offsets, None, 0, a, K, sa, b, K, 0, sb, 0, c, N, ops.OUT_BF16)
-    at = torch.cat([torch.arange(0, M, 4999, device="cuda"), torch.arange(M - 70, M, device="cuda")])
-    R.check_product(c[at], R.product(a[at].cpu(), sa[at].cpu(), b.cpu(), sb.cpu()))
-    assert not (c[:, ::61] == 3.0).all(dim=1).any()         # no row left out
+    at = torch.cat([torch.arange(300), torch.arange(0, N, 100003), torch.arange(N - 300, N)]).cuda()
+    R.check_product(c[:, at], R.product(a, sa, b[at], sb[at]))
+    assert not torch.isnan(c[::5, ::64]).any() and not torch.isnan(c[4::5, 63::64]).any()
